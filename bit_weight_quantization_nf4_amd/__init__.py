@@ -150,6 +150,16 @@ def lib() -> ctypes.CDLL:
     return h
 
 
+def _lib_functions(signatures):
+    """The loaded library with further typed entry points (another header's)."""
+    h = lib()
+    for name, res, args in signatures:
+        fn = getattr(h, name)
+        fn.restype = res
+        fn.argtypes = args
+    return h
+
+
 def exported_names() -> list[str]:
     return [s[0] for s in _SIGNATURES]
 
@@ -507,7 +517,11 @@ def linear(x: torch.Tensor, qs: QuantState, bias: torch.Tensor | None = None,
     return out
 
 
+from .kv import (  # noqa: E402  (needs the helpers above)
+    KVCache, kv_attention, kv_attention_workspace_bytes, kv_read, kv_write)
+
 __all__ = [
+    "KVCache", "kv_write", "kv_read", "kv_attention", "kv_attention_workspace_bytes",
     "QuantState", "QWeightDesc", "Nf4Error", "lib", "exported_names", "codebook", "packed_bytes",
     "num_blocks", "quantize", "quantize_grouped", "double_quant", "dequantize",
     "dequantize_grouped", "gemv", "gemv_grouped", "gemm", "linear", "workspace_bytes",

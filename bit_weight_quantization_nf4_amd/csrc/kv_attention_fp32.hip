@@ -1,0 +1,10 @@
+// kv_attention_fp32.hip -- the attention kernels for fp32 rows.
+#include "kv_attention_kernel.h"
+
+namespace nf4 {
+namespace kvattn {
+
+template hipError_t launch_shape<kFP32>(const AttnArgs &, const Plan &, int, int, hipStream_t);
+
+}  // namespace kvattn
+}  // namespace nf4

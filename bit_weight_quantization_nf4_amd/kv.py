@@ -1,0 +1,258 @@
+"""Python binding of the 4-bit key/value cache (``include/nf4_kv.h``): keys and
+values quantized as they are written into a paged cache, read back, and attended
+to in their 4 bits. Argument marshalling only, as in the package's other calls.
+
+The sequences of a call are given by ``block_table`` (int32 [batch, pages of a
+sequence], -1 for none), ``kv_lens`` (int32 [batch], positions cached, the ones
+written in the same call included) and ``row_offsets`` (int32 [batch + 1], or
+None where every sequence has equally many rows). Rows row_offsets[b] ...
+row_offsets[b + 1] - 1 of the row tensors are sequence b's last positions.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _DT, _QT, _check, _lib_functions
+
+_P = ctypes.c_void_p
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
+
+
+class KVCacheDesc(ctypes.Structure):
+    """ctypes mirror of ``nf4_kv_cache``."""
+
+    _fields_ = [("k_packed", _P), ("k_absmax", _P), ("v_packed", _P), ("v_absmax", _P),
+                ("num_pages", _I64), ("packed_page_stride", _I64), ("absmax_page_stride", _I64),
+                ("page_size", _I32), ("num_kv_heads", _I32), ("head_dim", _I32),
+                ("blocksize", _I32), ("quant_type", _I32)]
+
+
+class KVRowsDesc(ctypes.Structure):
+    """ctypes mirror of ``nf4_kv_rows``."""
+
+    _fields_ = [("block_table", _P), ("kv_lens", _P), ("row_offsets", _P),
+                ("table_stride", _I64), ("table_cols", _I32), ("batch", _I32),
+                ("total_rows", _I32)]
+
+
+_CACHE, _ROWS = ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVRowsDesc)
+# (name, restype, argtypes) of every entry point of nf4_kv.h
+_SIGNATURES = [
+    ("nf4_kv_write", _I32, [_CACHE, _ROWS, _P, _P, _I64, _I64, _I32, _P, _P, _P]),
+    ("nf4_kv_read", _I32, [_CACHE, _ROWS, _I32, _P, _P, _I64, _I64, _P]),
+    ("nf4_kv_attention_workspace_bytes", _I64, [_I32] * 6),
+    ("nf4_kv_attention", _I32,
+     [_CACHE, _ROWS, _P, _I64, _I64, _I32, _I32, ctypes.c_float, _I32, _I32, _I32, _I32, _P, _I64,
+      _I64, _P, _I64, _P]),
+]
+
+_fns = None
+
+
+def _lib():
+    global _fns
+    if _fns is None:
+        _fns = _lib_functions(_SIGNATURES)
+    return _fns
+
+
+def kv_exported_names() -> list[str]:
+    return [s[0] for s in _SIGNATURES]
+
+
+class KVCache:
+    """A paged 4-bit key/value cache: uint8 ``k_packed`` and ``v_packed`` [pages,
+    kv heads, page_size, head_dim / 2] and fp32 ``k_absmax`` and ``v_absmax``
+    [pages, kv heads, page_size, head_dim / blocksize] on the GPU, contiguous
+    within a page (pages may lie further apart, keys' and values' equally far).
+    The layout of the codes within a head of a page is nf4_kv.h's."""
+
+    def __init__(self, k_packed: torch.Tensor, k_absmax: torch.Tensor, v_packed: torch.Tensor,
+                 v_absmax: torch.Tensor, blocksize: int = 64, quant_type: str = "nf4"):
+        if k_packed.dim() != 4:
+            raise ValueError("KVCache expects codes [pages, kv heads, page_size, head_dim / 2]")
+        pages, heads, page_size, half = k_packed.shape
+        nb = 2 * half // blocksize if blocksize > 0 else 0
+        inner = (page_size * half, half, 1)
+        sinner = (page_size * nb, nb, 1)
+        for t in (k_packed, v_packed):
+            if t.dtype != torch.uint8 or t.shape != k_packed.shape or (
+                    pages and t.stride()[1:] != inner) or t.stride(0) != k_packed.stride(0):
+                raise ValueError("KVCache expects uint8 codes of one shape, contiguous in a page")
+        for t in (k_absmax, v_absmax):
+            if t.dtype != torch.float32 or t.shape != (pages, heads, page_size, nb) or (
+                    pages and t.stride()[1:] != sinner) or t.stride(0) != k_absmax.stride(0):
+                raise ValueError("KVCache expects fp32 scales [pages, kv heads, page_size, "
+                                 "head_dim / blocksize], contiguous in a page")
+        dev = k_packed.device
+        if dev.type != "cuda" or not (k_absmax.device == v_packed.device == v_absmax.device == dev):
+            raise TypeError("KVCache expects four tensors on one GPU")
+        self.k_packed, self.k_absmax = k_packed, k_absmax
+        self.v_packed, self.v_absmax = v_packed, v_absmax
+        self.blocksize, self.quant_type = blocksize, quant_type
+        self.num_pages, self.num_kv_heads, self.page_size = pages, heads, page_size
+        self.head_dim = 2 * half
+        self.device = dev
+        self.desc = KVCacheDesc(k_packed.data_ptr(), k_absmax.data_ptr(), v_packed.data_ptr(),
+                                v_absmax.data_ptr(), pages, k_packed.stride(0), k_absmax.stride(0),
+                                page_size, heads, 2 * half, blocksize, _QT[quant_type])
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+              blocksize: int = 64, quant_type: str = "nf4", device="cuda") -> "KVCache":
+        """A cache of uninitialised pages."""
+        shape = (num_pages, num_kv_heads, page_size)
+        t = [torch.empty(*shape, head_dim // 2, dtype=torch.uint8, device=device)
+             if i % 2 == 0 else
+             torch.empty(*shape, head_dim // blocksize, dtype=torch.float32, device=device)
+             for i in range(4)]
+        return cls(*t, blocksize, quant_type)
+
+    def nbytes(self) -> int:
+        return 2 * (self.k_packed.numel() + 4 * self.k_absmax.numel())
+
+
+def _rows(cache: KVCache, total: int, block_table, kv_lens, row_offsets, what: str) -> KVRowsDesc:
+    if block_table.dtype != torch.int32 or kv_lens.dtype != torch.int32 or \
+            block_table.dim() != 2 or kv_lens.dim() != 1:
+        raise TypeError(f"{what} expects int32 block_table [batch, pages] and kv_lens [batch]")
+    batch, cols = block_table.shape
+    if kv_lens.shape[0] != batch or not kv_lens.is_contiguous() or \
+            (cols > 1 and block_table.stride(1) != 1) or \
+            (batch > 1 and block_table.stride(0) < cols):
+        raise ValueError(f"{what}: block_table needs unit column stride, kv_lens [batch]")
+    if block_table.device != cache.device or kv_lens.device != cache.device:
+        raise TypeError(f"{what} expects every tensor on the cache's GPU")
+    off = None
+    if row_offsets is not None:
+        if row_offsets.dtype != torch.int32 or row_offsets.shape != (batch + 1,) or \
+                not row_offsets.is_contiguous() or row_offsets.device != cache.device:
+            raise ValueError(f"{what} expects int32 row_offsets [batch + 1] on the cache's GPU")
+        off = row_offsets.data_ptr()
+    return KVRowsDesc(block_table.data_ptr(), kv_lens.data_ptr(), off,
+                      block_table.stride(0) if batch > 1 else cols, cols, batch, total)
+
+
+def _strided(t: torch.Tensor) -> bool:
+    """Whether the ABI takes [rows, heads, head_dim] as it is."""
+    es, (r, h, e) = t.element_size(), t.stride()
+    d = t.shape[2]
+    return (e == 1 and r >= d and h >= d and r * es % 16 == 0 and h * es % 16 == 0
+            and t.data_ptr() % 16 == 0)
+
+
+def _check_rows(t: torch.Tensor, cache: KVCache, what: str) -> None:
+    if t.dtype not in _DT or t.device != cache.device:
+        raise TypeError(f"{what} expects bf16 / fp16 / fp32 rows on the cache's GPU")
+    if t.dim() != 3 or t.shape[2] != cache.head_dim:
+        raise ValueError(f"{what} expects rows [rows, heads, head_dim]")
+
+
+def _aligned_copy(t: torch.Tensor) -> torch.Tensor:
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _call(cache: KVCache, fn, name: str, *args) -> None:
+    """fn(*args, stream) on the cache's device and that device's current stream."""
+    if cache.device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream), name)
+    else:
+        with torch.cuda.device(cache.device):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream), name)
+
+
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+             kv_lens: torch.Tensor, row_offsets: torch.Tensor | None = None, values: bool = False):
+    """nf4_kv_write: quantizes k and v [rows, kv heads, head_dim] into the cache.
+    With ``values`` returns (k, v) as the cache now holds them, rounded to their
+    dtype, for a computation that is to see what later reads will see."""
+    for t in (k, v):
+        _check_rows(t, cache, "kv_write")
+    if k.dtype != v.dtype or k.shape != v.shape or k.shape[1] != cache.num_kv_heads:
+        raise ValueError("kv_write expects k and v [rows, kv heads, head_dim] of one dtype")
+    if not (k.stride() == v.stride() and _strided(k) and _strided(v)):
+        k, v = _aligned_copy(k), _aligned_copy(v)
+    rows = _rows(cache, k.shape[0], block_table, kv_lens, row_offsets, "kv_write")
+    kq = torch.empty(k.shape, dtype=k.dtype, device=k.device) if values else None
+    vq = torch.empty(k.shape, dtype=k.dtype, device=k.device) if values else None
+    _call(cache, _lib().nf4_kv_write, "nf4_kv_write", cache.desc, rows, k.data_ptr(), v.data_ptr(),
+          k.stride(0), k.stride(1), _DT[k.dtype], kq.data_ptr() if values else None,
+          vq.data_ptr() if values else None)
+    return (kq, vq) if values else None
+
+
+def kv_read(cache: KVCache, rows: int, block_table: torch.Tensor, kv_lens: torch.Tensor,
+            row_offsets: torch.Tensor | None = None, dtype=torch.bfloat16, out=None):
+    """nf4_kv_read: the last positions of each sequence, ``rows`` in all, as (k, v)
+    [rows, kv heads, head_dim] (or into the pair ``out``). Rows behind the last
+    offset are left as they are: unspecified without ``out``."""
+    if out is None:
+        shape = (rows, cache.num_kv_heads, cache.head_dim)
+        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    k, v = out
+    for t in out:
+        _check_rows(t, cache, "kv_read")
+        if t.shape != (rows, cache.num_kv_heads, cache.head_dim) or t.dtype != k.dtype or \
+                t.stride() != k.stride() or not _strided(t):
+            raise ValueError("kv_read: out must be two [rows, kv heads, head_dim] tensors of one "
+                             "dtype and layout, with 16-byte aligned heads")
+    desc = _rows(cache, rows, block_table, kv_lens, row_offsets, "kv_read")
+    _call(cache, _lib().nf4_kv_read, "nf4_kv_read", cache.desc, desc, _DT[k.dtype], k.data_ptr(),
+          v.data_ptr(), k.stride(0), k.stride(1))
+    return k, v
+
+
+def kv_attention_workspace_bytes(batch: int, max_rows: int, max_len: int, num_heads: int,
+                                 num_kv_heads: int, head_dim: int) -> int:
+    """nf4_kv_attention_workspace_bytes on the current device."""
+    return int(_lib().nf4_kv_attention_workspace_bytes(batch, max_rows, max_len, num_heads,
+                                                       num_kv_heads, head_dim))
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                 row_offsets: torch.Tensor | None = None, max_rows: int = 0, max_len: int = 0,
+                 scale: float | None = None, causal: bool = True, window: int = 0,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """nf4_kv_attention (with a workspace this call allocates): attention of q
+    [rows, heads, head_dim] to the cache, in q's dtype. ``max_rows`` is the most
+    rows of a sequence where row_offsets is given (0: that many as there are
+    rows), ``max_len`` about the longest of kv_lens (0: what the table can hold);
+    both only size the launch, but rows of a sequence past max_rows stay
+    unwritten. ``scale`` defaults to head_dim ** -0.5. Rows behind the last
+    offset are left as they are: unspecified without ``out``."""
+    _check_rows(q, cache, "kv_attention")
+    total, heads, d = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _check_rows(out, cache, "kv_attention")
+        if out.shape != q.shape or out.dtype != q.dtype or not _strided(out):
+            raise ValueError("kv_attention: out must be like q, with 16-byte aligned heads")
+    if not _strided(q):
+        q = _aligned_copy(q)
+    rows = _rows(cache, total, block_table, kv_lens, row_offsets, "kv_attention")
+    if heads % cache.num_kv_heads:
+        raise ValueError("kv_attention expects a multiple of the cache's heads")
+    if row_offsets is None:
+        max_rows = total // rows.batch if rows.batch else 0
+    elif max_rows <= 0:
+        max_rows = total
+    if max_len <= 0:
+        max_len = min(rows.table_cols * cache.page_size, 0x7fff0000)
+    args = (cache.desc, rows, q.data_ptr(), q.stride(0), q.stride(1), heads, _DT[q.dtype],
+            d ** -0.5 if scale is None else scale, int(causal), window, max_rows, max_len,
+            out.data_ptr(), out.stride(0), out.stride(1))
+    with torch.cuda.device(cache.device):  # the split goes by that device's CUs
+        need = kv_attention_workspace_bytes(rows.batch, max_rows, max_len, heads,
+                                            cache.num_kv_heads, d)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        _call(cache, _lib().nf4_kv_attention, "nf4_kv_attention", *args,
+              None if ws is None else ws.data_ptr(), max(need, 0))
+    return out
+
+
+__all__ = ["KVCache", "KVCacheDesc", "KVRowsDesc", "kv_write", "kv_read", "kv_attention",
+           "kv_attention_workspace_bytes", "kv_exported_names"]
