@@ -41,10 +41,13 @@ nf4_status check_call(const nf4_kv_cache *c, const nf4_kv_rows *r, int32_t dtype
     return NF4_ERR_INVALID_ARGUMENT;
   if (!valid_head_dim(c->head_dim) || c->blocksize > 128 || c->head_dim % c->blocksize != 0)
     return NF4_ERR_UNSUPPORTED;
-  // a head's part of a page is addressed with 31-bit byte offsets
+  // a head's part of a page is addressed with 31-bit byte offsets, and pages with
+  // 32-bit strides in 16 bytes and in floats
   if (c->page_size % 16 != 0 || (int64_t)c->page_size * (c->head_dim / 2) >= ((int64_t)1 << 31))
     return NF4_ERR_UNSUPPORTED;
   if (c->num_pages > INT32_MAX || c->num_kv_heads > 65535 || r->batch > 65535)
+    return NF4_ERR_UNSUPPORTED;
+  if (c->packed_page_stride >= ((int64_t)1 << 36) || c->absmax_page_stride >= ((int64_t)1 << 32))
     return NF4_ERR_UNSUPPORTED;
   const int64_t positions = (int64_t)c->num_kv_heads * c->page_size;
   if (c->num_pages > 0) {
@@ -165,13 +168,14 @@ nf4_status nf4_kv_read(const nf4_kv_cache *cache, const nf4_kv_rows *rows, int32
 
 int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_t max_len,
                                          int32_t num_heads, int32_t num_kv_heads,
-                                         int32_t head_dim) {
+                                         int32_t head_dim, int32_t dtype, int32_t window) {
   if (batch < 0 || max_rows < 0 || max_len < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-      num_heads % num_kv_heads != 0 || !valid_head_dim(head_dim))
+      num_heads % num_kv_heads != 0 || !valid_head_dim(head_dim) || !valid_dtype(dtype) ||
+      window < 0)
     return -1;
   if (batch == 0 || max_rows == 0) return 0;
-  if (!kv_attention_fits(batch, max_rows, max_len, num_heads, num_kv_heads, head_dim)) return -1;
-  return kv_attention_bytes(batch, max_rows, max_len, num_heads, num_kv_heads, head_dim);
+  const KvAttentionSizes z{batch, max_rows, max_len, num_heads, num_kv_heads, head_dim, dtype, window};
+  return kv_attention_fits(z) ? kv_attention_bytes(z) : -1;
 }
 
 nf4_status nf4_kv_attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, const void *q,
@@ -202,21 +206,23 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, 
   c.q_head = q_head_stride;
   c.out_row = out_row_stride;
   c.out_head = out_head_stride;
-  c.group = num_heads / kv.kv_heads;
-  c.max_rows = kv.offsets == nullptr ? kv.uniform : (max_rows > 0 ? max_rows : kv.total_rows);
-  c.max_len = max_len > 0 ? max_len : kv.capacity;
   c.scale = scale;
   c.causal = causal != 0;
-  c.window = window;
   c.workspace = workspace;
-  if (!kv_attention_fits(kv.batch, c.max_rows, c.max_len, num_heads, kv.kv_heads, sh.head_dim))
-    return NF4_ERR_UNSUPPORTED;
+  const KvAttentionSizes z{
+      kv.batch, kv.offsets == nullptr ? kv.uniform : (max_rows > 0 ? max_rows : kv.total_rows),
+      max_len > 0 ? max_len : kv.capacity, num_heads, kv.kv_heads, sh.head_dim, dtype, window};
+  if (!kv_attention_fits(z)) return NF4_ERR_UNSUPPORTED;
   st = nf4_device_check();
   if (st != NF4_OK) return st;
-  const int64_t need = kv_attention_bytes(kv.batch, c.max_rows, c.max_len, num_heads, kv.kv_heads,
-                                          sh.head_dim);
+  const int64_t need = kv_attention_bytes(z);
   if (workspace_bytes < need) return NF4_ERR_SCRATCH;
-  return from_hip(launch_kv_attention(kv, sh, c, reinterpret_cast<hipStream_t>(stream)));
+  if (log_on())
+    log_msg("kv_attention rows=%d batch=%d heads=%d/%d head_dim=%d bs=%d dtype=%d max_rows=%d "
+            "max_len=%d: kv_attention_kernel%s", kv.total_rows, kv.batch, num_heads, kv.kv_heads,
+            sh.head_dim, sh.blocksize, dtype, z.max_rows, z.max_len,
+            need > 0 ? ", positions split, joined by kv_attention_join_kernel" : "");
+  return from_hip(launch_kv_attention(kv, sh, z, c, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

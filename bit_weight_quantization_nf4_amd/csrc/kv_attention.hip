@@ -8,90 +8,135 @@ using namespace kvattn;
 
 namespace {
 
-// Joins the splits of a row: out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),
-// in split order within each of the workgroup's waves, then in wave order.
+// Joins the ranges of a row: out = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), in
+// range order within a wave. ROWS_APART: each of the workgroup's waves has a row of
+// its own, else they share one and add up in wave order. Rows that see nothing
+// become zeros.
 constexpr int kJoinWaves = 4;
 
-template <int D, int DT>
-__global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(AttnArgs args, int rows) {
-  constexpr int C = D / 64 > 0 ? D / 64 : 1;  // elements of a lane, at lane + 64 c
-  __shared__ float acc[kJoinWaves][D];
-  __shared__ float sums[kJoinWaves];
+template <int D, int DT, bool ROWS_APART>
+__global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(AttnArgs, int align) {
+  constexpr int C = (D + 127) / 128;  // element pairs of a lane, at 2 lane + 128 c
+  constexpr int SW = ROWS_APART ? 1 : kJoinWaves;  // waves of a row
+  __shared__ float acc[SW][D];
+  __shared__ float sums[SW];
+  fetch_args();
+  KernelArgs &args = *kernel_args();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pair = (int)blockIdx.x, h = (int)blockIdx.y, seq = (int)blockIdx.z;
-  const int rb = pair / rows, row = pair - rb * rows;
-  const Block blk = block_of(args, seq, rb, rows);
+  const int sw = ROWS_APART ? 0 : wave;
+  const int pair = ROWS_APART ? (int)blockIdx.x * kJoinWaves + wave : (int)blockIdx.x;
+  const int h = (int)blockIdx.y, seq = (int)blockIdx.z;
+  const int wb = args.wg_blocks == 1 ? 0 : pair / args.wg_rows, row = pair - wb * args.wg_rows;
+  const Block blk = block_of(args, sequence_of(args, seq), wb * args.wg_rows, args.wg_rows);
   if (pair >= blk.pairs) return;
-  const int chunk = chunk_of(blk, args.splits);
-  const int used = chunk > 0 ? (blk.hi - blk.lo + chunk - 1) / chunk : 0;
-  const int64_t item = ((int64_t)seq * args.kv.kv_heads + h) * args.row_blocks + rb;
-  const int64_t base = item * args.splits * args.part_rows + row;
+  const int range = range_of(blk, args.splits, align);
+  const int pieces = range > 0 ? (blk.hi - blk.lo + range - 1) / range : 0;
+  const int64_t base = item_of(args, seq, h, wb) * args.splits * args.part_rows + row;
+  auto part_row = [&](int i) { return base + (int64_t)i * args.part_rows; };
 
   float top = -__builtin_inff();
-  for (int s = lane; s < used; s += 64)
-    top = fmaxf(top, args.stats[base + (int64_t)s * args.part_rows].x);
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  for (int i = lane; i < pieces; i += 64) top = fmaxf(top, args.stats[part_row(i)].x);
+  top = max_over_groups(row16_max(top));
   const float use = top == -__builtin_inff() ? 0.0f : top;
 
-  float sum = 0.0f, o[C + 1];
+  float sum = 0.0f;
+  f32x2 o[C];
 #pragma unroll
-  for (int c = 0; c <= C; ++c) o[c] = 0.0f;
-  for (int s = wave; s < used; s += kJoinWaves) {
-    const int64_t at = base + (int64_t)s * args.part_rows;
+  for (int c = 0; c < C; ++c) o[c] = f32x2{0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = sw; i < pieces; i += SW) {
+    const int64_t at = part_row(i);
     const float2 st = args.stats[at];
     const float f = __builtin_amdgcn_exp2f(st.x - use);
     sum = __builtin_fmaf(st.y, f, sum);
     const float *p = args.part + at * D;
 #pragma unroll
-    for (int c = 0; c < (D + 63) / 64; ++c)
-      if (lane + 64 * c < D) o[c] = __builtin_fmaf(p[lane + 64 * c], f, o[c]);
+    for (int c = 0; c < C; ++c) {
+      const int e = 2 * lane + 128 * c;
+      if (e < D) {
+        const f32x2 v = *reinterpret_cast<const f32x2 *>(p + e);
+        o[c].x = __builtin_fmaf(v.x, f, o[c].x);
+        o[c].y = __builtin_fmaf(v.y, f, o[c].y);
+      }
+    }
   }
+  if constexpr (!ROWS_APART) {
 #pragma unroll
-  for (int c = 0; c < (D + 63) / 64; ++c)
-    if (lane + 64 * c < D) acc[wave][lane + 64 * c] = o[c];
-  if (lane == 0) sums[wave] = sum;
-  __syncthreads();
+    for (int c = 0; c < C; ++c) {
+      const int e = 2 * lane + 128 * c;
+      if (e < D) *reinterpret_cast<f32x2 *>(&acc[sw][e]) = o[c];
+    }
+    if (lane == 0) sums[sw] = sum;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int i = 1; i < SW; ++i) {
+      sum += sums[i];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int e = 2 * lane + 128 * c;
+        if (e < D) o[c] += *reinterpret_cast<const f32x2 *>(&acc[i][e]);
+      }
+    }
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   const int token = pair / args.group;
   const int64_t at = (int64_t)(blk.first + token) * args.out_row +
                      (int64_t)(h * args.group + pair - token * args.group) * args.out_head;
-  float l = sums[0];
 #pragma unroll
-  for (int i = 1; i < kJoinWaves; ++i) l += sums[i];
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  for (int e = threadIdx.x; e < D; e += 64 * kJoinWaves) {
-    float v = acc[0][e];
-#pragma unroll
-    for (int i = 1; i < kJoinWaves; ++i) v += acc[i][e];
-    v *= inv;
-    if constexpr (DT == kFP32) static_cast<float *>(args.out)[at + e] = v;
-    else static_cast<uint16_t *>(args.out)[at + e] = (uint16_t)out_bits<DT>(v);
+  for (int c = 0; c < C; ++c) {
+    const int e = 2 * lane + 128 * c;
+    if (e >= D) continue;
+    if constexpr (DT == kFP32)
+      *reinterpret_cast<f32x2 *>(static_cast<float *>(args.out) + at + e) = o[c] * inv;
+    else
+      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(args.out) + at + e) =
+          pack2<DT>(o[c].x * inv, o[c].y * inv);
   }
 }
 
 // ------------------------------------------------------------------- host
 
-// The split of a call: 16-row tiles of a workgroup, and ranges of positions so
-// that the launch has about two workgroups for each CU.
-Plan plan_of(int64_t batch, int64_t max_rows, int64_t max_len, int64_t heads, int64_t kv_heads,
-             int head_dim) {
+// From this many rows of a kv head on, a workgroup's waves have rows of their own.
+constexpr int kApartMinRows = 128;
+
+// From how many positions on an item is split, and the fewest that a range has.
+constexpr int64_t kSplitFrom = 1536, kMinRange = 512, kMinRangeApart = 1024;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The split of a call: blocks of rows, and ranges of positions.
+Plan plan_of(const KvAttentionSizes &z) {
   Plan p;
-  const int64_t pairs = max_rows * (heads / kv_heads);
-  p.tiles = pairs <= 16 ? 1 : max_tiles(head_dim);
-  const int64_t rows = 16 * p.tiles;
-  const int64_t rb = (pairs + rows - 1) / rows;
-  const int64_t items = batch * kv_heads * rb;
-  const int64_t want = 2 * (int64_t)device_cu_count();
-  int64_t s = items > 0 ? (want + items - 1) / items : 1;
-  const int64_t most = (max_len + kChunkAlign - 1) / kChunkAlign;
-  if (s > most) s = most;
+  const int64_t pairs = (int64_t)z.max_rows * (z.heads / z.kv_heads);
+  p.merge = pairs < kApartMinRows;
+  p.tiles = p.merge && pairs <= 16 ? 1 : max_tiles(z.head_dim);
+  p.wg_rows = 16 * p.tiles * (p.merge ? 1 : kApartWaves);
+  p.wg_blocks = (int)ceil_div(pairs, p.wg_rows);
+  p.align = kStep * (p.merge ? kMergeWaves : 1);
+  const int64_t items = (int64_t)z.batch * z.kv_heads * p.wg_blocks;
+  // positions that a row sees at most, in units of the time that one takes at 16 bits
+  // and head_dim 128
+  int64_t span = z.max_len;
+  if (z.window > 0 && span > (int64_t)z.window + z.max_rows) span = (int64_t)z.window + z.max_rows;
+  const int64_t weight = z.head_dim * (z.dtype == kFP32 ? 3 : 1);
+  // two workgroups for a CU; a second launch is worth it where a workgroup alone
+  // would take kSplitFrom positions or more
+  int64_t s = 1;
+  if (span * weight >= kSplitFrom * 128) {
+    const int64_t want = 2 * (int64_t)device_cu_count();
+    s = items > 0 ? ceil_div(want, items) : 1;
+    const int64_t least = p.merge ? kMinRange * 128 / weight : kMinRangeApart;
+    const int64_t most = ceil_div(span, least > 0 ? least : 1);
+    if (s > most) s = most;
+    if (!p.merge && items >= want / 2) s = 1;
+  }
   if (s < 1) s = 1;
-  p.row_blocks = (int)rb;
   p.splits = (int)s;
-  p.part_rows = (int)(pairs < rows ? pairs : rows);
-  p.part_floats = s > 1 ? items * s * p.part_rows * head_dim : 0;
+  p.part_rows = (int)(pairs < p.wg_rows ? pairs : p.wg_rows);
   p.stats = s > 1 ? items * s * p.part_rows : 0;
+  p.part_floats = p.stats * z.head_dim;
   return p;
 }
 
@@ -108,10 +153,16 @@ uint32_t f16_bits(double v, double *rest) {
 
 template <int D, int DT>
 hipError_t launch_join(const AttnArgs &a, const Plan &p, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.max_rows * a.group), (unsigned)a.kv.kv_heads,
-                  (unsigned)a.kv.batch);
-  hipLaunchKernelGGL((kv_attention_join_kernel<D, DT>), grid, dim3(64 * kJoinWaves), 0, stream, a,
-                     16 * p.tiles);
+  const int rows = a.max_rows * a.group;
+  dim3 grid((unsigned)rows, (unsigned)a.kv.kv_heads, (unsigned)a.kv.batch);
+  if (p.merge) {
+    hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, false>), grid, dim3(64 * kJoinWaves), 0,
+                       stream, a, p.align);
+  } else {
+    grid.x = (unsigned)ceil_div(rows, kJoinWaves);
+    hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, true>), grid, dim3(64 * kJoinWaves), 0,
+                       stream, a, p.align);
+  }
   return hipGetLastError();
 }
 
@@ -131,25 +182,23 @@ hipError_t launch_dt(const AttnArgs &a, const Plan &p, const KvShape &sh, hipStr
 
 }  // namespace
 
-int64_t kv_attention_bytes(int batch, int max_rows, int max_len, int heads, int kv_heads,
-                           int head_dim) {
-  const Plan p = plan_of(batch, max_rows, max_len, heads, kv_heads, head_dim);
+int64_t kv_attention_bytes(const KvAttentionSizes &z) {
+  const Plan p = plan_of(z);
   const int64_t bytes = p.part_floats * 4 + p.stats * 8;
   return (bytes + 255) / 256 * 256;
 }
 
-bool kv_attention_fits(int batch, int max_rows, int max_len, int heads, int kv_heads,
-                       int head_dim) {
-  const int64_t pairs = (int64_t)max_rows * (heads / kv_heads);
-  if (pairs * (64 * kJoinWaves) > 0xffffffffll || batch > 65535 || kv_heads > 65535) return false;
-  const Plan p = plan_of(batch, max_rows, max_len, heads, kv_heads, head_dim);
-  return (int64_t)p.row_blocks * p.splits * kThreads <= 0xffffffffll;
+bool kv_attention_fits(const KvAttentionSizes &z) {
+  const int64_t pairs = (int64_t)z.max_rows * (z.heads / z.kv_heads);
+  if (pairs * (64 * kJoinWaves) > 0xffffffffll || z.batch > 65535 || z.kv_heads > 65535)
+    return false;
+  const Plan p = plan_of(z);
+  return (int64_t)p.wg_blocks * p.splits * (64 * kMergeWaves) <= 0xffffffffll;
 }
 
-hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAttentionCall &c,
-                               hipStream_t stream) {
-  const int heads = c.group * kv.kv_heads;
-  const Plan p = plan_of(kv.batch, c.max_rows, c.max_len, heads, kv.kv_heads, sh.head_dim);
+hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAttentionSizes &z,
+                               const KvAttentionCall &c, hipStream_t stream) {
+  const Plan p = plan_of(z);
   AttnArgs a;
   a.kv = kv;
   a.q = c.q;
@@ -158,11 +207,12 @@ hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAtte
   a.q_head = c.q_head;
   a.out_row = c.out_row;
   a.out_head = c.out_head;
-  a.group = c.group;
-  a.max_rows = c.max_rows;
+  a.group = z.heads / z.kv_heads;
+  a.max_rows = z.max_rows;
   a.causal = c.causal;
-  a.window = c.window;
-  a.row_blocks = p.row_blocks;
+  a.window = z.window;
+  a.wg_rows = p.wg_rows;
+  a.wg_blocks = p.wg_blocks;
   a.splits = p.splits;
   a.part_rows = p.part_rows;
   a.part = static_cast<float *>(c.workspace);
@@ -173,8 +223,8 @@ hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAtte
   const CodeTables &t = code_tables(sh.quant_type);
   for (int i = 0; i < 16; ++i) {
     double rest;
-    a.hi[i] = f16_bits((double)t.value[i] * mu, &rest);
-    a.lo[i] = f16_bits(rest, nullptr);
+    const uint32_t c1 = f16_bits((double)t.value[i] * mu, &rest);
+    a.codes[i] = c1 | f16_bits(rest, nullptr) << 16;
   }
   if (sh.dtype == kFP32) return launch_dt<kFP32>(a, p, sh, stream);
   if (sh.dtype == kFP16) return launch_dt<kFP16>(a, p, sh, stream);

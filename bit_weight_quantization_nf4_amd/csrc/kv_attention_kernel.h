@@ -38,6 +38,10 @@
 // in fp16 after a power of two. w: one fp16 for bf16 rows (2^-12), two for fp16
 // rows, whose output resolves 2^-11. fp32 rows: q, c' and w in two parts each, the
 // three leading products. Accumulators and statistics are fp32.
+//
+// Work. An item is a workgroup's block of rows of one sequence and kv head; where
+// items are few its positions are split into equal ranges, whose partial sums a second
+// kernel joins.
 #pragma once
 
 #include <type_traits>
@@ -47,11 +51,13 @@
 namespace nf4 {
 namespace kvattn {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kStep = 32;                  // positions of a wave's step
+constexpr int kStep = 32;   // positions of a wave's step
 constexpr int kTableBytes = 256 * 256;
-constexpr int kChunkAlign = kStep * kWaves;  // a workgroup's range is a multiple
+// Two shapes of workgroup. Few rows: its 8 waves share one block of rows and take
+// the steps of its positions in turn, then merge. Many rows: each of its 4 waves
+// has a block of rows of its own and takes every step, so nothing is merged.
+constexpr int kMergeWaves = 8;
+constexpr int kApartWaves = 4;
 
 struct AttnArgs {
   KvArgs kv;
@@ -62,15 +68,39 @@ struct AttnArgs {
   float f;       // scale log2(e) / mu
   float inv_mu;
   int32_t causal, window;
-  int32_t row_blocks;  // per sequence and kv head
-  int32_t splits;
-  int32_t part_rows;   // rows of a partial result
-  float *part;         // [item][split][part_rows][D]
-  float2 *stats;       // [item][split][part_rows]: reference, sum
-  uint32_t hi[16], lo[16];  // fp16 code values c' by nibble, and what they leave
+  int32_t wg_rows;    // (row, head) pairs of a workgroup's block
+  int32_t wg_blocks;  // such blocks of a sequence and kv head
+  int32_t splits;     // ranges of positions of an item
+  int32_t part_rows;  // rows of a partial result
+  float *part;        // [item][split][part_rows][D]
+  float2 *stats;      // [item][split][part_rows]: reference, sum
+  uint32_t codes[16];  // by nibble: c1 in the low half, c2 in the high one (fp16)
 };
 
-// A row block of one sequence: its rows and the positions that they see.
+// The kernels read their arguments through this type, from the argument segment
+// and through a pointer that is renewed where a kernel's phases meet: held in
+// scalar registers from end to end they would not leave enough of these.
+typedef const __attribute__((address_space(4))) AttnArgs KernelArgs;
+
+__device__ __forceinline__ KernelArgs *kernel_args() {
+  auto *p = (KernelArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
+// Has every 64-byte line of the arguments on its way to the scalar cache at once:
+// they lie in host memory, and a line takes about a microsecond.
+__device__ __forceinline__ void fetch_args() {
+  const auto *p = (const __attribute__((address_space(4))) uint32_t *)kernel_args();
+  constexpr int kLines = (sizeof(AttnArgs) + 63) / 64;
+  uint32_t v[kLines];
+#pragma unroll
+  for (int i = 0; i < kLines; ++i) v[i] = p[16 * i];
+#pragma unroll
+  for (int i = 0; i < kLines; ++i) asm volatile("" ::"s"(v[i]));
+}
+
+// A block of rows of one sequence, and the positions that they see.
 struct Block {
   int n;         // rows of the sequence in the call
   int first;     // their first row in the tensors
@@ -78,41 +108,74 @@ struct Block {
   int row0;      // first (row, head) pair of the block, row-major by token
   int pairs;     // such pairs of the sequence (up to max_rows tokens)
   int lo, hi;    // positions [lo, hi) that any row of the block sees
+  int all_lo, all_hi;  // positions that every row sees
 };
 
-__device__ __forceinline__ int seen_end(const AttnArgs &a, const Block &b, int token) {
+// Positions of a range: equal multiples of `align`.
+__device__ __forceinline__ int range_of(const Block &b, int splits, int align) {
+  const int total = b.hi - b.lo;
+  const int range = splits == 1 ? total : (total + splits - 1) / splits;
+  return (range + align - 1) / align * align;
+}
+
+__device__ __forceinline__ int64_t item_of(KernelArgs &a, int seq, int h, int wb) {
+  return ((int64_t)seq * a.kv.kv_heads + h) * a.wg_blocks + wb;
+}
+
+__device__ __forceinline__ int seen_end(KernelArgs &a, const Block &b, int token) {
   return a.causal ? b.len - b.n + token + 1 : b.len;
 }
 
-__device__ __forceinline__ int seen_begin(const AttnArgs &a, int end) {
+__device__ __forceinline__ int seen_begin(KernelArgs &a, int end) {
   return a.window > 0 && end > a.window ? end - a.window : 0;
 }
 
-__device__ __forceinline__ Block block_of(const AttnArgs &a, int seq, int rb, int rows) {
+// A sequence of the call.
+struct Sequence {
+  int first;  // its first row in the tensors
+  int n;      // its rows in the call
+  int len;
+};
+
+__device__ __forceinline__ Sequence sequence_of(KernelArgs &a, int seq) {
+  Sequence s;
+  const int len = scalar_load(a.kv.lens, seq);
+  int end;
+  if (a.kv.offsets == nullptr) {
+    s.first = seq * a.kv.uniform;
+    end = s.first + a.kv.uniform;
+  } else {
+    const int b0 = scalar_load(a.kv.offsets, seq), b1 = scalar_load(a.kv.offsets, seq + 1);
+    s.first = clamp_to(b0, 0, a.kv.total_rows);
+    end = clamp_to(b1, 0, a.kv.total_rows);
+  }
+  s.n = end > s.first ? end - s.first : 0;
+  s.len = clamp_to(len, 0, a.kv.capacity);
+  return s;
+}
+
+__device__ __forceinline__ Block block_of(KernelArgs &a, const Sequence &s, int row0, int rows) {
   Block b;
-  b.first = row_begin(a.kv, seq);
-  const int end = row_begin(a.kv, seq + 1);
-  b.n = end > b.first ? end - b.first : 0;
-  b.len = clamp_to(scalar_load(a.kv.lens, seq), 0, a.kv.capacity);
+  b.n = s.n;
+  b.first = s.first;
+  b.len = s.len;
   const int tokens = b.n < a.max_rows ? b.n : a.max_rows;
   b.pairs = tokens * a.group;
-  b.row0 = rb * rows;
-  b.lo = b.hi = 0;
+  b.row0 = row0;
+  b.lo = b.hi = b.all_lo = b.all_hi = 0;
   if (b.row0 < b.pairs) {
-    const int last = (b.row0 + rows < b.pairs ? b.row0 + rows : b.pairs) - 1;
-    b.hi = seen_end(a, b, last / a.group);
-    b.lo = seen_begin(a, seen_end(a, b, b.row0 / a.group));
+    // divisions only where a sequence has several blocks
+    const int token0 = row0 == 0 ? 0 : row0 / a.group;
+    const int token1 = row0 + rows >= b.pairs ? tokens - 1 : (row0 + rows - 1) / a.group;
+    const int end0 = seen_end(a, b, token0), end1 = seen_end(a, b, token1);
+    b.hi = end1;
+    b.lo = seen_begin(a, end0);
+    b.all_hi = end0;
+    b.all_lo = seen_begin(a, end1);
     if (b.hi <= b.lo) b.lo = b.hi = 0;
     b.lo &= ~(kStep - 1);
   }
   return b;
-}
-
-// Positions of a split: equal multiples of kChunkAlign.
-__device__ __forceinline__ int chunk_of(const Block &b, int splits) {
-  const int total = b.hi - b.lo;
-  const int chunk = (total + splits - 1) / splits;
-  return (chunk + kChunkAlign - 1) / kChunkAlign * kChunkAlign;
 }
 
 // Byte SRC of w as the second byte of a table address, lane_off as its first.
@@ -128,8 +191,53 @@ __device__ __forceinline__ float row_scale(const float *s) {
       0, (int)__float_as_uint(s[V / 16]), 0x150 + V % 16, 0xf, 0xf, true));
 }
 
-__device__ __forceinline__ float max4(f32x4 v) {
-  return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+// Maximum of numbers: fmaxf would first quiet NaNs, one instruction an operand.
+__device__ __forceinline__ float max2(float a, float b) {
+  return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return max2(max2(a, b), c); }
+
+// A barrier for what the workgroup shares in LDS. (__syncthreads would also wait
+// for every load from memory.)
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A lane's value that is not known before this point: what a loop derives from it is
+// not computed ahead of the loop and held in registers throughout.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// A wave-uniform value to be held in scalar registers from here on.
+template <typename T>
+__device__ __forceinline__ T pin(T v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// Maximum over the lanes n, n + 16, n + 32, n + 48.
+__device__ __forceinline__ float max_over_groups(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = max2(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return max2(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+__device__ __forceinline__ float sum_over_groups(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Half H of four fp16 pairs, each pair twice.
+template <int H>
+__device__ __forceinline__ uint4 twice(uint4 v) {
+  return H == 0 ? make_uint4(v.x, v.x, v.y, v.y) : make_uint4(v.z, v.z, v.w, v.w);
 }
 
 template <int I, int N, typename F>
@@ -140,28 +248,36 @@ __device__ __forceinline__ void unroll(F &&f) {
   }
 }
 
-// Two fp32 as an fp16 pair, and what that leaves as another.
+// What an fp16 pair leaves of two fp32, as another.
 __device__ __forceinline__ uint32_t rest_f16x2(float a, float b, uint32_t h) {
   return pack_f16x2(a - widen16<kFP16>(h & 0xffffu), b - widen16<kFP16>(h >> 16));
 }
 
+// Pointers to global memory that stay so (not generic) through pin().
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef const __attribute__((address_space(1))) uint8_t *GlobalU8;
+typedef const __attribute__((address_space(1))) float *GlobalF32;
+
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&d)[N], const uint8_t *p) {
+__device__ __forceinline__ void load_words(uint32_t (&d)[N], GlobalU8 p) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-      d[4 * i] = v.x; d[4 * i + 1] = v.y; d[4 * i + 2] = v.z; d[4 * i + 3] = v.w;
+      const u32x4 v = ((const __attribute__((address_space(1))) u32x4 *)p)[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[4 * i + j] = v[j];
     }
   } else if constexpr (N % 2 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-      const uint2 v = reinterpret_cast<const uint2 *>(p)[i];
-      d[2 * i] = v.x; d[2 * i + 1] = v.y;
+      const u32x2 v = ((const __attribute__((address_space(1))) u32x2 *)p)[i];
+      d[2 * i] = v[0];
+      d[2 * i + 1] = v[1];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) d[i] = reinterpret_cast<const uint32_t *>(p)[i];
+    for (int i = 0; i < N; ++i) d[i] = ((const __attribute__((address_space(1))) uint32_t *)p)[i];
   }
 }
 
@@ -174,22 +290,31 @@ __device__ __forceinline__ uint32_t word_at(const uint32_t (&d)[N]) {
   else return d[O / 4] >> (8 * (O % 4));
 }
 
-// DT: element type of q and out. NR: 16-row tiles of query rows.
-template <int D, int BS, int DT, int NR>
+// DT: element type of q and out. NR: 16-row tiles of a wave's block of rows. MERGE:
+// the workgroup's waves share the block (the first shape).
+template <int D, int BS, int DT, int NR, bool MERGE>
 struct Attn {
+  static constexpr int kWaves = MERGE ? kMergeWaves : kApartWaves;
+  static constexpr int kThreads = 64 * kWaves;
   static constexpr int P = D / 32;          // 32-wide pieces
   static constexpr int NB = D / BS;         // blocks of a head vector
   static constexpr int PB = BS / 32;        // pieces of a block
-  static constexpr int RW = D / 32;         // words a lane holds of a 16-position tile
   static constexpr int NS = (8 * NB + 15) / 16;  // scales a lane holds of a step
   static constexpr bool kSplitW = DT != kBF16;   // two-part weights
   static constexpr bool kSplitQ = DT == kFP32;   // two-part queries and keys' code values
   static constexpr int kRows = 16 * NR;
-  static constexpr int kPad = D + 4;
-  // the merge of the waves' results handles this many 16-row tiles and columns at once
-  static constexpr int kMergeCols = D > 128 ? D / 2 : D;
-  static constexpr int kMergeBytes = kWaves * 16 * (kMergeCols + 4) * 4;
-  static constexpr int kLds = kTableBytes > kMergeBytes ? kTableBytes : kMergeBytes;
+  // waves for which registers are shared out: two workgroups of a CU where they
+  // suffice (128 registers), else one of 8 waves or two of 4 (256)
+  static constexpr int kWavesPerSimd = MERGE && NR == 1 && D <= 128 && DT != kFP32 ? 4 : 2;
+  // with two waves on a SIMD, lookups are kept ahead of the products that they feed;
+  // with four the others fill the wait, and the registers are needed
+  static constexpr bool kAhead = kWavesPerSimd < 4 && !(kSplitQ && D > 128);
+  // the merge of the waves' results handles this many rows and columns at once, so
+  // that its buffer and the table leave room for a second workgroup where there is one
+  static constexpr int kMergeRows = kWavesPerSimd == 4 ? 4 : 16;
+  static constexpr int kMergeCols = kWavesPerSimd == 4 || D > 128 ? D / 2 : D;
+  static constexpr int kMergeStride = kMergeCols + 4;
+  static constexpr int kMergeFloats = MERGE ? kWaves * kMergeRows * kMergeStride : 1;
 };
 
 // Raw inputs of a step.
@@ -200,220 +325,350 @@ struct StepIn {
   float ks[(8 * (D / BS) + 15) / 16], vs[(8 * (D / BS) + 15) / 16];
 };
 
-template <int D, int BS, int DT, int NR>
-__global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs args) {
-  using A = Attn<D, BS, DT, NR>;
+template <int D, int BS, int DT, int NR, bool MERGE>
+__global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute__((
+    amdgpu_waves_per_eu(Attn<D, BS, DT, NR, MERGE>::kWavesPerSimd))) void kv_attention_kernel(
+    AttnArgs) {
+  using A = Attn<D, BS, DT, NR, MERGE>;
   constexpr int P = A::P, NB = A::NB, PB = A::PB, NS = A::NS;
-  __shared__ __attribute__((aligned(16))) char lds[A::kLds];
-  __shared__ float wave_m[kWaves][A::kRows];
-  __shared__ float wave_l[kWaves][A::kRows];
+  constexpr int kWaves = A::kWaves, kThreads = A::kThreads;
+  constexpr int TW = MERGE ? kWaves : 1;  // waves that share a block's steps
+  __shared__ __attribute__((aligned(16))) char lds[kTableBytes];
+  // the waves' results where they merge; before, the queries they share
+  __shared__ __attribute__((aligned(16))) float merge_buf[A::kMergeFloats];
+  __shared__ float wave_m[MERGE ? kWaves : 1][A::kRows];
+  __shared__ float wave_l[MERGE ? kWaves : 1][A::kRows];
   __shared__ float total_l[A::kRows];
+  __shared__ float wave_top[kWaves];
 
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = lane & 15, g = lane >> 4;
-  const KvArgs &kv = args.kv;
-  const int split = (int)blockIdx.x % args.splits;
-  const int rb = (int)blockIdx.x / args.splits;
-  const int h = (int)blockIdx.y, seq = (int)blockIdx.z;
+  fetch_args();
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int tw = MERGE ? wave : 0;
+  const uint32_t my_code = kernel_args()->codes[threadIdx.x & 15];
 
-  const Block blk = block_of(args, seq, rb, A::kRows);
-  if (blk.row0 >= blk.pairs) return;
-  const int chunk = chunk_of(blk, args.splits);
-  const int begin = blk.lo + split * chunk;
-  const int end = begin + chunk < blk.hi ? begin + chunk : blk.hi;
-  // a split past the positions leaves nothing behind; with one split the rows
-  // that see nothing are still written
-  if (begin >= blk.hi && args.splits > 1) return;
-
-  // the table: thread t fills the half t & 1 of entry t >> 1
-  {
-    const int e = tid >> 1;
-    const uint32_t w = tid & 1 ? args.lo[e >> 4] | args.lo[e & 15] << 16
-                               : args.hi[e >> 4] | args.hi[e & 15] << 16;
-    uint4 *dst = reinterpret_cast<uint4 *>(lds + 256 * e + 128 * (tid & 1));
+  // the table, in pieces of 128 bytes: first and second parts of an entry. Lane l
+  // holds code l & 15. A barrier follows before it is read.
+  auto write_table = [&] {
+    for (int i = threadIdx.x; i < 512; i += kThreads) {
+      const int e = i >> 1;
+      const uint32_t a = (uint32_t)__shfl((int)my_code, e >> 4, 64);
+      const uint32_t b = (uint32_t)__shfl((int)my_code, e & 15, 64);
+      const uint32_t w = i & 1 ? a >> 16 | (b & 0xffff0000u) : (a & 0xffffu) | b << 16;
+      uint4 *dst = reinterpret_cast<uint4 *>(lds + 128 * i);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dst[(i + tid) & 7] = make_uint4(w, w, w, w);
-  }
-  const uint32_t lane_off = 4u * (lane & 31);
+      for (int j = 0; j < 8; ++j) dst[(j + i) & 7] = make_uint4(w, w, w, w);
+    }
+  };
 
-  // queries: lane (n, g) holds elements 32 c + 8 g .. + 7 of row n of each tile
-  const void *qbase = args.q;
+  // ---- the positions [begin, end) of an item
+  const int lane = (int)threadIdx.x & 63;
+  const int n = lane & 15, g = lane >> 4;
+  const uint32_t lane_off = 4u * (lane & 31);
+  KernelArgs &args = *kernel_args();
+  const auto &kv = args.kv;
+  const int h = (int)blockIdx.y, seq = (int)blockIdx.z;
+  int wb = (int)blockIdx.x, split = 0;
+  if (args.splits > 1) {
+    wb = (int)blockIdx.x / args.splits;
+    split = (int)blockIdx.x - wb * args.splits;
+  }
+  // blocks of later rows see more positions: they come first
+  wb = args.wg_blocks - 1 - wb;
+  const Sequence of = sequence_of(args, seq);
+  const Block item = block_of(args, of, wb * args.wg_rows, args.wg_rows);
+  const int range = range_of(item, args.splits, kStep * TW);
+  int begin = item.lo + split * range;
+  int end = range < item.hi - begin ? begin + range : item.hi;
+  // a workgroup without rows, or with a range past the positions, leaves nothing
+  // behind; with one range the rows that see nothing are still written
+  if (item.row0 >= item.pairs || (begin >= item.hi && args.splits > 1)) return;
+  const bool whole_item = args.splits == 1;
+  const int64_t part_row0 = (item_of(args, seq, h, wb) * args.splits + split) * args.part_rows;
+  // a wave's own rows may see less, and there may be none
+  const Block blk = MERGE ? item : block_of(args, of, item.row0 + wave * A::kRows, A::kRows);
+  const bool have_rows = blk.row0 < blk.pairs;
+  if (!MERGE) {
+    begin = begin > blk.lo ? begin : blk.lo;
+    end = end < blk.hi ? end : blk.hi;
+  }
+
+  // ---- where its steps lie, and the first one's inputs on their way
+  const int steps_all = end > begin ? (end - begin + kStep - 1) / kStep : 0;
+  const int nsteps = steps_all > tw ? (steps_all - tw + TW - 1) / TW : 0;
+  // scalars of the loop, kept in registers
+  const int64_t head_packed = (int64_t)h * kv.page_size * (16 * P);
+  const int64_t head_absmax = (int64_t)h * kv.page_size * NB;
+  const GlobalU8 k_base = pin((GlobalU8)(uintptr_t)kv.packed[0] + head_packed);
+  const GlobalU8 v_base = pin((GlobalU8)(uintptr_t)kv.packed[1] + head_packed);
+  const GlobalF32 ks_base = pin((GlobalF32)(uintptr_t)kv.absmax[0] + head_absmax);
+  const GlobalF32 vs_base = pin((GlobalF32)(uintptr_t)kv.absmax[1] + head_absmax);
+  const uint32_t packed_units = pin((uint32_t)(kv.packed_stride >> 4));
+  const uint32_t absmax_units = pin((uint32_t)kv.absmax_stride);
+  const ConstI32 table = pin((ConstI32)(uintptr_t)kv.table + (int64_t)seq * kv.table_stride);
+  const int last_col = pin(kv.table_cols - 1);
+  const uint32_t num_pages = pin((uint32_t)kv.num_pages);
+  const int tiles_per_page = pin(kv.page_size / 16);
+  // both tiles of a step in one page, which holds an even number of them
+  const bool paired = (tiles_per_page & 1) == 0;
+  const int tile0 = (begin >> 4) + 2 * tw;
+  int col = nsteps > 0 ? tile0 / tiles_per_page : 0;
+  int in_page = tile0 - col * tiles_per_page;
+  const int step_cols = pin(2 * TW / tiles_per_page);
+  const int step_in_page = pin(2 * TW - step_cols * tiles_per_page);
+  auto advance = [&] {
+    col += step_cols;
+    in_page += step_in_page;
+    if (in_page >= tiles_per_page) {
+      in_page -= tiles_per_page;
+      ++col;
+    }
+  };
+  // pages (and tiles within them) of a step's two 16-position tiles
+  struct Where { uint32_t page[2]; int at[2]; };
+  auto locate = [&] {
+    Where w;
+    w.page[0] = (uint32_t)table[col];
+    w.at[0] = in_page;
+    w.page[1] = w.page[0];
+    w.at[1] = in_page + 1;
+    if (!paired && in_page + 1 == tiles_per_page) {
+      w.page[1] = (uint32_t)table[col < last_col ? col + 1 : last_col];
+      w.at[1] = 0;
+    }
+    return w;
+  };
+  // where the tiles' codes and scales lie; a page that is not there is read as the
+  // first one and masked
+  struct Places {
+    GlobalU8 k[2], v[2];
+    GlobalF32 ks[2], vs[2];
+    bool ok[2];
+  };
+  auto places_of = [&](const Where &w) {
+    Places p;
+    uint64_t codes, scales;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (t == 0 || !paired) {
+        p.ok[t] = w.page[t] < num_pages;
+        const uint32_t page = p.ok[t] ? w.page[t] : 0;
+        codes = ((uint64_t)page * packed_units + (uint32_t)(w.at[t] * (16 * P))) << 4;
+        scales = (uint64_t)page * absmax_units + (uint32_t)(w.at[t] * (16 * NB));
+      } else {
+        p.ok[1] = p.ok[0];
+        codes += 256 * P;
+        scales += 16 * NB;
+      }
+      p.k[t] = k_base + codes;
+      p.v[t] = v_base + codes;
+      p.ks[t] = ks_base + scales;
+      p.vs[t] = vs_base + scales;
+    }
+    return p;
+  };
+  StepIn<D, BS> in;
+  // the scales that the lane holds: values 16 u + n of the DPP row's 8 positions
+  auto load_scales = [&](float (&s)[NS], const GlobalF32 (&base)[2]) {
+#pragma unroll
+    for (int u = 0; u < NS; ++u) {
+      int v = 16 * u + n;
+      v = v < 8 * NB ? v : v % (8 * NB);
+      const int tk = v / NB;
+      s[u] = (tk < 4 ? base[0] : base[1])[(uint32_t)((4 * g + (tk & 3)) * NB + (v - tk * NB))];
+    }
+  };
+  auto load_k = [&](const Places &p) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      load_words(in.k[t], p.k[t] + (uint32_t)(n * (16 * P) + g * (4 * P)));
+    load_scales(in.ks, p.ks);
+  };
+  auto load_v = [&](const Places &p) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      load_words(in.v[t], p.v[t] + (uint32_t)(g * (64 * P) + n * (4 * P)));
+    load_scales(in.vs, p.vs);
+  };
+  bool ok0 = false, ok1 = false;
+  if (nsteps > 0) {
+    const Places p = places_of(locate());
+    load_k(p);
+    load_v(p);
+    ok0 = p.ok[0];
+    ok1 = p.ok[1];
+  }
+
+  // token and head (of the group) of a row of the block: small numbers, so a
+  // product with the reciprocal and half a step is the quotient
+  struct RowAt { int token, head; };
+  const int token0 = blk.row0 == 0 ? 0 : blk.row0 / args.group, head0 = blk.row0 - token0 * args.group;
+  const float per_group = 1.0f / (float)args.group;
+  auto row_at = [&](int i) {
+    const int q = (int)(((float)(head0 + i) + 0.5f) * per_group);
+    return RowAt{token0 + q, head0 + i - q * args.group};
+  };
+
+  // ---- queries: lane (n, g) holds elements 32 c + 8 g .. + 7 of row n of each tile,
+  // as fp16 after one power of two for all rows that brings the largest below 2^15.
+  // Rows past the last repeat the first one; nothing of theirs is stored. Waves that
+  // share a block convert a fragment each.
   uint4 qh[NR][P];
-  uint4 ql[A::kSplitQ ? NR : 1][A::kSplitQ ? P : 1];
+  uint4 ql[A::kSplitQ && !MERGE ? NR : 1][A::kSplitQ && !MERGE ? P : 1];
   int row_lo[NR], row_hi[NR];  // positions the row sees
-  int min_hi = 0x7fffffff, max_lo = 0;
-  float qscale_f;
+  float qscale;
+  uint4 *const q_shared = reinterpret_cast<uint4 *>(merge_buf);  // [first, second parts][fragment][lane]
   {
-    float qf[NR][P][8];
-    float top = 0.0f;
+    struct Raw { uint4 v[DT == kFP32 ? 2 : 1]; };
+    auto load_raw = [&](int nr, int c) {
+      Raw r;
+      const RowAt ra = row_at(blk.row0 + 16 * nr + n < blk.pairs ? 16 * nr + n : 0);
+      const int64_t at = (int64_t)(blk.first + ra.token) * args.q_row +
+                         (int64_t)(h * args.group + ra.head) * args.q_head + 8 * g + 32 * c;
+      const uint4 *p = reinterpret_cast<const uint4 *>(
+          static_cast<const char *>(args.q) + at * (DT == kFP32 ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < (DT == kFP32 ? 2 : 1); ++i) r.v[i] = p[i];
+      return r;
+    };
+    auto element = [](const Raw &r, int i) {
+      if constexpr (DT == kFP32) {
+        const uint32_t w[4] = {r.v[i >> 2].x, r.v[i >> 2].y, r.v[i >> 2].z, r.v[i >> 2].w};
+        return __uint_as_float(w[i & 3]);
+      } else {
+        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+        return widen16<DT>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu);
+      }
+    };
+    auto largest = [&](const Raw &r) {
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) top = max3(top, fabsf(element(r, i)), fabsf(element(r, i + 1)));
+      return top;
+    };
+    auto exponent = [](float top) {
+      return __builtin_amdgcn_readfirstlane(top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0);
+    };
+    auto convert = [&](const Raw &r, int ex, uint4 &hi, uint4 &lo) {
+      uint32_t h16[4], l16[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = __builtin_amdgcn_ldexpf(element(r, 2 * i), 15 - ex);
+        const float x1 = __builtin_amdgcn_ldexpf(element(r, 2 * i + 1), 15 - ex);
+        h16[i] = pack_f16x2(x0, x1);
+        if constexpr (A::kSplitQ) l16[i] = rest_f16x2(x0, x1, h16[i]);
+      }
+      hi = make_uint4(h16[0], h16[1], h16[2], h16[3]);
+      if constexpr (A::kSplitQ) lo = make_uint4(l16[0], l16[1], l16[2], l16[3]);
+    };
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
-      const int pair = blk.row0 + 16 * nr + n;
-      const bool have = pair < blk.pairs;
-      const int token = have ? pair / args.group : 0;
-      const int64_t at = (int64_t)(blk.first + token) * args.q_row +
-                         (int64_t)(h * args.group + (have ? pair - token * args.group : 0)) *
-                             args.q_head + 8 * g;
-      row_hi[nr] = have ? seen_end(args, blk, token) : 0;
+      const bool have = blk.row0 + 16 * nr + n < blk.pairs;
+      row_hi[nr] = have ? seen_end(args, blk, row_at(16 * nr + n).token) : 0;
       row_lo[nr] = have ? seen_begin(args, row_hi[nr]) : 0;
-#pragma unroll
-      for (int c = 0; c < P; ++c) {
-        float (&x)[8] = qf[nr][c];
-        if constexpr (DT == kFP32) {
-          const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(qbase) + at + 32 * c);
-          const float4 u = p[0], v = p[1];
-          x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-          x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-        } else {
-          const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(qbase) + at + 32 * c);
-          const uint32_t d[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[2 * i] = widen16<DT>(d[i] & 0xffffu);
-            x[2 * i + 1] = widen16<DT>(d[i] >> 16);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = have ? x[i] : 0.0f;
-          top = fmaxf(top, fabsf(x[i]));
-        }
-      }
-      if (have) {
-        min_hi = row_hi[nr] < min_hi ? row_hi[nr] : min_hi;
-        max_lo = row_lo[nr] > max_lo ? row_lo[nr] : max_lo;
-      }
     }
-    // one power of two for all rows brings the largest element below 2^15
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      top = fmaxf(top, __shfl_xor(top, off, 64));
-      const int oh = __shfl_xor(min_hi, off, 64), ol = __shfl_xor(max_lo, off, 64);
-      min_hi = oh < min_hi ? oh : min_hi;
-      max_lo = ol > max_lo ? ol : max_lo;
-    }
-    min_hi = __builtin_amdgcn_readfirstlane(min_hi);
-    max_lo = __builtin_amdgcn_readfirstlane(max_lo);
-    const int ex = __builtin_amdgcn_readfirstlane(top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0);
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int c = 0; c < P; ++c) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = __builtin_amdgcn_ldexpf(qf[nr][c][2 * i], 15 - ex);
-          const float x1 = __builtin_amdgcn_ldexpf(qf[nr][c][2 * i + 1], 15 - ex);
-          hi[i] = pack_f16x2(x0, x1);
-          if constexpr (A::kSplitQ) lo[i] = rest_f16x2(x0, x1, hi[i]);
-        }
-        qh[nr][c] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if constexpr (A::kSplitQ) ql[nr][c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    int ex;
+    if constexpr (MERGE) {
+      static_assert(NR * P <= kWaves, "a fragment for each wave");
+      Raw raw;
+      const int nr = wave / P, c = wave - nr * P;
+      if (wave < NR * P) raw = load_raw(nr, c);
+      write_table();
+      if (wave < NR * P) {
+        const float top = max_over_groups(row16_max(largest(raw)));
+        if (lane == 0) wave_top[wave] = top;
       }
-    qscale_f = __builtin_amdgcn_ldexpf(args.f, ex - 15);
+      lds_barrier();
+      float top = wave_top[0];
+#pragma unroll
+      for (int i = 1; i < NR * P; ++i) top = max2(top, wave_top[i]);
+      ex = exponent(top);
+      if (wave < NR * P) {
+        uint4 hi, lo;
+        convert(raw, ex, hi, lo);
+        q_shared[64 * wave + lane] = hi;
+        if constexpr (A::kSplitQ) q_shared[64 * (NR * P + wave) + lane] = lo;
+      }
+      lds_barrier();
+#pragma unroll
+      for (int f = 0; f < NR * P; ++f) qh[f / P][f % P] = q_shared[64 * f + lane];
+    } else {
+      Raw raw[NR][P];
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+          if (have_rows) raw[nr][c] = load_raw(nr, c);
+      write_table();
+      lds_barrier();
+      float top = 0.0f;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int c = 0; c < P; ++c) top = max2(top, largest(raw[nr][c]));
+      ex = exponent(max_over_groups(row16_max(top)));
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+          convert(raw[nr][c], ex, qh[nr][c], ql[A::kSplitQ ? nr : 0][A::kSplitQ ? c : 0]);
+    }
+    qscale = __builtin_amdgcn_ldexpf(args.f, ex - 15);
   }
+  // the second parts of a fragment
+  auto q_low = [&](auto nrc, auto cc) {
+    if constexpr (MERGE) return q_shared[64 * (NR * P + nrc * P + cc) + lane];
+    else return ql[nrc][cc];
+  };
 
+  // ---- state: m_ref is -inf before a row has seen anything; m_use stands for it
   f32x4 o[NR][2 * P];
-  float m_ref[NR], m_use[NR], l_sum[NR];
+  float m_use[NR], m_limit[NR], l_sum[NR];
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
     for (int j = 0; j < 2 * P; ++j) o[nr][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    m_ref[nr] = -__builtin_inff();
     m_use[nr] = 0.0f;
+    m_limit[nr] = -__builtin_inff();  // a score past m_use by more moves the reference
     l_sum[nr] = 0.0f;
   }
-  int a_exp = -1000;       // A = 2^a_exp
-  float a_inv = 0.0f;      // 2^8 / A
-  float a_limit = -1.0f;   // 8 A
+  int a_exp = -1000;      // A = 2^a_exp
+  float a_inv = 0.0f;     // 2^8 / A
+  float a_limit = -1.0f;  // 8 A
 
-  // ---- the wave's steps: 32-position steps wave, wave + 8, ... of the range
-  const int steps_all = (end - begin + kStep - 1) / kStep;
-  const int nsteps = steps_all > wave ? (steps_all - wave + kWaves - 1) / kWaves : 0;
-  const int tiles_per_page = kv.page_size / 16;
-  const int64_t head_packed = (int64_t)h * kv.page_size * (16 * P);
-  const int64_t head_absmax = (int64_t)h * kv.page_size * NB;
-  const int64_t table_row = (int64_t)seq * kv.table_stride;
-
-  // page and tile within it of a 16-position tile
-  struct Where { int32_t page; int at; };
-  auto where = [&](int tile) {
-    int col = tile / tiles_per_page;
-    const int at = tile - col * tiles_per_page;
-    col = col < kv.table_cols ? col : kv.table_cols - 1;
-    return Where{scalar_load(kv.table, table_row + col), at};
-  };
-  auto valid_page = [&](int32_t page) { return page >= 0 && page < kv.num_pages; };
-
-  StepIn<D, BS> in;
-  bool ok[2];
-  auto load_k = [&](const Where (&w)[2]) {
-    const uint8_t *base[2];
-    const float *sbase[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int64_t page = valid_page(w[t].page) ? w[t].page : 0;
-      base[t] = kv.packed[0] + page * kv.packed_stride + head_packed + w[t].at * (256 * P);
-      sbase[t] = kv.absmax[0] + page * kv.absmax_stride + head_absmax + w[t].at * (16 * NB);
-      load_words(in.k[t], base[t] + (uint32_t)(n * (16 * P) + g * (4 * P)));
-    }
-#pragma unroll
-    for (int u = 0; u < NS; ++u) {
-      int v = 16 * u + n;
-      v = v < 8 * NB ? v : v % (8 * NB);
-      const int tk = v / NB;
-      const uint32_t off = (uint32_t)((4 * g + (tk & 3)) * NB + (v - tk * NB));
-      in.ks[u] = (tk < 4 ? sbase[0] : sbase[1])[off];
-    }
-  };
-  auto load_v = [&](const Where (&w)[2]) {
-    const float *sbase[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int64_t page = valid_page(w[t].page) ? w[t].page : 0;
-      const uint8_t *base = kv.packed[1] + page * kv.packed_stride + head_packed + w[t].at * (256 * P);
-      sbase[t] = kv.absmax[1] + page * kv.absmax_stride + head_absmax + w[t].at * (16 * NB);
-      load_words(in.v[t], base + (uint32_t)(g * (64 * P) + n * (4 * P)));
-    }
-#pragma unroll
-    for (int u = 0; u < NS; ++u) {
-      int v = 16 * u + n;
-      v = v < 8 * NB ? v : v % (8 * NB);
-      const int tk = v / NB;
-      const uint32_t off = (uint32_t)((4 * g + (tk & 3)) * NB + (v - tk * NB));
-      in.vs[u] = (tk < 4 ? sbase[0] : sbase[1])[off];
-    }
-  };
-
-  Where w[2], wn[2];
-  const int tile0 = (begin >> 4) + 2 * wave;
-  if (nsteps > 0) {
-    w[0] = where(tile0);
-    w[1] = where(tile0 + 1);
-    load_k(w);
-    load_v(w);
-  }
-  __syncthreads();  // the table
-
+  const int all_lo = pin(blk.all_lo), all_hi = pin(blk.all_hi), len = pin(blk.len);
   for (int s = 0; s < nsteps; ++s) {
-    const int pos0 = begin + kStep * (wave + kWaves * s);
-    const int next = s + 1 < nsteps ? s + 1 : s;
-    wn[0] = where(tile0 + 2 * kWaves * next);
-    wn[1] = where(tile0 + 2 * kWaves * next + 1);
-    ok[0] = valid_page(w[0].page);
-    ok[1] = valid_page(w[1].page);
+    const int pos0 = begin + kStep * (tw + TW * s);
+    if (s + 1 < nsteps) advance();  // the last step loads its own inputs again
+    const Where next_at = locate();
+    const bool ok[2] = {ok0, ok1};
     // every row sees the whole step (uniform)
-    const bool whole = ok[0] && ok[1] && pos0 >= max_lo && pos0 + kStep <= min_hi;
+    const bool whole = ok0 && ok1 && pos0 >= all_lo && pos0 + kStep <= all_hi;
 
-    // ---- S^T = K Q^T, combined over blocks into log2 units
+    // ---- S^T = K Q^T, combined over blocks into log2 units past m_use
     float ks[NS];
 #pragma unroll
-    for (int u = 0; u < NS; ++u) ks[u] = in.ks[u] * qscale_f;
+    for (int u = 0; u < NS; ++u) ks[u] = in.ks[u] * qscale;
     f32x4 t[NR][2];
+    // four code pairs of piece c: the byte of elements 32 c + 8 g + 2 i is i P + c of
+    // the lane's run
+    auto look_up_k = [&](auto tc, auto cc, uint32_t off) {
+      uint32_t e[4];
+      unroll<0, 4>([&](auto ic) {
+        constexpr int O = ic * P + cc;
+        e[ic] = *reinterpret_cast<const uint32_t *>(
+            lds + table_address<O % 4>(in.k[tc][O / 4], off));
+      });
+      return make_uint4(e[0], e[1], e[2], e[3]);
+    };
+    uint4 ahead[A::kAhead ? 2 : 1][A::kAhead ? P : 1];
+    auto look_up_tile = [&](auto tc) {
+      unroll<0, P>([&](auto cc) { ahead[tc][cc] = look_up_k(tc, cc, lane_off); });
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (A::kAhead) look_up_tile(std::integral_constant<int, 0>{});
     unroll<0, 2>([&](auto tc) {
       constexpr int T = tc;
+      if constexpr (A::kAhead && T == 0) look_up_tile(std::integral_constant<int, 1>{});
       unroll<0, NB>([&](auto bc) {
         constexpr int B = bc;
         f32x4 acc[NR];
@@ -421,22 +676,19 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs args) {
         for (int nr = 0; nr < NR; ++nr) acc[nr] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         unroll<0, PB>([&](auto pc) {
           constexpr int C = B * PB + pc;  // 32-wide piece
-          uint32_t kh[4], kl[4];
-          unroll<0, 4>([&](auto ic) {
-            constexpr int O = ic * P + C;  // the byte of elements 32 C + 8 g + 2 i
-            const uint32_t ad = table_address<O % 4>(in.k[T][O / 4], lane_off);
-            kh[ic] = *reinterpret_cast<const uint32_t *>(lds + ad);
-            if constexpr (A::kSplitQ) kl[ic] = *reinterpret_cast<const uint32_t *>(lds + ad + 128);
-          });
-          const uint4 a = make_uint4(kh[0], kh[1], kh[2], kh[3]);
+          const std::integral_constant<int, C> cc;
+          uint4 k1;
+          if constexpr (A::kAhead) k1 = ahead[T][C];
+          else k1 = look_up_k(tc, cc, lane_off);
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr) {
-            acc[nr] = mfma16x16x32<kFP16>(a, qh[nr][C], acc[nr]);
-            if constexpr (A::kSplitQ) {
-              acc[nr] = mfma16x16x32<kFP16>(a, ql[nr][C], acc[nr]);
-              acc[nr] = mfma16x16x32<kFP16>(make_uint4(kl[0], kl[1], kl[2], kl[3]), qh[nr][C],
-                                            acc[nr]);
-            }
+          for (int nr = 0; nr < NR; ++nr) acc[nr] = mfma16x16x32<kFP16>(k1, qh[nr][C], acc[nr]);
+          if constexpr (A::kSplitQ) {
+            const uint4 k2 = look_up_k(tc, cc, lane_off + 128u);
+            unroll<0, NR>([&](auto nrc) {
+              constexpr int nr = nrc;
+              acc[nr] = mfma16x16x32<kFP16>(k1, q_low(nrc, cc), acc[nr]);
+              acc[nr] = mfma16x16x32<kFP16>(k2, qh[nr][C], acc[nr]);
+            });
           }
         });
         unroll<0, 4>([&](auto rc) {
@@ -444,11 +696,12 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs args) {
           const float a = row_scale<(4 * T + R) * NB + B>(ks);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
-            t[nr][T][R] = B == 0 ? acc[nr][R] * a : __builtin_fmaf(acc[nr][R], a, t[nr][T][R]);
+            t[nr][T][R] = __builtin_fmaf(acc[nr][R], a, B == 0 ? -m_use[nr] : t[nr][T][R]);
         });
       });
     });
-    load_k(wn);
+    const Places next = places_of(next_at);
+    load_k(next);
 
     // ---- masks
     float vs[NS];
@@ -472,7 +725,7 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs args) {
         v = v < 8 * NB ? v : v % (8 * NB);
         const int tk = v / NB;
         const int p = pos0 + 16 * (tk >> 2) + 4 * g + (tk & 3);
-        vs[u] = p < blk.len && (tk < 4 ? ok[0] : ok[1]) ? vs[u] : 0.0f;
+        vs[u] = p < len && (tk < 4 ? ok[0] : ok[1]) ? vs[u] : 0.0f;
       }
     }
 
@@ -481,17 +734,17 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs args) {
     bool far = false;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
-      top[nr] = fmaxf(max4(t[nr][0]), max4(t[nr][1]));
-      far = far || top[nr] > m_ref[nr] + 4.0f;
+      const f32x4 u = t[nr][0], v = t[nr][1];
+      top[nr] = max3(max3(u[0], u[1], u[2]), max3(u[3], v[0], v[1]), max2(v[2], v[3]));
+      far = far || top[nr] > m_limit[nr];
     }
 #pragma unroll
     for (int u = 0; u < NS; ++u) far = far || vs[u] > a_limit;
     if (__builtin_amdgcn_ballot_w64(far) != 0) {
       float av = vs[0];
 #pragma unroll
-      for (int u = 1; u < NS; ++u) av = fmaxf(av, vs[u]);
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) av = fmaxf(av, __shfl_xor(av, off, 64));
+      for (int u = 1; u < NS; ++u) av = max2(av, vs[u]);
+      av = max_over_groups(row16_max(av));
       // 2^8 / A stays finite: from 2^127 on, smaller scales are exact in fp16 steps
       // finer than the result's
       int ex = __builtin_amdgcn_readfirstlane(av > 0.0f ? __builtin_amdgcn_frexp_expf(av) : -119);
@@ -503,17 +756,18 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs args) {
       a_limit = __builtin_amdgcn_ldexpf(8.0f, ex);
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
-        float mx = top[nr];
-        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-        const float m_new = fmaxf(m_ref[nr], mx);
-        const float use = m_new == -__builtin_inff() ? 0.0f : m_new;
-        // a row that has seen nothing has nothing to rescale
-        const float alpha = __builtin_amdgcn_exp2f(m_ref[nr] - use);
+        const float mx = max_over_groups(top[nr]);
+        const bool fresh = m_limit[nr] != 4.0f;         // nothing seen before
+        const bool some = mx != -__builtin_inff();
+        // how far the reference moves: to the maximum, never back
+        const float move = !some ? 0.0f : (fresh ? mx : fmaxf(mx, 0.0f));
+        const float alpha = fresh ? 0.0f : __builtin_amdgcn_exp2f(-move);
         const float beta = __builtin_amdgcn_ldexpf(alpha, shift);
-        m_ref[nr] = m_new;
-        m_use[nr] = use;
+        m_use[nr] += move;
+        m_limit[nr] = some ? 4.0f : m_limit[nr];
         l_sum[nr] *= alpha;
+#pragma unroll
+        for (int T = 0; T < 2; ++T) t[nr][T] -= move;
 #pragma unroll
         for (int j = 0; j < 2 * P; ++j) o[nr][j] *= beta;
       }
@@ -528,7 +782,7 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs args) {
     for (int nr = 0; nr < NR; ++nr) {
       float p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(t[nr][i >> 2][i & 3] - m_use[nr]);
+      for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(t[nr][i >> 2][i & 3]);
       l_sum[nr] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       unroll<0, NB>([&](auto bc) {
         constexpr int B = bc;
@@ -545,149 +799,224 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(AttnArgs args) {
     }
 
     // ---- O^T += V^T W^T
-    unroll<0, (P + 3) / 4>([&](auto wc) {
-      constexpr int WD = wc;                              // word of a position's run
-      constexpr int KN = P - 4 * WD < 4 ? P - 4 * WD : 4;  // its bytes
-      uint32_t even[2][2], odd[2][2];  // [tile][pair of positions]: merged nibbles
+    // word wd of the positions' runs: merged nibbles of [tile][pair of positions]
+    uint32_t even[2][2], odd[2][2];
+    auto merge_nibbles = [&](auto wc) {
       unroll<0, 2>([&](auto tc) {
         constexpr int T = tc;
         unroll<0, 2>([&](auto pc) {
           constexpr int R = 2 * pc;
-          const uint32_t a = word_at<R * P + 4 * WD>(in.v[T]);
-          const uint32_t b = word_at<(R + 1) * P + 4 * WD>(in.v[T]);
+          const uint32_t a = word_at<R * P + 4 * wc>(in.v[T]);
+          const uint32_t b = word_at<(R + 1) * P + 4 * wc>(in.v[T]);
           even[T][pc] = (a & 0xf0f0f0f0u) | ((b >> 4) & 0x0f0f0f0fu);
           odd[T][pc] = ((a << 4) & 0xf0f0f0f0u) | (b & 0x0f0f0f0fu);
         });
       });
-      unroll<0, KN>([&](auto kc) {
-        constexpr int K = 4 * WD + kc;
-        constexpr int B = K / PB;
+    };
+    // both parts of two pairs of positions side by side
+    auto look_up_v = [&](auto kk, auto jc, auto tc) {
+      uint32_t e[4];
+      unroll<0, 2>([&](auto ic) {
+        const uint32_t ad = table_address<kk % 4>(jc == 0 ? even[tc][ic] : odd[tc][ic], lane_off);
+        e[2 * ic] = *reinterpret_cast<const uint32_t *>(lds + ad);
+        e[2 * ic + 1] = *reinterpret_cast<const uint32_t *>(lds + ad + 128);
+      });
+      return make_uint4(e[0], e[1], e[2], e[3]);
+    };
+    // [tile of elements][tile of positions], of this piece and the next
+    uint4 vc[A::kAhead ? 2 : 1][2][2];
+    auto look_up_piece = [&](auto kk) {
+      if constexpr (kk % 4 == 0) merge_nibbles(std::integral_constant<int, kk / 4>{});
+      unroll<0, 2>([&](auto tc) {
+        unroll<0, 2>([&](auto jc) { vc[kk & 1][jc][tc] = look_up_v(kk, jc, tc); });
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (A::kAhead) look_up_piece(std::integral_constant<int, 0>{});
+    unroll<0, P>([&](auto kk) {
+      constexpr int K = kk;
+      constexpr int B = K / PB;
+      if constexpr (!A::kAhead && K % 4 == 0) merge_nibbles(std::integral_constant<int, K / 4>{});
+      if constexpr (A::kAhead && K + 1 < P) look_up_piece(std::integral_constant<int, K + 1>{});
+      // weights twice, as both parts of a pair take the same
+      unroll<0, 2>([&](auto tc) {
         unroll<0, 2>([&](auto jc) {
-          uint32_t vh[4], vl[4];
-          unroll<0, 4>([&](auto ic) {
-            const uint32_t src = jc == 0 ? even[ic >> 1][ic & 1] : odd[ic >> 1][ic & 1];
-            const uint32_t ad = table_address<kc>(src, lane_off);
-            vh[ic] = *reinterpret_cast<const uint32_t *>(lds + ad);
-            vl[ic] = *reinterpret_cast<const uint32_t *>(lds + ad + 128);
-          });
-          const uint4 a = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+          uint4 v;
+          if constexpr (A::kAhead) v = vc[K & 1][jc][tc];
+          else v = look_up_v(kk, jc, tc);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) {
             f32x4 &acc = o[nr][2 * K + jc];
-            acc = mfma16x16x32<kFP16>(a, wh[nr][B], acc);
-            if constexpr (A::kSplitW) acc = mfma16x16x32<kFP16>(a, wl[nr][B], acc);
-            acc = mfma16x16x32<kFP16>(make_uint4(vl[0], vl[1], vl[2], vl[3]), wh[nr][B], acc);
+            acc = mfma16x16x32<kFP16>(v, twice<tc>(wh[nr][B]), acc);
+            if constexpr (A::kSplitW) acc = mfma16x16x32<kFP16>(v, twice<tc>(wl[nr][B]), acc);
           }
         });
       });
     });
-    load_v(wn);
-    w[0] = wn[0];
-    w[1] = wn[1];
+    load_v(next);
+    ok0 = next.ok[0];
+    ok1 = next.ok[1];
   }
 
-  // ---- merge the waves: one reference per row, then the sums in wave order
+  // ---- results: a row's output, or its partial sums
+  float l_row[NR], m_ref[NR];
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) {
-    float l = l_sum[nr];
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    if (g == 0) {
-      wave_m[wave][16 * nr + n] = m_ref[nr];
-      wave_l[wave][16 * nr + n] = l;
-    }
+    l_row[nr] = sum_over_groups(l_sum[nr]);
+    m_ref[nr] = m_limit[nr] == 4.0f ? m_use[nr] : -__builtin_inff();
   }
-  __syncthreads();
-  float factor[NR];
-  const int64_t item = ((int64_t)seq * kv.kv_heads + h) * args.row_blocks + rb;
-  const int64_t part_row0 = (item * args.splits + split) * args.part_rows;
+  KernelArgs &end_args = *kernel_args();
+  const int tid = fresh((int)threadIdx.x);
+  auto out_at = [&](int i) {
+    const RowAt ra = row_at(i);
+    return (int64_t)(blk.first + ra.token) * end_args.out_row +
+           (int64_t)(h * end_args.group + ra.head) * end_args.out_head;
+  };
+
+  if constexpr (!MERGE) {
 #pragma unroll
-  for (int nr = 0; nr < NR; ++nr) {
-    float mx = wave_m[0][16 * nr + n];
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) mx = fmaxf(mx, wave_m[i][16 * nr + n]);
-    const float use = mx == -__builtin_inff() ? 0.0f : mx;
-    factor[nr] = args.inv_mu * __builtin_amdgcn_exp2f(m_ref[nr] - use);
-    if (wave == 0 && g == 0) {
-      float l = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i)
-        l += wave_l[i][16 * nr + n] * __builtin_amdgcn_exp2f(wave_m[i][16 * nr + n] - use);
-      total_l[16 * nr + n] = l;
-      if (args.splits > 1 && 16 * nr + n < args.part_rows)
-        args.stats[part_row0 + 16 * nr + n] = make_float2(mx, l);
-    }
-  }
-  constexpr int MC = A::kMergeCols, ML = MC + 4;
-  float *buf = reinterpret_cast<float *>(lds);
-  unroll<0, NR>([&](auto nrc) {
-    constexpr int nr = nrc;
-    unroll<0, D / MC>([&](auto cc) {
-      constexpr int K0 = cc * (MC / 32);
-      __syncthreads();
-      // lane (n, g) holds row n's elements 32 k + 8 g + 2 r + {0, 1}
-      unroll<0, MC / 32>([&](auto kc) {
-        constexpr int K = K0 + kc;
-        float *dst = buf + (wave * 16 + n) * ML + 32 * kc + 8 * g;
-        // undo A apart from the factor: their product may be subnormal
-        auto undo = [&](float v) { return __builtin_amdgcn_ldexpf(v * factor[nr], a_exp - 8); };
+    for (int nr = 0; nr < NR; ++nr) {
+      const int pair = blk.row0 + 16 * nr + n;
+      if (pair >= blk.pairs) continue;
+      const int64_t part_row = part_row0 + wave * A::kRows + 16 * nr + n;
+      const float f = !whole_item ? end_args.inv_mu
+                                  : (l_row[nr] > 0.0f ? end_args.inv_mu / l_row[nr] : 0.0f);
+      // undo A apart from the factor: their product may be subnormal
+      auto undo = [&](float v) { return __builtin_amdgcn_ldexpf(v * f, a_exp - 8); };
+      if (!whole_item && g == 0) end_args.stats[part_row] = make_float2(m_ref[nr], l_row[nr]);
+      float *part = end_args.part + part_row * D + 8 * g;
+      const int64_t at = out_at(16 * nr + n) + 8 * g;
+      // the lane holds elements 32 k + 8 g + 2 r + {0, 1}
+      unroll<0, P>([&](auto kc) {
+        constexpr int K = kc;
         const f32x4 e = o[nr][2 * K], d = o[nr][2 * K + 1];
-        reinterpret_cast<f32x4 *>(dst)[0] = f32x4{undo(e[0]), undo(d[0]), undo(e[1]), undo(d[1])};
-        reinterpret_cast<f32x4 *>(dst)[1] = f32x4{undo(e[2]), undo(d[2]), undo(e[3]), undo(d[3])};
-      });
-      __syncthreads();
-      for (int idx = tid; idx < 16 * (MC / 4); idx += kThreads) {
-        const int row = idx / (MC / 4), col = 4 * (idx - row * (MC / 4));
-        f32x4 sum = *reinterpret_cast<const f32x4 *>(buf + row * ML + col);
-#pragma unroll
-        for (int i = 1; i < kWaves; ++i)
-          sum += *reinterpret_cast<const f32x4 *>(buf + (i * 16 + row) * ML + col);
-        const int pair = blk.row0 + 16 * nr + row;
-        const int ccol = cc * MC + col;
-        if (pair >= blk.pairs) continue;
-        if (args.splits > 1) {
-          *reinterpret_cast<f32x4 *>(args.part + (part_row0 + 16 * nr + row) * D + ccol) = sum;
+        const f32x4 v0 = {undo(e[0]), undo(d[0]), undo(e[1]), undo(d[1])};
+        const f32x4 v1 = {undo(e[2]), undo(d[2]), undo(e[3]), undo(d[3])};
+        if (!whole_item || DT == kFP32) {
+          f32x4 *dst = reinterpret_cast<f32x4 *>(
+              whole_item ? static_cast<float *>(end_args.out) + at + 32 * K : part + 32 * K);
+          dst[0] = v0;
+          dst[1] = v1;
         } else {
-          const float l = total_l[16 * nr + row];
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-          const int token = pair / args.group;
-          const int64_t at = (int64_t)(blk.first + token) * args.out_row +
-                             (int64_t)(h * args.group + pair - token * args.group) * args.out_head +
-                             ccol;
-          if constexpr (DT == kFP32) {
-            *reinterpret_cast<f32x4 *>(static_cast<float *>(args.out) + at) = sum * inv;
-          } else {
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(args.out) + at) =
-                make_uint2(pack2<DT>(sum[0] * inv, sum[1] * inv), pack2<DT>(sum[2] * inv, sum[3] * inv));
-          }
+          constexpr int T = DT == kFP32 ? kBF16 : DT;
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(end_args.out) + at + 32 * K) =
+              make_uint4(pack2<T>(v0[0], v0[1]), pack2<T>(v0[2], v0[3]), pack2<T>(v1[0], v1[1]),
+                         pack2<T>(v1[2], v1[3]));
         }
+      });
+    }
+  } else {
+    // merge the waves: one reference per row, then the sums in wave order
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      if (g == 0) {
+        wave_m[wave][16 * nr + n] = m_ref[nr];
+        wave_l[wave][16 * nr + n] = l_row[nr];
+      }
+    }
+    lds_barrier();
+    float factor[NR];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      float mx = wave_m[0][16 * nr + n];
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) mx = fmaxf(mx, wave_m[i][16 * nr + n]);
+      const float use = mx == -__builtin_inff() ? 0.0f : mx;
+      factor[nr] = end_args.inv_mu * __builtin_amdgcn_exp2f(m_ref[nr] - use);
+      if (wave == 0 && g == 0) {
+        float l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i)
+          l += wave_l[i][16 * nr + n] * __builtin_amdgcn_exp2f(wave_m[i][16 * nr + n] - use);
+        total_l[16 * nr + n] = l;
+        if (!whole_item && 16 * nr + n < end_args.part_rows)
+          end_args.stats[part_row0 + 16 * nr + n] = make_float2(mx, l);
+      }
+    }
+    constexpr int MR = A::kMergeRows, MC = A::kMergeCols, ML = A::kMergeStride;
+    const int rows = blk.pairs - blk.row0;  // of the block, where fewer than its tiles
+    unroll<0, NR>([&](auto nrc) {
+      constexpr int nr = nrc;
+      for (int r0 = 0; r0 < 16 && 16 * nr + r0 < rows; r0 += MR) {
+        unroll<0, D / MC>([&](auto cc) {
+          constexpr int K0 = cc * (MC / 32);
+          lds_barrier();
+          if (n >= r0 && n < r0 + MR) {
+            unroll<0, MC / 32>([&](auto kc) {
+              constexpr int K = K0 + kc;
+              float *dst = merge_buf + (wave * MR + n - r0) * ML + 32 * kc + 8 * g;
+              // undo A apart from the factor: their product may be subnormal
+              auto undo = [&](float v) {
+                return __builtin_amdgcn_ldexpf(v * factor[nr], a_exp - 8);
+              };
+              const f32x4 e = o[nr][2 * K], d = o[nr][2 * K + 1];
+              reinterpret_cast<f32x4 *>(dst)[0] =
+                  f32x4{undo(e[0]), undo(d[0]), undo(e[1]), undo(d[1])};
+              reinterpret_cast<f32x4 *>(dst)[1] =
+                  f32x4{undo(e[2]), undo(d[2]), undo(e[3]), undo(d[3])};
+            });
+          }
+          lds_barrier();
+          for (int idx = tid; idx < MR * (MC / 4); idx += kThreads) {
+            const int row = idx / (MC / 4), cl = 4 * (idx - row * (MC / 4));
+            const int in_block = 16 * nr + r0 + row;
+            if (in_block >= rows) continue;
+            f32x4 sum = *reinterpret_cast<const f32x4 *>(merge_buf + row * ML + cl);
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i)
+              sum += *reinterpret_cast<const f32x4 *>(merge_buf + (i * MR + row) * ML + cl);
+            const int ccol = cc * MC + cl;
+            if (!whole_item) {
+              *reinterpret_cast<f32x4 *>(end_args.part + (part_row0 + in_block) * D + ccol) = sum;
+            } else {
+              const float l = total_l[in_block];
+              const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+              const int64_t at = out_at(in_block) + ccol;
+              if constexpr (DT == kFP32) {
+                *reinterpret_cast<f32x4 *>(static_cast<float *>(end_args.out) + at) = sum * inv;
+              } else {
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(end_args.out) + at) = make_uint2(
+                    pack2<DT>(sum[0] * inv, sum[1] * inv), pack2<DT>(sum[2] * inv, sum[3] * inv));
+              }
+            }
+          }
+        });
       }
     });
-  });
+  }
 }
 
 // ------------------------------------------------------------------- host
 
 struct Plan {
-  int tiles, row_blocks, splits, part_rows;
+  bool merge;             // shape of the workgroups
+  int tiles;              // 16-row tiles of a wave's block of rows
+  int wg_rows, wg_blocks;
+  int splits, align;      // ranges of positions, their granularity
+  int part_rows;
   int64_t part_floats, stats;  // totals
 };
 
-// Largest number of 16-row tiles of a workgroup: what its registers hold.
+// Largest number of 16-row tiles of a wave's block: what its registers hold.
 constexpr int max_tiles(int head_dim) { return head_dim <= 128 ? 2 : 1; }
+
+template <int D, int BS, int DT, int NR, bool MERGE>
+hipError_t launch_one(const AttnArgs &a, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.wg_blocks * a.splits), (unsigned)a.kv.kv_heads,
+                  (unsigned)a.kv.batch);
+  hipLaunchKernelGGL((kv_attention_kernel<D, BS, DT, NR, MERGE>), grid,
+                     dim3(Attn<D, BS, DT, NR, MERGE>::kThreads), 0, stream, a);
+  return hipGetLastError();
+}
 
 template <int D, int BS, int DT>
 hipError_t launch_main(const AttnArgs &a, const Plan &p, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.row_blocks * p.splits), (unsigned)a.kv.kv_heads,
-                  (unsigned)a.kv.batch);
-  if constexpr (max_tiles(D) >= 2) {
-    if (p.tiles == 2) {
-      hipLaunchKernelGGL((kv_attention_kernel<D, BS, DT, 2>), grid, dim3(kThreads), 0, stream, a);
-      return hipGetLastError();
-    }
+  constexpr int T = max_tiles(D);
+  if (!p.merge) return launch_one<D, BS, DT, T, false>(a, stream);
+  if constexpr (T > 1) {
+    if (p.tiles > 1) return launch_one<D, BS, DT, T, true>(a, stream);
   }
-  hipLaunchKernelGGL((kv_attention_kernel<D, BS, DT, 1>), grid, dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
+  return launch_one<D, BS, DT, 1, true>(a, stream);
 }
 
 // Instantiated for each element type in a file of its own.

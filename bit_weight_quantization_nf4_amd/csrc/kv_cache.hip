@@ -13,6 +13,8 @@
 // sequence these share the run of 64 P bytes that holds four positions' values.
 // Both kernels are bound by HBM; a lane's 4-byte accesses to the 16-bit rows
 // cover 64 contiguous bytes per head vector and k.
+#include <type_traits>
+
 #include "kv_internal.h"
 
 namespace nf4 {
@@ -26,7 +28,8 @@ struct KvRowsArgs {
   const void *in[2];   // write: keys, values
   void *out[2];        // read: keys, values; write: their stored values or null
   int64_t row_stride, head_stride;  // elements
-  int64_t jobs;        // waves' worth of work: row groups x heads x 2
+  int64_t jobs;        // waves' worth of work: row groups x head groups x 2
+  int32_t job_heads, head_groups;
   float value[16];
   float cell_thr[kCells];
   uint32_t cell_codes[kCells];
@@ -110,18 +113,7 @@ __device__ __forceinline__ void load_run(const uint8_t *p, uint32_t (&w)[2]) {
   }
 }
 
-// A pair of neighbouring elements at element offset e (even), widened exactly.
-template <int DT>
-__device__ __forceinline__ f32x2 load_pair(const void *base, int64_t e) {
-  if constexpr (DT == kFP32) {
-    return *reinterpret_cast<const f32x2 *>(static_cast<const float *>(base) + e);
-  } else {
-    const uint32_t d =
-        *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + e);
-    return f32x2{widen16<DT>(d & 0xffffu), widen16<DT>(d >> 16)};
-  }
-}
-
+// A pair of neighbouring elements at element offset e (even).
 template <int DT>
 __device__ __forceinline__ void store_pair(void *base, int64_t e, float v0, float v1) {
   if constexpr (DT == kFP32) {
@@ -130,6 +122,52 @@ __device__ __forceinline__ void store_pair(void *base, int64_t e, float v0, floa
     *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + e) = pack2<DT>(v0, v1);
   }
 }
+
+// A lane's elements of a head vector as they are stored, and widened.
+template <int DT, int P>
+struct Pieces {
+  typename std::conditional<DT == kFP32, f32x2, uint32_t>::type v[P];
+};
+
+template <int DT, int P>
+__device__ __forceinline__ void load_row(Pieces<DT, P> &p, const void *base, int64_t e) {
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    if constexpr (DT == kFP32)
+      p.v[k] = *reinterpret_cast<const f32x2 *>(static_cast<const float *>(base) + e + 32 * k);
+    else
+      p.v[k] =
+          *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + e + 32 * k);
+  }
+}
+
+template <int DT, int P>
+__device__ __forceinline__ void widen(f32x2 (&x)[P], const Pieces<DT, P> &p) {
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    if constexpr (DT == kFP32) x[k] = p.v[k];
+    else x[k] = f32x2{widen16<DT>(p.v[k] & 0xffffu), widen16<DT>(p.v[k] >> 16)};
+  }
+}
+
+// The rows and heads of a job; consecutive jobs take keys and values of the same.
+struct Job {
+  int which, head0, head1;
+  int64_t row_group;
+};
+
+__device__ __forceinline__ Job job_of(const KvRowsArgs &args, int64_t job) {
+  Job j;
+  j.which = (int)(job & 1);
+  j.row_group = (job >> 1) / args.head_groups;
+  j.head0 = (int)((job >> 1) - j.row_group * args.head_groups) * args.job_heads;
+  j.head1 = j.head0 + args.job_heads < args.kv.kv_heads ? j.head0 + args.job_heads
+                                                        : args.kv.kv_heads;
+  return j;
+}
+
+// Heads whose codes a reading wave has in flight.
+constexpr int kInFlight = 4;
 
 // RN(x / a) given r = RN(1 / a): one product and one residual step (Markstein),
 // correctly rounded while a, r and the residual stay normal (a in [2^-100,
@@ -157,71 +195,72 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvRowsArgs args) {
                        __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t nwaves = (int64_t)gridDim.x * kWaves;
   for (int64_t job = wave; job < args.jobs; job += nwaves) {
-    const int which = (int)(job & 1);
-    const int64_t rg = (job >> 1) / kv.kv_heads;
-    const int h = (int)((job >> 1) - rg * kv.kv_heads);
-    const int64_t row = rg * 4 + (lane >> 4);
-    const bool have = row < kv.total_rows;
-    f32x2 x[P];
-    if (have) {
-      const int64_t e = row * args.row_stride + h * args.head_stride + 2 * m;
-#pragma unroll
-      for (int k = 0; k < P; ++k) x[k] = load_pair<DT>(args.in[which], e + 32 * k);
-    } else {
-#pragma unroll
-      for (int k = 0; k < P; ++k) x[k] = f32x2{0.0f, 0.0f};
-    }
-    const RowPlace place = have ? place_of(kv, (int)row) : RowPlace{false, false, 0, 0};
-
-    float a[NB], as[NB], r[NB];
-    int sh[NB];
-    bool normal = true;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float v = 0.0f;
-#pragma unroll
-      for (int k = b * PB; k < (b + 1) * PB; ++k)
-        v = fmaxf(v, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
-      a[b] = row16_max(v);
-      normal = normal && a[b] >= 0x1p-100f && a[b] < 0x1p120f;
-    }
-    // outside that range x and a are first scaled by the power of two that
-    // brings a into [1, 2): the quotient is the same. One branch for the wave.
-    const bool scaled = __builtin_amdgcn_ballot_w64(!normal) != 0;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      as[b] = a[b];
-      sh[b] = 0;
-      if (scaled && a[b] > 0.0f) {
-        sh[b] = 1 - __builtin_amdgcn_frexp_expf(a[b]);
-        as[b] = __builtin_amdgcn_ldexpf(a[b], sh[b]);
-      }
-      r[b] = as[b] == 0.0f ? 0.0f : 1.0f / as[b];
-    }
-    uint32_t w[2] = {0, 0};
+    const Job j = job_of(args, job);
+    const int64_t row = j.row_group * 4 + (lane >> 4);
+    // rows past the last take its values and have no place
+    const int64_t from = row < kv.total_rows ? row : kv.total_rows - 1;
+    const void *in = args.in[j.which];
+    Pieces<DT, P> next;
+    load_row(next, in, from * args.row_stride + j.head0 * args.head_stride + 2 * m);
+    const RowPlace place =
+        row < kv.total_rows ? place_of(kv, (int)row) : RowPlace{false, false, 0, 0};
     const bool values = args.out[0] != nullptr && place.in_call;
-    const int64_t ve = (row * kv.kv_heads + h) * D + 2 * m;
+    for (int h = j.head0; h < j.head1; ++h) {
+      f32x2 x[P];
+      widen(x, next);
+      // the next head's elements are on their way while this one's are encoded
+      const int hn = h + 1 < j.head1 ? h + 1 : h;
+      load_row(next, in, from * args.row_stride + hn * args.head_stride + 2 * m);
+
+      float a[NB], as[NB], r[NB];
+      int sh[NB];
+      bool normal = true;
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const int b = k / PB;
-      float x0 = x[k].x, x1 = x[k].y;
-      if (scaled) {
-        x0 = __builtin_amdgcn_ldexpf(x0, sh[b]);
-        x1 = __builtin_amdgcn_ldexpf(x1, sh[b]);
+      for (int b = 0; b < NB; ++b) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = b * PB; k < (b + 1) * PB; ++k)
+          v = fmaxf(v, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
+        a[b] = row16_max(v);
+        normal = normal && a[b] >= 0x1p-100f && a[b] < 0x1p120f;
       }
-      const uint32_t c0 = code_of(quotient(x0, as[b], r[b]), lut);
-      const uint32_t c1 = code_of(quotient(x1, as[b], r[b]), lut);
-      w[k >> 2] |= (c0 << 4 | c1) << (8 * (k & 3));
-      if (values) store_pair<DT>(args.out[which], ve + 32 * k, value[c0] * a[b], value[c1] * a[b]);
-    }
-    if (place.in_cache) {
-      store_run<P>(kv.packed[which] + run_offset<P>(kv, place, h, which, m), w);
-      float mine = a[0];
+      // outside that range x and a are first scaled by the power of two that
+      // brings a into [1, 2): the quotient is the same. One branch for the wave.
+      const bool scaled = __builtin_amdgcn_ballot_w64(!normal) != 0;
 #pragma unroll
-      for (int b = 1; b < NB; ++b) mine = m == b ? a[b] : mine;
-      if (m < NB)
-        kv.absmax[which][place.page * kv.absmax_stride +
-                         ((int64_t)h * kv.page_size + place.at) * NB + m] = mine;
+      for (int b = 0; b < NB; ++b) {
+        as[b] = a[b];
+        sh[b] = 0;
+        if (scaled && a[b] > 0.0f) {
+          sh[b] = 1 - __builtin_amdgcn_frexp_expf(a[b]);
+          as[b] = __builtin_amdgcn_ldexpf(a[b], sh[b]);
+        }
+        r[b] = as[b] == 0.0f ? 0.0f : 1.0f / as[b];
+      }
+      uint32_t w[2] = {0, 0};
+      const int64_t ve = (row * kv.kv_heads + h) * D + 2 * m;
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int b = k / PB;
+        float x0 = x[k].x, x1 = x[k].y;
+        if (scaled) {
+          x0 = __builtin_amdgcn_ldexpf(x0, sh[b]);
+          x1 = __builtin_amdgcn_ldexpf(x1, sh[b]);
+        }
+        const uint32_t c0 = code_of(quotient(x0, as[b], r[b]), lut);
+        const uint32_t c1 = code_of(quotient(x1, as[b], r[b]), lut);
+        w[k >> 2] |= (c0 << 4 | c1) << (8 * (k & 3));
+        if (values) store_pair<DT>(args.out[j.which], ve + 32 * k, value[c0] * a[b], value[c1] * a[b]);
+      }
+      if (place.in_cache) {
+        store_run<P>(kv.packed[j.which] + run_offset<P>(kv, place, h, j.which, m), w);
+        float mine = a[0];
+#pragma unroll
+        for (int b = 1; b < NB; ++b) mine = m == b ? a[b] : mine;
+        if (m < NB)
+          kv.absmax[j.which][place.page * kv.absmax_stride +
+                           ((int64_t)h * kv.page_size + place.at) * NB + m] = mine;
+      }
     }
   }
 }
@@ -238,34 +277,49 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRowsArgs args) {
                        __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t nwaves = (int64_t)gridDim.x * kWaves;
   for (int64_t job = wave; job < args.jobs; job += nwaves) {
-    const int which = (int)(job & 1);
-    const int64_t rg = (job >> 1) / kv.kv_heads;
-    const int h = (int)((job >> 1) - rg * kv.kv_heads);
-    const int64_t row = rg * 4 + (lane >> 4);
+    const Job j = job_of(args, job);
+    const int64_t row = j.row_group * 4 + (lane >> 4);
     if (row >= kv.total_rows) continue;
     const RowPlace place = place_of(kv, (int)row);
     if (!place.in_call) continue;
-    uint32_t w[2] = {0, 0};
-    float a[NB];
+    void *out = args.out[j.which];
+    if (!place.in_cache) {
+      for (int h = j.head0; h < j.head1; ++h)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) a[b] = 0.0f;
-    if (place.in_cache) {
-      load_run<P>(kv.packed[which] + run_offset<P>(kv, place, h, which, m), w);
-      const float *s = kv.absmax[which] + place.page * kv.absmax_stride +
-                       ((int64_t)h * kv.page_size + place.at) * NB;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) a[b] = s[b];
+        for (int k = 0; k < P; ++k)
+          store_pair<DT>(out, row * args.row_stride + h * args.head_stride + 2 * m + 32 * k, 0.0f,
+                         0.0f);
+      continue;
     }
-    const int64_t e = row * args.row_stride + h * args.head_stride + 2 * m;
+    // kInFlight heads' codes and scales a time
+    for (int h0 = j.head0; h0 < j.head1; h0 += kInFlight) {
+      uint32_t w[kInFlight][2];
+      float a[kInFlight][NB];
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const uint32_t byte = w[k >> 2] >> (8 * (k & 3)) & 0xffu;
-      float v0 = value[byte >> 4] * a[k / PB], v1 = value[byte & 15] * a[k / PB];
-      if (!place.in_cache) v0 = v1 = 0.0f;  // code 0 is not the value 0
-      store_pair<DT>(args.out[which], e + 32 * k, v0, v1);
+      for (int u = 0; u < kInFlight; ++u) {
+        const int h = h0 + u < j.head1 ? h0 + u : j.head1 - 1;
+        load_run<P>(kv.packed[j.which] + run_offset<P>(kv, place, h, j.which, m), w[u]);
+        const float *s = kv.absmax[j.which] + place.page * kv.absmax_stride +
+                         ((int64_t)h * kv.page_size + place.at) * NB;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) a[u][b] = s[b];
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        if (h0 + u >= j.head1) break;
+        const int64_t e = row * args.row_stride + (h0 + u) * args.head_stride + 2 * m;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const uint32_t byte = w[u][k >> 2] >> (8 * (k & 3)) & 0xffu;
+          store_pair<DT>(out, e + 32 * k, value[byte >> 4] * a[u][k / PB],
+                         value[byte & 15] * a[u][k / PB]);
+        }
+      }
     }
   }
 }
+
+constexpr int64_t kJobsWanted = 4096;
 
 KvRowsArgs make_args(const KvArgs &kv, const KvShape &sh) {
   KvRowsArgs a;
@@ -278,7 +332,16 @@ KvRowsArgs make_args(const KvArgs &kv, const KvShape &sh) {
   }
   a.in[0] = a.in[1] = nullptr;
   a.out[0] = a.out[1] = nullptr;
-  a.jobs = ((int64_t)kv.total_rows + 3) / 4 * kv.kv_heads * 2;
+  // A row's place costs a chain of dependent loads, so a wave takes as many heads
+  // of it as leave the launch kJobsWanted waves.
+  const int64_t row_groups = ((int64_t)kv.total_rows + 3) / 4;
+  int heads = 1;
+  while (heads < kv.kv_heads &&
+         row_groups * 2 * ((kv.kv_heads + 2 * heads - 1) / (2 * heads)) >= kJobsWanted)
+    heads *= 2;
+  a.job_heads = heads < kv.kv_heads ? heads : kv.kv_heads;
+  a.head_groups = (kv.kv_heads + a.job_heads - 1) / a.job_heads;
+  a.jobs = row_groups * a.head_groups * 2;
   return a;
 }
 

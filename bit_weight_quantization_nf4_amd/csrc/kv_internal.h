@@ -32,24 +32,26 @@ hipError_t launch_kv_write(const KvArgs &kv, const KvShape &sh, const void *k, c
 hipError_t launch_kv_read(const KvArgs &kv, const KvShape &sh, void *k, void *v,
                           int64_t row_stride, int64_t head_stride, hipStream_t stream);
 
+// What a call's split goes by.
+struct KvAttentionSizes {
+  int32_t batch, max_rows, max_len, heads, kv_heads, head_dim, dtype, window;
+};
+
 struct KvAttentionCall {
   const void *q;
   void *out;
   int64_t q_row, q_head, out_row, out_head;  // strides in elements
-  int32_t group, max_rows, max_len;
   float scale;
-  int32_t causal, window;
+  int32_t causal;
   void *workspace;
 };
 
-// Workspace bytes of a call; launch_kv_attention splits by the same rule. And
-// whether the launches of a call stay within the device's grid limits.
-int64_t kv_attention_bytes(int batch, int max_rows, int max_len, int heads, int kv_heads,
-                           int head_dim);
-bool kv_attention_fits(int batch, int max_rows, int max_len, int heads, int kv_heads,
-                       int head_dim);
-hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAttentionCall &c,
-                               hipStream_t stream);
+// Workspace bytes of a call, and whether its launches stay within the device's grid
+// limits.
+int64_t kv_attention_bytes(const KvAttentionSizes &z);
+bool kv_attention_fits(const KvAttentionSizes &z);
+hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAttentionSizes &z,
+                               const KvAttentionCall &c, hipStream_t stream);
 
 // ------------------------------------------------------------ device code
 

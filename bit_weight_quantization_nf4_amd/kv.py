@@ -42,7 +42,7 @@ _CACHE, _ROWS = ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVRowsDesc)
 _SIGNATURES = [
     ("nf4_kv_write", _I32, [_CACHE, _ROWS, _P, _P, _I64, _I64, _I32, _P, _P, _P]),
     ("nf4_kv_read", _I32, [_CACHE, _ROWS, _I32, _P, _P, _I64, _I64, _P]),
-    ("nf4_kv_attention_workspace_bytes", _I64, [_I32] * 6),
+    ("nf4_kv_attention_workspace_bytes", _I64, [_I32] * 8),
     ("nf4_kv_attention", _I32,
      [_CACHE, _ROWS, _P, _I64, _I64, _I32, _I32, ctypes.c_float, _I32, _I32, _I32, _I32, _P, _I64,
       _I64, _P, _I64, _P]),
@@ -71,23 +71,23 @@ class KVCache:
 
     def __init__(self, k_packed: torch.Tensor, k_absmax: torch.Tensor, v_packed: torch.Tensor,
                  v_absmax: torch.Tensor, blocksize: int = 64, quant_type: str = "nf4"):
-        if k_packed.dim() != 4:
-            raise ValueError("KVCache expects codes [pages, kv heads, page_size, head_dim / 2]")
-        pages, heads, page_size, half = k_packed.shape
+        if k_packed.dim() != 4 or k_packed.dtype != torch.uint8 or v_packed.dtype != torch.uint8:
+            raise ValueError("KVCache expects uint8 codes [pages, kv heads, page_size, head_dim / 2]")
+        shape, stride, sstride = k_packed.shape, k_packed.stride(), k_absmax.stride()
+        pages, heads, page_size, half = shape
         nb = 2 * half // blocksize if blocksize > 0 else 0
-        inner = (page_size * half, half, 1)
-        sinner = (page_size * nb, nb, 1)
-        for t in (k_packed, v_packed):
-            if t.dtype != torch.uint8 or t.shape != k_packed.shape or (
-                    pages and t.stride()[1:] != inner) or t.stride(0) != k_packed.stride(0):
-                raise ValueError("KVCache expects uint8 codes of one shape, contiguous in a page")
-        for t in (k_absmax, v_absmax):
-            if t.dtype != torch.float32 or t.shape != (pages, heads, page_size, nb) or (
-                    pages and t.stride()[1:] != sinner) or t.stride(0) != k_absmax.stride(0):
-                raise ValueError("KVCache expects fp32 scales [pages, kv heads, page_size, "
-                                 "head_dim / blocksize], contiguous in a page")
+        if v_packed.shape != shape or v_packed.stride() != stride or (
+                pages and stride[1:] != (page_size * half, half, 1)):
+            raise ValueError("KVCache expects codes of one shape, contiguous in a page")
+        if k_absmax.dtype != torch.float32 or v_absmax.dtype != torch.float32 or \
+                k_absmax.shape != (pages, heads, page_size, nb) or \
+                v_absmax.shape != k_absmax.shape or v_absmax.stride() != sstride or (
+                    pages and sstride[1:] != (page_size * nb, nb, 1)):
+            raise ValueError("KVCache expects fp32 scales [pages, kv heads, page_size, "
+                             "head_dim / blocksize], contiguous in a page")
         dev = k_packed.device
-        if dev.type != "cuda" or not (k_absmax.device == v_packed.device == v_absmax.device == dev):
+        if dev.type != "cuda" or k_absmax.device != dev or v_packed.device != dev or \
+                v_absmax.device != dev:
             raise TypeError("KVCache expects four tensors on one GPU")
         self.k_packed, self.k_absmax = k_packed, k_absmax
         self.v_packed, self.v_absmax = v_packed, v_absmax
@@ -96,7 +96,7 @@ class KVCache:
         self.head_dim = 2 * half
         self.device = dev
         self.desc = KVCacheDesc(k_packed.data_ptr(), k_absmax.data_ptr(), v_packed.data_ptr(),
-                                v_absmax.data_ptr(), pages, k_packed.stride(0), k_absmax.stride(0),
+                                v_absmax.data_ptr(), pages, stride[0], sstride[0],
                                 page_size, heads, 2 * half, blocksize, _QT[quant_type])
 
     @classmethod
@@ -143,6 +143,10 @@ def _strided(t: torch.Tensor) -> bool:
             and t.data_ptr() % 16 == 0)
 
 
+def _empty_rows(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _check_rows(t: torch.Tensor, cache: KVCache, what: str) -> None:
     if t.dtype not in _DT or t.device != cache.device:
         raise TypeError(f"{what} expects bf16 / fp16 / fp32 rows on the cache's GPU")
@@ -157,11 +161,16 @@ def _aligned_copy(t: torch.Tensor) -> torch.Tensor:
 
 def _call(cache: KVCache, fn, name: str, *args) -> None:
     """fn(*args, stream) on the cache's device and that device's current stream."""
-    if cache.device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream), name)
+    index = cache.device.index
+    # the raw handle: building a Stream object takes longer than the launch
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(cache.device):
-            _check(fn(*args, torch.cuda.current_stream().cuda_stream), name)
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status:
+        _check(status, name)
 
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
@@ -176,8 +185,7 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torc
     if not (k.stride() == v.stride() and _strided(k) and _strided(v)):
         k, v = _aligned_copy(k), _aligned_copy(v)
     rows = _rows(cache, k.shape[0], block_table, kv_lens, row_offsets, "kv_write")
-    kq = torch.empty(k.shape, dtype=k.dtype, device=k.device) if values else None
-    vq = torch.empty(k.shape, dtype=k.dtype, device=k.device) if values else None
+    kq, vq = (_empty_rows(k), _empty_rows(k)) if values else (None, None)
     _call(cache, _lib().nf4_kv_write, "nf4_kv_write", cache.desc, rows, k.data_ptr(), v.data_ptr(),
           k.stride(0), k.stride(1), _DT[k.dtype], kq.data_ptr() if values else None,
           vq.data_ptr() if values else None)
@@ -206,10 +214,11 @@ def kv_read(cache: KVCache, rows: int, block_table: torch.Tensor, kv_lens: torch
 
 
 def kv_attention_workspace_bytes(batch: int, max_rows: int, max_len: int, num_heads: int,
-                                 num_kv_heads: int, head_dim: int) -> int:
+                                 num_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
+                                 window: int = 0) -> int:
     """nf4_kv_attention_workspace_bytes on the current device."""
-    return int(_lib().nf4_kv_attention_workspace_bytes(batch, max_rows, max_len, num_heads,
-                                                       num_kv_heads, head_dim))
+    return _lib().nf4_kv_attention_workspace_bytes(batch, max_rows, max_len, num_heads,
+                                                   num_kv_heads, head_dim, _DT[dtype], window)
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -226,7 +235,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
     _check_rows(q, cache, "kv_attention")
     total, heads, d = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _empty_rows(q)
     else:
         _check_rows(out, cache, "kv_attention")
         if out.shape != q.shape or out.dtype != q.dtype or not _strided(out):
@@ -245,12 +254,18 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
     args = (cache.desc, rows, q.data_ptr(), q.stride(0), q.stride(1), heads, _DT[q.dtype],
             d ** -0.5 if scale is None else scale, int(causal), window, max_rows, max_len,
             out.data_ptr(), out.stride(0), out.stride(1))
-    with torch.cuda.device(cache.device):  # the split goes by that device's CUs
+    def run():
         need = kv_attention_workspace_bytes(rows.batch, max_rows, max_len, heads,
-                                            cache.num_kv_heads, d)
+                                            cache.num_kv_heads, d, q.dtype, window)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
         _call(cache, _lib().nf4_kv_attention, "nf4_kv_attention", *args,
               None if ws is None else ws.data_ptr(), max(need, 0))
+
+    if cache.device.index == torch.cuda.current_device():
+        run()
+    else:
+        with torch.cuda.device(cache.device):  # the split goes by that device's CUs
+            run()
     return out
 
 

@@ -108,7 +108,7 @@ nf4_status nf4_kv_read(const nf4_kv_cache *cache, const nf4_kv_rows *rows, int32
  * there: total_rows / batch without row_offsets, the table's capacity for 0. */
 int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_t max_len,
                                          int32_t num_heads, int32_t num_kv_heads,
-                                         int32_t head_dim);
+                                         int32_t head_dim, int32_t dtype, int32_t window);
 
 /* Attention of query rows to the cache. q, out: [total_rows][num_heads][
  * head_dim] of `dtype` with strides as in nf4_kv_write; num_heads is a multiple

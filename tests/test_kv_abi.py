@@ -156,12 +156,15 @@ def test_workspace_query(kv):
                 (1, 1, 1, 8, 3, 128), (1, 1, 1, 0, 8, 128), (1, 1, 1, 8, 0, 128),
                 (1, 1, 1, 8, 8, 100), (70000, 1, 1, 8, 8, 128)):
         assert q(*bad) == -1, bad
+    assert q(1, 1, 1, 8, 8, 128, window=-1) == -1
+    assert kv._lib().nf4_kv_attention_workspace_bytes(1, 1, 1, 8, 8, 128, 3, 0) == -1
     assert q(0, 1, 100, 8, 8, 128) == 0 and q(1, 0, 100, 8, 8, 128) == 0
     assert q(1, 1, 1, 8, 8, 128) == 0
     # a long sequence and few heads is split: fp32 sums of 128 columns and two statistics a row
     n = q(1, 1, 1 << 17, 8, 8, 128)
     assert n > 0 and n % 256 == 0
     assert q(4096, 1, 1 << 17, 8, 8, 128) == 0  # enough sequences: no split
+    assert q(1, 1, 1 << 17, 8, 8, 128, window=100) == 0  # nor for what a window shows
 
 
 def test_binding_refuses_cpu_tensors(kv):
