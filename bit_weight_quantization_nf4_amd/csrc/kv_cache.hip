@@ -5,14 +5,17 @@
 // block of BS elements a = max|x|, s = RN(x / a), the code nearest to s (a tie
 // to the smaller value); a code stands for RN(c[code] a).
 //
-// Layout of the work. A head vector belongs to the 16 lanes of a DPP row: lane
-// m owns elements 32 k + 2 m and + 1 for every k < P = D / 32, which are the P
-// bytes that the cache keeps together for it (nf4_kv.h), so a lane stores (or
-// loads) its codes in one piece and nothing moves between lanes but the block
-// maxima. A wave takes the same head of four neighbouring rows: of one
-// sequence these share the run of 64 P bytes that holds four positions' values.
-// Both kernels are bound by HBM; a lane's 4-byte accesses to the 16-bit rows
-// cover 64 contiguous bytes per head vector and k.
+// Layout of the work. A wave takes the same heads of four neighbouring rows, a DPP
+// row of 16 lanes (j = lane / 4 & 3, i = lane & 3) a head vector. Its 32-element
+// pieces are taken in parts of W = 4, 2 or 1; a lane owns 2 W consecutive elements of
+// a part, so rows move in 16-byte accesses that cover whole lines, and holds their W
+// code bytes. The cache keeps together what lane m = 4 j + i of another arrangement
+// owns, byte m of every piece: the bytes change hands within quads of lanes, by DPP and
+// byte permutes. Four neighbouring positions' values share a run of 64 P bytes.
+//   W = 4: elements 32 (k0 + i) + 8 j ..         W = 1: 32 k0 + 2 m ..
+//   W = 2: elements 32 (k0 + i % 2) + 8 j + 4 (i / 2) ..
+// Both kernels are bound by HBM. A row's place costs a chain of dependent loads, so a
+// wave takes as many heads of it as leave the launch enough waves.
 #include <type_traits>
 
 #include "kv_internal.h"
@@ -113,41 +116,181 @@ __device__ __forceinline__ void load_run(const uint8_t *p, uint32_t (&w)[2]) {
   }
 }
 
-// A pair of neighbouring elements at element offset e (even).
-template <int DT>
-__device__ __forceinline__ void store_pair(void *base, int64_t e, float v0, float v1) {
-  if constexpr (DT == kFP32) {
-    *reinterpret_cast<f32x2 *>(static_cast<float *>(base) + e) = f32x2{v0, v1};
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Part X of P pieces: its first piece and how many.
+template <int P, int X>
+struct Part {
+  static constexpr int K0 = 4 * X;
+  static constexpr int W = P - K0 >= 4 ? 4 : (P - K0 >= 2 ? 2 : 1);
+};
+// P = 3 is 2 + 1, P = 6 is 4 + 2.
+template <>
+struct Part<3, 0> {
+  static constexpr int K0 = 0, W = 2;
+};
+template <>
+struct Part<3, 1> {
+  static constexpr int K0 = 2, W = 1;
+};
+template <int P>
+constexpr int kParts = P == 3 ? 2 : (P + 3) / 4;
+
+// First element of a lane's in a part, and its piece.
+template <int P, int X>
+__device__ __forceinline__ int part_element(int m) {
+  constexpr int K0 = Part<P, X>::K0, W = Part<P, X>::W;
+  const int i = m & 3, j = m >> 2;
+  if (W == 4) return 32 * (K0 + i) + 8 * j;
+  if (W == 2) return 32 * (K0 + (i & 1)) + 8 * j + 4 * (i >> 1);
+  return 32 * K0 + 2 * m;
+}
+template <int P, int X>
+__device__ __forceinline__ int part_piece(int m) {
+  constexpr int K0 = Part<P, X>::K0, W = Part<P, X>::W;
+  return K0 + (W == 4 ? m & 3 : (W == 2 ? m & 1 : 0));
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+
+// W bytes of a lane, one for each m it covers, to W bytes, one for each piece (or
+// back): the exchange is its own inverse. m: lane & 15.
+template <int W>
+__device__ __forceinline__ uint32_t exchange(uint32_t v, int m) {
+  if constexpr (W == 4) {
+    const uint32_t i = (uint32_t)m & 3u;
+    const uint32_t sel = 0x0c0c0400u + 0x0101u * i;
+    const uint32_t q01 = __builtin_amdgcn_perm(dpp<0x55>(v), dpp<0x00>(v), sel);
+    const uint32_t q23 = __builtin_amdgcn_perm(dpp<0xff>(v), dpp<0xaa>(v), sel);
+    return q01 | q23 << 16;
+  } else if constexpr (W == 2) {
+    const uint32_t sel = 0x0c0c0400u + 0x0101u * ((uint32_t)m & 1u);
+    return __builtin_amdgcn_perm(dpp<0xf5>(v), dpp<0xa0>(v), sel);  // lanes 1 1 3 3, 0 0 2 2
   } else {
-    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + e) = pack2<DT>(v0, v1);
+    return v;
   }
 }
 
-// A lane's elements of a head vector as they are stored, and widened.
+// Maximum over the lanes that own a block (PB pieces) of a part with W pieces.
+template <int W, int PB>
+__device__ __forceinline__ float block_max(float v) {
+  auto with = [](float x, uint32_t o) { return fmaxf(x, __uint_as_float(o)); };
+  v = with(v, dpp<0x124>(__float_as_uint(v)));  // row_ror 4, 8: the lanes of equal i
+  v = with(v, dpp<0x128>(__float_as_uint(v)));
+  if (W < 4 || PB == 4) v = with(v, dpp<0x4e>(__float_as_uint(v)));  // quad 2 3 0 1
+  if (W < 2 || PB >= 2) v = with(v, dpp<0xb1>(__float_as_uint(v)));  // quad 1 0 3 2
+  return v;
+}
+
+// The 2 W elements of a lane's in a part as they are stored.
+template <int DT, int W>
+struct Raw {
+  static constexpr int kWords = (DT == kFP32 ? 2 : 1) * W;
+  uint32_t w[kWords];
+};
+
+template <int DT, int W>
+__device__ __forceinline__ void load_raw(Raw<DT, W> &r, const void *base, int64_t e) {
+  const char *p = static_cast<const char *>(base) + e * (DT == kFP32 ? 4 : 2);
+  constexpr int N = Raw<DT, W>::kWords;
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 v = reinterpret_cast<const u32x4 *>(p)[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r.w[4 * i + k] = v[k];
+    }
+  } else if constexpr (N == 2) {
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+    r.w[0] = v[0];
+    r.w[1] = v[1];
+  } else {
+    r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+}
+
+// Written once and not read back here: past the caches' reuse.
+template <int DT, int W>
+__device__ __forceinline__ void store_raw(const Raw<DT, W> &r, void *base, int64_t e) {
+  char *p = static_cast<char *>(base) + e * (DT == kFP32 ? 4 : 2);
+  constexpr int N = Raw<DT, W>::kWords;
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 v = {r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]};
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p) + i);
+    }
+  } else if constexpr (N == 2) {
+    const u32x2 v = {r.w[0], r.w[1]};
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x2 *>(p));
+  } else {
+    __builtin_nontemporal_store(r.w[0], reinterpret_cast<uint32_t *>(p));
+  }
+}
+
+template <int DT, int W>
+__device__ __forceinline__ float element(const Raw<DT, W> &r, int i) {
+  if constexpr (DT == kFP32) return __uint_as_float(r.w[i]);
+  else return widen16<DT>(i & 1 ? r.w[i >> 1] >> 16 : r.w[i >> 1] & 0xffffu);
+}
+
+// Elements 2 i and 2 i + 1.
+template <int DT, int W>
+__device__ __forceinline__ void set_pair(Raw<DT, W> &r, int i, float v0, float v1) {
+  if constexpr (DT == kFP32) {
+    r.w[2 * i] = __float_as_uint(v0);
+    r.w[2 * i + 1] = __float_as_uint(v1);
+  } else {
+    r.w[i] = pack2<DT>(v0, v1);
+  }
+}
+
+// Largest magnitude of a lane's elements; those of 16-bit types order like integers.
+template <int DT, int W>
+__device__ __forceinline__ float largest(const Raw<DT, W> &r) {
+  if constexpr (DT == kFP32) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i) v = fmaxf(v, fabsf(element(r, i)));
+    return v;
+  } else {
+    u16x2 m = __builtin_bit_cast(u16x2, r.w[0] & 0x7fff7fffu);
+#pragma unroll
+    for (int i = 1; i < W; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, r.w[i] & 0x7fff7fffu));
+    return widen16<DT>(m.x > m.y ? m.x : m.y);
+  }
+}
+
+template <int I, int N, typename F>
+__device__ __forceinline__ void unroll(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unroll<I + 1, N>(static_cast<F &&>(f));
+  }
+}
+
+// All parts of a head vector.
 template <int DT, int P>
-struct Pieces {
-  typename std::conditional<DT == kFP32, f32x2, uint32_t>::type v[P];
+struct Row {
+  Raw<DT, Part<P, 0>::W> a;
+  Raw<DT, Part<P, kParts<P> - 1>::W> b;  // the second part, where there is one
+  template <int X>
+  __device__ __forceinline__ auto &part() {
+    if constexpr (X == 0) return a;
+    else return b;
+  }
 };
 
 template <int DT, int P>
-__device__ __forceinline__ void load_row(Pieces<DT, P> &p, const void *base, int64_t e) {
-#pragma unroll
-  for (int k = 0; k < P; ++k) {
-    if constexpr (DT == kFP32)
-      p.v[k] = *reinterpret_cast<const f32x2 *>(static_cast<const float *>(base) + e + 32 * k);
-    else
-      p.v[k] =
-          *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + e + 32 * k);
-  }
-}
-
-template <int DT, int P>
-__device__ __forceinline__ void widen(f32x2 (&x)[P], const Pieces<DT, P> &p) {
-#pragma unroll
-  for (int k = 0; k < P; ++k) {
-    if constexpr (DT == kFP32) x[k] = p.v[k];
-    else x[k] = f32x2{widen16<DT>(p.v[k] & 0xffffu), widen16<DT>(p.v[k] >> 16)};
-  }
+__device__ __forceinline__ void load_row(Row<DT, P> &r, const void *base, int64_t e, int m) {
+  unroll<0, kParts<P>>([&](auto x) {
+    load_raw(r.template part<x>(), base, e + part_element<P, x>(m));
+  });
 }
 
 // The rows and heads of a job; consecutive jobs take keys and values of the same.
@@ -171,22 +314,57 @@ constexpr int kInFlight = 4;
 
 // RN(x / a) given r = RN(1 / a): one product and one residual step (Markstein),
 // correctly rounded while a, r and the residual stay normal (a in [2^-100,
-// 2^120); a quotient so small that it does not lies in zero's cell anyway).
+// 2^120); a quotient so small that it does not lies in zero's cell anyway). For
+// bf16 x and a the product alone gives the same NF4 code, shown for every pair
+// (quantize.hip).
+template <bool PRODUCT>
 __device__ __forceinline__ float quotient(float x, float a, float r) {
   const float q = x * r;
+  if (PRODUCT) return q;
   return __builtin_fmaf(__builtin_fmaf(-q, a, x), r, q);
 }
 
-template <int D, int BS, int DT>
+// Lookup of s: its cell's entry (threshold, and the codes on either side as in
+// cell_of) and, 64 entries on, the values of these codes. Byte J of `codes` becomes
+// the code in the nibble that SRC selects (2: high, 0: low), `value` its value. J = 0
+// of the first in a byte clears the others.
+template <int J, int SRC>
+__device__ __forceinline__ void encode(uint32_t &codes, float &value, float s, const uint2 *lut) {
+  const float t = __builtin_fmaf(s, 128.0f, 8388736.0f);  // 2^23 + 128
+  const uint2 *entry = reinterpret_cast<const uint2 *>(reinterpret_cast<const char *>(lut) +
+                                                       (__float_as_uint(t) & 0x1f8u));
+  const uint2 e = entry[0], v = entry[kLutSize];
+  if constexpr (J == 0) {
+    asm("v_cmp_gt_f32 vcc, %2, %3\n\t"
+        "s_nop 1\n\t"
+        "v_cndmask_b32_sdwa %0, %4, %4, vcc dst_sel:BYTE_0 dst_unused:UNUSED_PAD "
+        "src0_sel:BYTE_%7 src1_sel:BYTE_%8\n\t"
+        "v_cndmask_b32 %1, %5, %6, vcc"
+        : "=&v"(codes), "=v"(value)
+        : "v"(s), "v"(e.x), "v"(e.y), "v"(v.x), "v"(v.y), "n"(SRC), "n"(SRC + 1)
+        : "vcc");
+  } else {
+    asm("v_cmp_gt_f32 vcc, %2, %3\n\t"
+        "s_nop 1\n\t"
+        "v_cndmask_b32_sdwa %0, %4, %4, vcc dst_sel:BYTE_%9 dst_unused:UNUSED_PRESERVE "
+        "src0_sel:BYTE_%7 src1_sel:BYTE_%8\n\t"
+        "v_cndmask_b32 %1, %5, %6, vcc"
+        : "+&v"(codes), "=v"(value)
+        : "v"(s), "v"(e.x), "v"(e.y), "v"(v.x), "v"(v.y), "n"(SRC), "n"(SRC + 1), "n"(J)
+        : "vcc");
+  }
+}
+
+template <int D, int BS, int DT, bool PRODUCT>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvRowsArgs args) {
   constexpr int P = D / 32, NB = D / BS, PB = BS / 32;  // pieces of a row, blocks, pieces a block
-  __shared__ uint2 lut[kLutSize];
-  __shared__ float value[16];
+  __shared__ uint2 lut[2 * kLutSize];
   if (threadIdx.x < kLutSize) {
     const int c = threadIdx.x < kCells ? threadIdx.x : kCells - 1;
-    lut[threadIdx.x] = make_uint2(__float_as_uint(args.cell_thr[c]), args.cell_codes[c]);
-  } else if (threadIdx.x < kLutSize + 16) {
-    value[threadIdx.x - kLutSize] = args.value[threadIdx.x - kLutSize];
+    const uint32_t codes = args.cell_codes[c];
+    lut[threadIdx.x] = make_uint2(__float_as_uint(args.cell_thr[c]), codes);
+    lut[kLutSize + threadIdx.x] = make_uint2(__float_as_uint(args.value[codes & 15]),
+                                             __float_as_uint(args.value[codes >> 8 & 15]));
   }
   __syncthreads();
   const KvArgs &kv = args.kv;
@@ -197,70 +375,62 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvRowsArgs args) {
   for (int64_t job = wave; job < args.jobs; job += nwaves) {
     const Job j = job_of(args, job);
     const int64_t row = j.row_group * 4 + (lane >> 4);
-    // rows past the last take its values and have no place
+    // rows past the last take its elements and have no place
     const int64_t from = row < kv.total_rows ? row : kv.total_rows - 1;
     const void *in = args.in[j.which];
-    Pieces<DT, P> next;
-    load_row(next, in, from * args.row_stride + j.head0 * args.head_stride + 2 * m);
+    Row<DT, P> next;
+    load_row<DT, P>(next, in, from * args.row_stride + j.head0 * args.head_stride, m);
     const RowPlace place =
         row < kv.total_rows ? place_of(kv, (int)row) : RowPlace{false, false, 0, 0};
     const bool values = args.out[0] != nullptr && place.in_call;
     for (int h = j.head0; h < j.head1; ++h) {
-      f32x2 x[P];
-      widen(x, next);
+      Row<DT, P> x = next;
       // the next head's elements are on their way while this one's are encoded
       const int hn = h + 1 < j.head1 ? h + 1 : h;
-      load_row(next, in, from * args.row_stride + hn * args.head_stride + 2 * m);
+      load_row<DT, P>(next, in, from * args.row_stride + hn * args.head_stride, m);
 
-      float a[NB], as[NB], r[NB];
-      int sh[NB];
-      bool normal = true;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float v = 0.0f;
-#pragma unroll
-        for (int k = b * PB; k < (b + 1) * PB; ++k)
-          v = fmaxf(v, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
-        a[b] = row16_max(v);
-        normal = normal && a[b] >= 0x1p-100f && a[b] < 0x1p120f;
-      }
-      // outside that range x and a are first scaled by the power of two that
-      // brings a into [1, 2): the quotient is the same. One branch for the wave.
-      const bool scaled = __builtin_amdgcn_ballot_w64(!normal) != 0;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        as[b] = a[b];
-        sh[b] = 0;
-        if (scaled && a[b] > 0.0f) {
-          sh[b] = 1 - __builtin_amdgcn_frexp_expf(a[b]);
-          as[b] = __builtin_amdgcn_ldexpf(a[b], sh[b]);
+      uint32_t run[2] = {0, 0};
+      unroll<0, kParts<P>>([&](auto xc) {
+        constexpr int X = xc, K0 = Part<P, X>::K0, W = Part<P, X>::W;
+        auto &raw = x.template part<X>();
+        const float a = block_max<W, PB>(largest(raw));
+        // outside [2^-100, 2^120) x and a are first scaled by the power of two that
+        // brings a into [1, 2): the quotient is the same. One branch for the wave.
+        float as = a;
+        int sh = 0;
+        const bool scaled = __builtin_amdgcn_ballot_w64(!(a >= 0x1p-100f && a < 0x1p120f)) != 0;
+        if (scaled && a > 0.0f) {
+          sh = 1 - __builtin_amdgcn_frexp_expf(a);
+          as = __builtin_amdgcn_ldexpf(a, sh);
         }
-        r[b] = as[b] == 0.0f ? 0.0f : 1.0f / as[b];
-      }
-      uint32_t w[2] = {0, 0};
-      const int64_t ve = (row * kv.kv_heads + h) * D + 2 * m;
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int b = k / PB;
-        float x0 = x[k].x, x1 = x[k].y;
-        if (scaled) {
-          x0 = __builtin_amdgcn_ldexpf(x0, sh[b]);
-          x1 = __builtin_amdgcn_ldexpf(x1, sh[b]);
-        }
-        const uint32_t c0 = code_of(quotient(x0, as[b], r[b]), lut);
-        const uint32_t c1 = code_of(quotient(x1, as[b], r[b]), lut);
-        w[k >> 2] |= (c0 << 4 | c1) << (8 * (k & 3));
-        if (values) store_pair<DT>(args.out[j.which], ve + 32 * k, value[c0] * a[b], value[c1] * a[b]);
-      }
-      if (place.in_cache) {
-        store_run<P>(kv.packed[j.which] + run_offset<P>(kv, place, h, j.which, m), w);
-        float mine = a[0];
-#pragma unroll
-        for (int b = 1; b < NB; ++b) mine = m == b ? a[b] : mine;
-        if (m < NB)
+        const float r = as == 0.0f ? 0.0f : 1.0f / as;
+        uint32_t high, low;  // the codes of the even and of the odd elements
+        Raw<DT, W> out;
+        unroll<0, W>([&](auto ic) {
+          constexpr int I = ic;
+          float x0 = element(raw, 2 * I), x1 = element(raw, 2 * I + 1);
+          if (scaled) {
+            x0 = __builtin_amdgcn_ldexpf(x0, sh);
+            x1 = __builtin_amdgcn_ldexpf(x1, sh);
+          }
+          float v0, v1;
+          encode<I, 2>(high, v0, quotient<PRODUCT>(x0, as, r), lut);
+          encode<I, 0>(low, v1, quotient<PRODUCT>(x1, as, r), lut);
+          set_pair(out, I, v0 * a, v1 * a);
+        });
+        if (values)
+          store_raw(out, args.out[j.which], (row * kv.kv_heads + h) * D + part_element<P, X>(m));
+        const uint32_t bytes = exchange<W>(high | low, m);
+        run[K0 >> 2] |= bytes << (8 * (K0 & 3));
+        // a block's scale from the first of its lanes
+        const int piece = part_piece<P, X>(m);
+        const bool first = W == 1 ? m == 0 : (W == 2 ? m < 2 : m < 4);
+        if (place.in_cache && first && piece % PB == 0)
           kv.absmax[j.which][place.page * kv.absmax_stride +
-                           ((int64_t)h * kv.page_size + place.at) * NB + m] = mine;
-      }
+                             ((int64_t)h * kv.page_size + place.at) * NB + piece / PB] = a;
+      });
+      if (place.in_cache)
+        store_run<P>(kv.packed[j.which] + run_offset<P>(kv, place, h, j.which, m), run);
     }
   }
 }
@@ -279,41 +449,44 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRowsArgs args) {
   for (int64_t job = wave; job < args.jobs; job += nwaves) {
     const Job j = job_of(args, job);
     const int64_t row = j.row_group * 4 + (lane >> 4);
-    if (row >= kv.total_rows) continue;
-    const RowPlace place = place_of(kv, (int)row);
-    if (!place.in_call) continue;
+    const RowPlace place =
+        row < kv.total_rows ? place_of(kv, (int)row) : RowPlace{false, false, 0, 0};
     void *out = args.out[j.which];
-    if (!place.in_cache) {
-      for (int h = j.head0; h < j.head1; ++h)
-#pragma unroll
-        for (int k = 0; k < P; ++k)
-          store_pair<DT>(out, row * args.row_stride + h * args.head_stride + 2 * m + 32 * k, 0.0f,
-                         0.0f);
-      continue;
-    }
-    // kInFlight heads' codes and scales a time
+    // kInFlight heads' codes and scales a time; lanes without a place hold zeros
     for (int h0 = j.head0; h0 < j.head1; h0 += kInFlight) {
-      uint32_t w[kInFlight][2];
-      float a[kInFlight][NB];
+      uint32_t run[kInFlight][2];
+      float a[kInFlight][kParts<P>];
 #pragma unroll
       for (int u = 0; u < kInFlight; ++u) {
         const int h = h0 + u < j.head1 ? h0 + u : j.head1 - 1;
-        load_run<P>(kv.packed[j.which] + run_offset<P>(kv, place, h, j.which, m), w[u]);
-        const float *s = kv.absmax[j.which] + place.page * kv.absmax_stride +
-                         ((int64_t)h * kv.page_size + place.at) * NB;
+        run[u][0] = run[u][1] = 0;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) a[u][b] = s[b];
+        for (int x = 0; x < kParts<P>; ++x) a[u][x] = 0.0f;
+        if (place.in_cache) {
+          load_run<P>(kv.packed[j.which] + run_offset<P>(kv, place, h, j.which, m), run[u]);
+          const float *s = kv.absmax[j.which] + place.page * kv.absmax_stride +
+                           ((int64_t)h * kv.page_size + place.at) * NB;
+          unroll<0, kParts<P>>([&](auto x) { a[u][x] = s[part_piece<P, x>(m) / PB]; });
+        }
       }
 #pragma unroll
       for (int u = 0; u < kInFlight; ++u) {
         if (h0 + u >= j.head1) break;
-        const int64_t e = row * args.row_stride + (h0 + u) * args.head_stride + 2 * m;
+        unroll<0, kParts<P>>([&](auto xc) {
+          constexpr int X = xc, K0 = Part<P, X>::K0, W = Part<P, X>::W;
+          const uint32_t bytes = exchange<W>(run[u][K0 >> 2] >> (8 * (K0 & 3)), m);
+          Raw<DT, W> r;
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          const uint32_t byte = w[u][k >> 2] >> (8 * (k & 3)) & 0xffu;
-          store_pair<DT>(out, e + 32 * k, value[byte >> 4] * a[u][k / PB],
-                         value[byte & 15] * a[u][k / PB]);
-        }
+          for (int i = 0; i < W; ++i) {
+            const uint32_t byte = bytes >> (8 * i) & 0xffu;
+            const float v0 = value[byte >> 4] * a[u][X], v1 = value[byte & 15] * a[u][X];
+            // code 0 is not the value 0
+            set_pair(r, i, place.in_cache ? v0 : 0.0f, place.in_cache ? v1 : 0.0f);
+          }
+          if (place.in_call)
+            store_raw(r, out, row * args.row_stride + (h0 + u) * args.head_stride +
+                                  part_element<P, X>(m));
+        });
       }
     }
   }
@@ -332,8 +505,6 @@ KvRowsArgs make_args(const KvArgs &kv, const KvShape &sh) {
   }
   a.in[0] = a.in[1] = nullptr;
   a.out[0] = a.out[1] = nullptr;
-  // A row's place costs a chain of dependent loads, so a wave takes as many heads
-  // of it as leave the launch kJobsWanted waves.
   const int64_t row_groups = ((int64_t)kv.total_rows + 3) / 4;
   int heads = 1;
   while (heads < kv.kv_heads &&
@@ -346,22 +517,27 @@ KvRowsArgs make_args(const KvArgs &kv, const KvShape &sh) {
 }
 
 template <bool WRITE, int D, int BS, int DT>
-void launch_cfg(const KvRowsArgs &a, hipStream_t stream) {
+void launch_cfg(const KvRowsArgs &a, bool nf4, hipStream_t stream) {
   int64_t blocks = (a.jobs + kWaves - 1) / kWaves;
   if (blocks > 16384) blocks = 16384;
-  if constexpr (WRITE)
-    hipLaunchKernelGGL((kv_write_kernel<D, BS, DT>), dim3((unsigned)blocks), dim3(kThreads), 0,
-                       stream, a);
-  else
-    hipLaunchKernelGGL((kv_read_kernel<D, BS, DT>), dim3((unsigned)blocks), dim3(kThreads), 0,
-                       stream, a);
+  const dim3 grid((unsigned)blocks), block(kThreads);
+  if constexpr (!WRITE) {
+    hipLaunchKernelGGL((kv_read_kernel<D, BS, DT>), grid, block, 0, stream, a);
+  } else if constexpr (DT == kBF16) {
+    if (nf4) hipLaunchKernelGGL((kv_write_kernel<D, BS, DT, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((kv_write_kernel<D, BS, DT, false>), grid, block, 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((kv_write_kernel<D, BS, DT, false>), grid, block, 0, stream, a);
+  }
 }
 
 template <bool WRITE, int D, int BS>
-hipError_t launch_dt(const KvRowsArgs &a, int dtype, hipStream_t stream) {
-  if (dtype == kFP32) launch_cfg<WRITE, D, BS, kFP32>(a, stream);
-  else if (dtype == kFP16) launch_cfg<WRITE, D, BS, kFP16>(a, stream);
-  else launch_cfg<WRITE, D, BS, kBF16>(a, stream);
+hipError_t launch_dt(const KvRowsArgs &a, const KvShape &sh, hipStream_t stream) {
+  const bool nf4 = sh.quant_type == kQuantNF4;
+  const int dtype = sh.dtype;
+  if (dtype == kFP32) launch_cfg<WRITE, D, BS, kFP32>(a, nf4, stream);
+  else if (dtype == kFP16) launch_cfg<WRITE, D, BS, kFP16>(a, nf4, stream);
+  else launch_cfg<WRITE, D, BS, kBF16>(a, nf4, stream);
   return hipGetLastError();
 }
 
@@ -369,7 +545,7 @@ template <bool WRITE>
 hipError_t launch_shape(const KvRowsArgs &a, const KvShape &sh, hipStream_t stream) {
   switch (sh.head_dim * 1000 + sh.blocksize) {
 #define NF4_KV_CASE(DV, BSV) \
-  case DV * 1000 + BSV: return launch_dt<WRITE, DV, BSV>(a, sh.dtype, stream);
+  case DV * 1000 + BSV: return launch_dt<WRITE, DV, BSV>(a, sh, stream);
     NF4_KV_CASE(64, 32)
     NF4_KV_CASE(64, 64)
     NF4_KV_CASE(96, 32)
