@@ -71,33 +71,39 @@ class KVCache:
 
     def __init__(self, k_packed: torch.Tensor, k_absmax: torch.Tensor, v_packed: torch.Tensor,
                  v_absmax: torch.Tensor, blocksize: int = 64, quant_type: str = "nf4"):
-        if k_packed.dim() != 4 or k_packed.dtype != torch.uint8 or v_packed.dtype != torch.uint8:
+        shape, stride = k_packed.shape, k_packed.stride()
+        sshape, sstride = k_absmax.shape, k_absmax.stride()
+        if len(shape) != 4 or k_packed.dtype is not torch.uint8 or \
+                v_packed.dtype is not torch.uint8:
             raise ValueError("KVCache expects uint8 codes [pages, kv heads, page_size, head_dim / 2]")
-        shape, stride, sstride = k_packed.shape, k_packed.stride(), k_absmax.stride()
         pages, heads, page_size, half = shape
         nb = 2 * half // blocksize if blocksize > 0 else 0
         if v_packed.shape != shape or v_packed.stride() != stride or (
                 pages and stride[1:] != (page_size * half, half, 1)):
             raise ValueError("KVCache expects codes of one shape, contiguous in a page")
-        if k_absmax.dtype != torch.float32 or v_absmax.dtype != torch.float32 or \
-                k_absmax.shape != (pages, heads, page_size, nb) or \
-                v_absmax.shape != k_absmax.shape or v_absmax.stride() != sstride or (
+        if k_absmax.dtype is not torch.float32 or v_absmax.dtype is not torch.float32 or \
+                sshape != (pages, heads, page_size, nb) or \
+                v_absmax.shape != sshape or v_absmax.stride() != sstride or (
                     pages and sstride[1:] != (page_size * nb, nb, 1)):
             raise ValueError("KVCache expects fp32 scales [pages, kv heads, page_size, "
                              "head_dim / blocksize], contiguous in a page")
-        dev = k_packed.device
-        if dev.type != "cuda" or k_absmax.device != dev or v_packed.device != dev or \
-                v_absmax.device != dev:
+        index = k_packed.get_device()
+        if index < 0 or k_absmax.get_device() != index or v_packed.get_device() != index or \
+                v_absmax.get_device() != index:
             raise TypeError("KVCache expects four tensors on one GPU")
         self.k_packed, self.k_absmax = k_packed, k_absmax
         self.v_packed, self.v_absmax = v_packed, v_absmax
         self.blocksize, self.quant_type = blocksize, quant_type
         self.num_pages, self.num_kv_heads, self.page_size = pages, heads, page_size
         self.head_dim = 2 * half
-        self.device = dev
+        self.index = index  # of the GPU
         self.desc = KVCacheDesc(k_packed.data_ptr(), k_absmax.data_ptr(), v_packed.data_ptr(),
-                                v_absmax.data_ptr(), pages, stride[0], sstride[0],
-                                page_size, heads, 2 * half, blocksize, _QT[quant_type])
+                                v_absmax.data_ptr(), pages, stride[0], sstride[0], page_size, heads,
+                                2 * half, blocksize, _QT[quant_type])
+
+    @property
+    def device(self) -> torch.device:
+        return self.k_packed.device
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
@@ -115,32 +121,33 @@ class KVCache:
 
 
 def _rows(cache: KVCache, total: int, block_table, kv_lens, row_offsets, what: str) -> KVRowsDesc:
-    if block_table.dtype != torch.int32 or kv_lens.dtype != torch.int32 or \
+    int32 = torch.int32
+    if block_table.dtype is not int32 or kv_lens.dtype is not int32 or \
             block_table.dim() != 2 or kv_lens.dim() != 1:
         raise TypeError(f"{what} expects int32 block_table [batch, pages] and kv_lens [batch]")
     batch, cols = block_table.shape
+    stride, inner = block_table.stride()
     if kv_lens.shape[0] != batch or not kv_lens.is_contiguous() or \
-            (cols > 1 and block_table.stride(1) != 1) or \
-            (batch > 1 and block_table.stride(0) < cols):
+            (cols > 1 and inner != 1) or (batch > 1 and stride < cols):
         raise ValueError(f"{what}: block_table needs unit column stride, kv_lens [batch]")
-    if block_table.device != cache.device or kv_lens.device != cache.device:
+    index = cache.index
+    if block_table.get_device() != index or kv_lens.get_device() != index:
         raise TypeError(f"{what} expects every tensor on the cache's GPU")
     off = None
     if row_offsets is not None:
-        if row_offsets.dtype != torch.int32 or row_offsets.shape != (batch + 1,) or \
-                not row_offsets.is_contiguous() or row_offsets.device != cache.device:
+        if row_offsets.dtype is not int32 or row_offsets.shape != (batch + 1,) or \
+                not row_offsets.is_contiguous() or row_offsets.get_device() != index:
             raise ValueError(f"{what} expects int32 row_offsets [batch + 1] on the cache's GPU")
         off = row_offsets.data_ptr()
     return KVRowsDesc(block_table.data_ptr(), kv_lens.data_ptr(), off,
-                      block_table.stride(0) if batch > 1 else cols, cols, batch, total)
+                      stride if batch > 1 else cols, cols, batch, total)
 
 
 def _strided(t: torch.Tensor) -> bool:
     """Whether the ABI takes [rows, heads, head_dim] as it is."""
-    es, (r, h, e) = t.element_size(), t.stride()
-    d = t.shape[2]
-    return (e == 1 and r >= d and h >= d and r * es % 16 == 0 and h * es % 16 == 0
-            and t.data_ptr() % 16 == 0)
+    r, h, e = t.stride()
+    d, es = t.shape[2], t.element_size()
+    return (e == 1 and r >= d and h >= d and not (r * es | h * es | t.data_ptr()) & 15)
 
 
 def _empty_rows(t: torch.Tensor) -> torch.Tensor:
@@ -148,7 +155,7 @@ def _empty_rows(t: torch.Tensor) -> torch.Tensor:
 
 
 def _check_rows(t: torch.Tensor, cache: KVCache, what: str) -> None:
-    if t.dtype not in _DT or t.device != cache.device:
+    if t.dtype not in _DT or t.get_device() != cache.index:
         raise TypeError(f"{what} expects bf16 / fp16 / fp32 rows on the cache's GPU")
     if t.dim() != 3 or t.shape[2] != cache.head_dim:
         raise ValueError(f"{what} expects rows [rows, heads, head_dim]")
@@ -159,16 +166,20 @@ def _aligned_copy(t: torch.Tensor) -> torch.Tensor:
     return t.clone() if t.data_ptr() % 16 else t
 
 
-def _call(cache: KVCache, fn, name: str, *args) -> None:
-    """fn(*args, stream) on the cache's device and that device's current stream."""
-    index = cache.device.index
-    # the raw handle: building a Stream object takes longer than the launch
-    stream = torch._C._cuda_getCurrentRawStream(index)
+# the raw handle of a device's current stream: building a Stream object takes longer
+# than the launch itself
+_stream_of = torch._C._cuda_getCurrentRawStream
+
+
+def _call(cache: KVCache, run) -> None:
+    """run(stream) -> (status, name) with the cache's device current, on its current
+    stream."""
+    index = cache.index
     if index == torch.cuda.current_device():
-        status = fn(*args, stream)
+        status, name = run(_stream_of(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, stream)
+            status, name = run(_stream_of(index))
     if status:
         _check(status, name)
 
@@ -186,9 +197,11 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torc
         k, v = _aligned_copy(k), _aligned_copy(v)
     rows = _rows(cache, k.shape[0], block_table, kv_lens, row_offsets, "kv_write")
     kq, vq = (_empty_rows(k), _empty_rows(k)) if values else (None, None)
-    _call(cache, _lib().nf4_kv_write, "nf4_kv_write", cache.desc, rows, k.data_ptr(), v.data_ptr(),
-          k.stride(0), k.stride(1), _DT[k.dtype], kq.data_ptr() if values else None,
-          vq.data_ptr() if values else None)
+    rs, hs, _ = k.stride()
+    _call(cache, lambda stream: (_lib().nf4_kv_write(
+        cache.desc, rows, k.data_ptr(), v.data_ptr(), rs, hs, _DT[k.dtype],
+        kq.data_ptr() if values else None, vq.data_ptr() if values else None, stream),
+        "nf4_kv_write"))
     return (kq, vq) if values else None
 
 
@@ -197,19 +210,25 @@ def kv_read(cache: KVCache, rows: int, block_table: torch.Tensor, kv_lens: torch
     """nf4_kv_read: the last positions of each sequence, ``rows`` in all, as (k, v)
     [rows, kv heads, head_dim] (or into the pair ``out``). Rows behind the last
     offset are left as they are: unspecified without ``out``."""
+    shape = (rows, cache.num_kv_heads, cache.head_dim)
     if out is None:
-        shape = (rows, cache.num_kv_heads, cache.head_dim)
-        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
-    k, v = out
-    for t in out:
-        _check_rows(t, cache, "kv_read")
-        if t.shape != (rows, cache.num_kv_heads, cache.head_dim) or t.dtype != k.dtype or \
-                t.stride() != k.stride() or not _strided(t):
-            raise ValueError("kv_read: out must be two [rows, kv heads, head_dim] tensors of one "
-                             "dtype and layout, with 16-byte aligned heads")
+        if dtype not in _DT:
+            raise TypeError("kv_read gives bf16, fp16 or fp32")
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+        for t in out:
+            _check_rows(t, cache, "kv_read")
+            if t.shape != shape or t.dtype != k.dtype or t.stride() != k.stride() or \
+                    not _strided(t):
+                raise ValueError("kv_read: out must be two [rows, kv heads, head_dim] tensors of "
+                                 "one dtype and layout, with 16-byte aligned heads")
     desc = _rows(cache, rows, block_table, kv_lens, row_offsets, "kv_read")
-    _call(cache, _lib().nf4_kv_read, "nf4_kv_read", cache.desc, desc, _DT[k.dtype], k.data_ptr(),
-          v.data_ptr(), k.stride(0), k.stride(1))
+    rs, hs, _ = k.stride()
+    _call(cache, lambda stream: (_lib().nf4_kv_read(
+        cache.desc, desc, _DT[k.dtype], k.data_ptr(), v.data_ptr(), rs, hs, stream),
+        "nf4_kv_read"))
     return k, v
 
 
@@ -251,21 +270,21 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
         max_rows = total
     if max_len <= 0:
         max_len = min(rows.table_cols * cache.page_size, 0x7fff0000)
-    args = (cache.desc, rows, q.data_ptr(), q.stride(0), q.stride(1), heads, _DT[q.dtype],
-            d ** -0.5 if scale is None else scale, int(causal), window, max_rows, max_len,
-            out.data_ptr(), out.stride(0), out.stride(1))
-    def run():
-        need = kv_attention_workspace_bytes(rows.batch, max_rows, max_len, heads,
-                                            cache.num_kv_heads, d, q.dtype, window)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-        _call(cache, _lib().nf4_kv_attention, "nf4_kv_attention", *args,
-              None if ws is None else ws.data_ptr(), max(need, 0))
+    qr, qh, _ = q.stride()
+    orow, ohead, _ = out.stride()
+    kv_heads, dt = cache.num_kv_heads, _DT[q.dtype]
 
-    if cache.device.index == torch.cuda.current_device():
-        run()
-    else:
-        with torch.cuda.device(cache.device):  # the split goes by that device's CUs
-            run()
+    def run(stream):
+        lib = _lib()
+        need = lib.nf4_kv_attention_workspace_bytes(rows.batch, max_rows, max_len, heads, kv_heads,
+                                                    d, dt, window)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        return lib.nf4_kv_attention(
+            cache.desc, rows, q.data_ptr(), qr, qh, heads, dt, d ** -0.5 if scale is None else scale,
+            int(causal), window, max_rows, max_len, out.data_ptr(), orow, ohead,
+            None if ws is None else ws.data_ptr(), max(need, 0), stream), "nf4_kv_attention"
+
+    _call(cache, run)
     return out
 
 
