@@ -425,16 +425,15 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   };
   // pages (and tiles within them) of a step's two 16-position tiles
   struct Where { uint32_t page[2]; int at[2]; };
+  // (both loaded always: a page id copied here would have to be waited for here)
   auto locate = [&] {
+    const bool turn = in_page + 1 == tiles_per_page;
+    const int col1 = turn ? col + 1 : col;
     Where w;
     w.page[0] = (uint32_t)table[col];
+    w.page[1] = (uint32_t)table[col1 < last_col ? col1 : last_col];
     w.at[0] = in_page;
-    w.page[1] = w.page[0];
-    w.at[1] = in_page + 1;
-    if (!paired && in_page + 1 == tiles_per_page) {
-      w.page[1] = (uint32_t)table[col < last_col ? col + 1 : last_col];
-      w.at[1] = 0;
-    }
+    w.at[1] = turn ? 0 : in_page + 1;
     return w;
   };
   // where the tiles' codes and scales lie; a page that is not there is read as the
@@ -446,16 +445,17 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   };
   auto places_of = [&](const Where &w) {
     Places p;
-    uint64_t codes, scales;
+    uint64_t codes = 0, scales = 0;
+    // both pages are looked at here, so that neither load sinks into the branch below
+    p.ok[0] = w.page[0] < num_pages;
+    p.ok[1] = w.page[1] < num_pages;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (t == 0 || !paired) {
-        p.ok[t] = w.page[t] < num_pages;
         const uint32_t page = p.ok[t] ? w.page[t] : 0;
         codes = ((uint64_t)page * packed_units + (uint32_t)(w.at[t] * (16 * P))) << 4;
         scales = (uint64_t)page * absmax_units + (uint32_t)(w.at[t] * (16 * NB));
       } else {
-        p.ok[1] = p.ok[0];
         codes += 256 * P;
         scales += 16 * NB;
       }
