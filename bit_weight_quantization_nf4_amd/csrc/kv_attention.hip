@@ -126,11 +126,11 @@ Plan plan_of(const KvAttentionSizes &z) {
   int64_t s = 1;
   if (span * weight >= kSplitFrom * 128) {
     const int64_t want = 2 * (int64_t)device_cu_count();
-    s = items > 0 ? ceil_div(want, items) : 1;
+    // waves that merge leave room for uneven items; those apart fill what there is
+    s = items > 0 ? (p.merge ? ceil_div(want, items) : want / items) : 1;
     const int64_t least = p.merge ? kMinRange * 128 / weight : kMinRangeApart;
     const int64_t most = ceil_div(span, least > 0 ? least : 1);
     if (s > most) s = most;
-    if (!p.merge && items >= want / 2) s = 1;
   }
   if (s < 1) s = 1;
   p.splits = (int)s;

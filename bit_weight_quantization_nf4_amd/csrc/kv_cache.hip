@@ -310,7 +310,7 @@ __device__ __forceinline__ Job job_of(const KvRowsArgs &args, int64_t job) {
 }
 
 // Heads whose codes a reading wave has in flight.
-constexpr int kInFlight = 4;
+constexpr int kInFlight = 8;
 
 // RN(x / a) given r = RN(1 / a): one product and one residual step (Markstein),
 // correctly rounded while a, r and the residual stay normal (a in [2^-100,
