@@ -18,6 +18,15 @@ arithmetic of the method runs in Python:
   nf4::linear(Tensor x, packed, absmax, absmax_q, absmax_scale, absmax_offset,
       Tensor? bias, int N, int K, int blocksize, str quant_type,
       int double_quant) -> Tensor
+  nf4::kv_write(Tensor k, v, k_packed(a!), k_absmax(b!), v_packed(c!), v_absmax(d!),
+      block_table, kv_lens, Tensor? row_offsets, int blocksize, str quant_type) -> ()
+  nf4::kv_write_values(...) -> (k_values, v_values): the same, and what the cache holds
+  nf4::kv_read(Tensor k_packed, k_absmax, v_packed, v_absmax, block_table, kv_lens,
+      Tensor? row_offsets, int rows, int blocksize, str quant_type, ScalarType dtype)
+      -> (k, v)
+  nf4::kv_attention(Tensor q, k_packed, k_absmax, v_packed, v_absmax, block_table,
+      kv_lens, Tensor? row_offsets, int blocksize, str quant_type, int max_rows,
+      int max_len, float? scale, bool causal, int window) -> Tensor
 Scale tensors a double-quant mode does not use are passed as empty tensors.
 Each operator has a fake (meta) implementation for tracing. The operators
 are inference operators: no autograd formula is registered.
@@ -29,8 +38,9 @@ import math
 import torch
 from torch import nn
 
-from . import QuantState, _dq, dequantize as _dequantize, linear as _linear, \
-    quantize as _quantize
+from . import KVCache, QuantState, _dq, dequantize as _dequantize, \
+    kv_attention as _kv_attention, kv_read as _kv_read, kv_write as _kv_write, \
+    linear as _linear, quantize as _quantize
 
 
 def _state(packed, absmax, absmax_q, absmax_scale, absmax_offset, shape, blocksize, quant_type,
@@ -100,6 +110,73 @@ def linear_op(x: torch.Tensor, packed: torch.Tensor, absmax: torch.Tensor,
 def _(x, packed, absmax, absmax_q, absmax_scale, absmax_offset, bias, N, K, blocksize,
       quant_type, double_quant):
     return x.new_empty((*x.shape[:-1], N))
+
+
+@torch.library.custom_op("nf4::kv_write",
+                         mutates_args=("k_packed", "k_absmax", "v_packed", "v_absmax"))
+def kv_write_op(k: torch.Tensor, v: torch.Tensor, k_packed: torch.Tensor, k_absmax: torch.Tensor,
+                v_packed: torch.Tensor, v_absmax: torch.Tensor, block_table: torch.Tensor,
+                kv_lens: torch.Tensor, row_offsets: torch.Tensor | None, blocksize: int,
+                quant_type: str) -> None:
+    _kv_write(KVCache(k_packed, k_absmax, v_packed, v_absmax, blocksize, quant_type), k, v,
+              block_table, kv_lens, row_offsets)
+
+
+@kv_write_op.register_fake
+def _(k, v, k_packed, k_absmax, v_packed, v_absmax, block_table, kv_lens, row_offsets, blocksize,
+      quant_type):
+    return None
+
+
+@torch.library.custom_op("nf4::kv_write_values",
+                         mutates_args=("k_packed", "k_absmax", "v_packed", "v_absmax"))
+def kv_write_values_op(k: torch.Tensor, v: torch.Tensor, k_packed: torch.Tensor,
+                       k_absmax: torch.Tensor, v_packed: torch.Tensor, v_absmax: torch.Tensor,
+                       block_table: torch.Tensor, kv_lens: torch.Tensor,
+                       row_offsets: torch.Tensor | None, blocksize: int,
+                       quant_type: str) -> tuple[torch.Tensor, torch.Tensor]:
+    return _kv_write(KVCache(k_packed, k_absmax, v_packed, v_absmax, blocksize, quant_type), k, v,
+                     block_table, kv_lens, row_offsets, values=True)
+
+
+@kv_write_values_op.register_fake
+def _(k, v, k_packed, k_absmax, v_packed, v_absmax, block_table, kv_lens, row_offsets, blocksize,
+      quant_type):
+    return k.new_empty(k.shape), v.new_empty(v.shape)
+
+
+@torch.library.custom_op("nf4::kv_read", mutates_args=())
+def kv_read_op(k_packed: torch.Tensor, k_absmax: torch.Tensor, v_packed: torch.Tensor,
+               v_absmax: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+               row_offsets: torch.Tensor | None, rows: int, blocksize: int, quant_type: str,
+               dtype: torch.dtype) -> tuple[torch.Tensor, torch.Tensor]:
+    return _kv_read(KVCache(k_packed, k_absmax, v_packed, v_absmax, blocksize, quant_type), rows,
+                    block_table, kv_lens, row_offsets, dtype)
+
+
+@kv_read_op.register_fake
+def _(k_packed, k_absmax, v_packed, v_absmax, block_table, kv_lens, row_offsets, rows, blocksize,
+      quant_type, dtype):
+    shape = (rows, k_packed.shape[1], 2 * k_packed.shape[3])
+    return k_packed.new_empty(shape, dtype=dtype), k_packed.new_empty(shape, dtype=dtype)
+
+
+@torch.library.custom_op("nf4::kv_attention", mutates_args=())
+def kv_attention_op(q: torch.Tensor, k_packed: torch.Tensor, k_absmax: torch.Tensor,
+                    v_packed: torch.Tensor, v_absmax: torch.Tensor, block_table: torch.Tensor,
+                    kv_lens: torch.Tensor, row_offsets: torch.Tensor | None, blocksize: int,
+                    quant_type: str, max_rows: int = 0, max_len: int = 0,
+                    scale: float | None = None, causal: bool = True,
+                    window: int = 0) -> torch.Tensor:
+    cache = KVCache(k_packed, k_absmax, v_packed, v_absmax, blocksize, quant_type)
+    return _kv_attention(q, cache, block_table, kv_lens, row_offsets, max_rows, max_len, scale,
+                         causal, window)
+
+
+@kv_attention_op.register_fake
+def _(q, k_packed, k_absmax, v_packed, v_absmax, block_table, kv_lens, row_offsets, blocksize,
+      quant_type, max_rows=0, max_len=0, scale=None, causal=True, window=0):
+    return q.new_empty(q.shape)
 
 
 class Linear4bit(nn.Module):
@@ -195,4 +272,5 @@ class Linear4bit(nn.Module):
                                     self.double_quant)
 
 
-__all__ = ["Linear4bit", "quantize_op", "dequantize_op", "linear_op"]
+__all__ = ["Linear4bit", "quantize_op", "dequantize_op", "linear_op", "kv_write_op",
+           "kv_write_values_op", "kv_read_op", "kv_attention_op"]
