@@ -76,7 +76,8 @@ nf4_status check_call(const nf4_kv_cache *c, const nf4_kv_rows *r, int32_t dtype
       return NF4_ERR_MISALIGNED;
   }
   int64_t capacity = (int64_t)r->table_cols * c->page_size;
-  if (capacity > 0x7fff0000) capacity = 0x7fff0000;
+  // a range of positions may be rounded up past it, and stays below 2^31
+  if (capacity > kMaxPositions) capacity = kMaxPositions;
   if (c->num_pages == 0) capacity = 0;
   kv->packed[0] = c->k_packed;
   kv->packed[1] = c->v_packed;

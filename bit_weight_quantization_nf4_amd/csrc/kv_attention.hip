@@ -192,6 +192,7 @@ bool kv_attention_fits(const KvAttentionSizes &z) {
   const int64_t pairs = (int64_t)z.max_rows * (z.heads / z.kv_heads);
   if (pairs * (64 * kJoinWaves) > 0xffffffffll || z.batch > 65535 || z.kv_heads > 65535)
     return false;
+  if (z.heads / z.kv_heads > 65535) return false;  // a head's number is exact in row_at
   const Plan p = plan_of(z);
   return (int64_t)p.wg_blocks * p.splits * (64 * kMergeWaves) <= 0xffffffffll;
 }

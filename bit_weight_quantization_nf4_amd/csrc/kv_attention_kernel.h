@@ -35,7 +35,7 @@
 // rows take c1: there such a mean shifts all scores alike. mu = 1.6776896 2^7 makes
 // the 2-norm of NF4's c1 errors 6.2e-5 of the values' (1.6e-4 at mu = 2^7; a search
 // over 2^20 factors); E2M1 values are exact (mu = 6 2^7). 16-bit queries are exact
-// in fp16 after a power of two. w: one fp16 for bf16 rows (2^-12), two for fp16
+// in fp16 after a power of two of the row's own, so no row depends on another's size. w: one fp16 for bf16 rows (2^-12), two for fp16
 // rows, whose output resolves 2^-11. fp32 rows: q, c' and w in two parts each, the
 // three leading products. Accumulators and statistics are fp32.
 //
@@ -197,6 +197,11 @@ __device__ __forceinline__ float max2(float a, float b) {
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return max2(max2(a, b), c); }
 
+// The nearest number.
+__device__ __forceinline__ float finite(float v) {
+  return __builtin_amdgcn_fmed3f(v, -3.402823466e38f, 3.402823466e38f);
+}
+
 // A barrier for what the workgroup shares in LDS. (__syncthreads would also wait
 // for every load from memory.)
 __device__ __forceinline__ void lds_barrier() {
@@ -208,6 +213,13 @@ __device__ __forceinline__ void lds_barrier() {
 // A lane's value that is not known before this point: what a loop derives from it is
 // not computed ahead of the loop and held in registers throughout.
 __device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// A value that is computed at this point and not moved into a later block, away from the
+// lane exchanges that it takes as operands.
+__device__ __forceinline__ float here(float v) {
   asm volatile("" : "+v"(v));
   return v;
 }
@@ -339,7 +351,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   __shared__ float wave_m[MERGE ? kWaves : 1][A::kRows];
   __shared__ float wave_l[MERGE ? kWaves : 1][A::kRows];
   __shared__ float total_l[A::kRows];
-  __shared__ float wave_top[kWaves];
+  __shared__ float wave_top[kWaves][16];
 
   fetch_args();
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -509,13 +521,13 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   };
 
   // ---- queries: lane (n, g) holds elements 32 c + 8 g .. + 7 of row n of each tile,
-  // as fp16 after one power of two for all rows that brings the largest below 2^15.
+  // as fp16 after a power of two of the row's own that brings its largest below 2^15.
   // Rows past the last repeat the first one; nothing of theirs is stored. Waves that
   // share a block convert a fragment each.
   uint4 qh[NR][P];
   uint4 ql[A::kSplitQ && !MERGE ? NR : 1][A::kSplitQ && !MERGE ? P : 1];
   int row_lo[NR], row_hi[NR];  // positions the row sees
-  float qscale;
+  float qscale[NR];
   uint4 *const q_shared = reinterpret_cast<uint4 *>(merge_buf);  // [first, second parts][fragment][lane]
   {
     struct Raw { uint4 v[DT == kFP32 ? 2 : 1]; };
@@ -546,7 +558,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       return top;
     };
     auto exponent = [](float top) {
-      return __builtin_amdgcn_readfirstlane(top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0);
+      return top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
     };
     auto convert = [&](const Raw &r, int ex, uint4 &hi, uint4 &lo) {
       uint32_t h16[4], l16[4];
@@ -566,7 +578,6 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       row_hi[nr] = have ? seen_end(args, blk, row_at(16 * nr + n).token) : 0;
       row_lo[nr] = have ? seen_begin(args, row_hi[nr]) : 0;
     }
-    int ex;
     if constexpr (MERGE) {
       static_assert(NR * P <= kWaves, "a fragment for each wave");
       Raw raw;
@@ -574,19 +585,23 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       if (wave < NR * P) raw = load_raw(nr, c);
       write_table();
       if (wave < NR * P) {
-        const float top = max_over_groups(row16_max(largest(raw)));
-        if (lane == 0) wave_top[wave] = top;
+        const float top = max_over_groups(largest(raw));
+        if (g == 0) wave_top[wave][n] = top;
       }
       lds_barrier();
-      float top = wave_top[0];
 #pragma unroll
-      for (int i = 1; i < NR * P; ++i) top = max2(top, wave_top[i]);
-      ex = exponent(top);
-      if (wave < NR * P) {
-        uint4 hi, lo;
-        convert(raw, ex, hi, lo);
-        q_shared[64 * wave + lane] = hi;
-        if constexpr (A::kSplitQ) q_shared[64 * (NR * P + wave) + lane] = lo;
+      for (int i = 0; i < NR; ++i) {
+        float top = wave_top[i * P][n];
+#pragma unroll
+        for (int j = 1; j < P; ++j) top = max2(top, wave_top[i * P + j][n]);
+        const int ex = exponent(top);
+        qscale[i] = __builtin_amdgcn_ldexpf(args.f, ex - 15);
+        if (wave < NR * P && nr == i) {
+          uint4 hi, lo;
+          convert(raw, ex, hi, lo);
+          q_shared[64 * wave + lane] = hi;
+          if constexpr (A::kSplitQ) q_shared[64 * (NR * P + wave) + lane] = lo;
+        }
       }
       lds_barrier();
 #pragma unroll
@@ -600,19 +615,18 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
           if (have_rows) raw[nr][c] = load_raw(nr, c);
       write_table();
       lds_barrier();
-      float top = 0.0f;
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
+      for (int nr = 0; nr < NR; ++nr) {
+        float top = 0.0f;
 #pragma unroll
         for (int c = 0; c < P; ++c) top = max2(top, largest(raw[nr][c]));
-      ex = exponent(max_over_groups(row16_max(top)));
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
+        const int ex = exponent(max_over_groups(top));
+        qscale[nr] = __builtin_amdgcn_ldexpf(args.f, ex - 15);
 #pragma unroll
         for (int c = 0; c < P; ++c)
           convert(raw[nr][c], ex, qh[nr][c], ql[A::kSplitQ ? nr : 0][A::kSplitQ ? c : 0]);
+      }
     }
-    qscale = __builtin_amdgcn_ldexpf(args.f, ex - 15);
   }
   // the second parts of a fragment
   auto q_low = [&](auto nrc, auto cc) {
@@ -645,9 +659,6 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     const bool whole = ok0 && ok1 && pos0 >= all_lo && pos0 + kStep <= all_hi;
 
     // ---- S^T = K Q^T, combined over blocks into log2 units past m_use
-    float ks[NS];
-#pragma unroll
-    for (int u = 0; u < NS; ++u) ks[u] = in.ks[u] * qscale;
     f32x4 t[NR][2];
     // four code pairs of piece c: the byte of elements 32 c + 8 g + 2 i is i P + c of
     // the lane's run
@@ -693,12 +704,21 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
         });
         unroll<0, 4>([&](auto rc) {
           constexpr int R = rc;
-          const float a = row_scale<(4 * T + R) * NB + B>(ks);
+          const float a = row_scale<(4 * T + R) * NB + B>(in.ks);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
-            t[nr][T][R] = __builtin_fmaf(acc[nr][R], a, B == 0 ? -m_use[nr] : t[nr][T][R]);
+            t[nr][T][R] = B == 0    ? acc[nr][R] * a
+                          : NR == 1 ? t[nr][T][R] + acc[nr][R] * a
+                                    : __builtin_fmaf(acc[nr][R], a, t[nr][T][R]);
         });
       });
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float v = t[nr][T][r];
+          t[nr][T][r] = here(__builtin_fmaf(v, qscale[nr], -m_use[nr]));
+        }
     });
     const Places next = places_of(next_at);
     load_k(next);
@@ -739,11 +759,12 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       far = far || top[nr] > m_limit[nr];
     }
 #pragma unroll
-    for (int u = 0; u < NS; ++u) far = far || vs[u] > a_limit;
+    for (int u = 0; u < NS; ++u) far = far || fabsf(vs[u]) > a_limit;
     if (__builtin_amdgcn_ballot_w64(far) != 0) {
-      float av = vs[0];
+      float av = 0.0f;  // of the finite ones: an infinity is its own rows' matter
 #pragma unroll
-      for (int u = 1; u < NS; ++u) av = max2(av, vs[u]);
+      for (int u = 0; u < NS; ++u)
+        av = fabsf(vs[u]) < __builtin_inff() ? max2(av, fabsf(vs[u])) : av;
       av = max_over_groups(row16_max(av));
       // 2^8 / A stays finite: from 2^127 on, smaller scales are exact in fp16 steps
       // finer than the result's
@@ -773,11 +794,13 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       }
     }
 
-    // ---- weights
+    // ---- weights. A scale of infinity or NaN stands as the largest number: times the
+    // weight 0 of a row that does not see its position it is 0, and for the others it
+    // passes fp16's range.
     uint4 wh[NR][NB];
     uint4 wl[A::kSplitW ? NR : 1][A::kSplitW ? NB : 1];
 #pragma unroll
-    for (int u = 0; u < NS; ++u) vs[u] *= a_inv;
+    for (int u = 0; u < NS; ++u) vs[u] = finite(vs[u] * a_inv);
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
       float p[8];

@@ -21,6 +21,9 @@ struct KvArgs {
   int32_t capacity;  // positions that the table can hold
 };
 
+// Most positions of a sequence.
+constexpr int32_t kMaxPositions = 0x7ff00000;
+
 struct KvShape {
   int head_dim, blocksize, quant_type, dtype;
 };
@@ -65,12 +68,6 @@ __device__ __forceinline__ int32_t scalar_load(const int32_t *p, int64_t i) {
 
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) {
   return v < lo ? lo : (v > hi ? hi : v);
-}
-
-// First row of sequence b, b <= batch.
-__device__ __forceinline__ int row_begin(const KvArgs &kv, int b) {
-  if (kv.offsets == nullptr) return b * kv.uniform;
-  return clamp_to(scalar_load(kv.offsets, b), 0, kv.total_rows);
 }
 
 // 4-lane-row maximum of 16 lanes by DPP, in every lane.

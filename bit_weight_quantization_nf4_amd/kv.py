@@ -269,7 +269,9 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
     elif max_rows <= 0:
         max_rows = total
     if max_len <= 0:
-        max_len = min(rows.table_cols * cache.page_size, 0x7fff0000)
+        max_len = rows.table_cols * cache.page_size
+    # what does not fit 32 bits is past every position
+    max_rows, max_len, window = (min(n, 0x7ff00000) for n in (max_rows, max_len, window))
     qr, qh, _ = q.stride()
     orow, ohead, _ = out.stride()
     kv_heads, dt = cache.num_kv_heads, _DT[q.dtype]

@@ -8,7 +8,8 @@
  * Quantization is nf4_quantize's: per block of `blocksize` consecutive elements
  * of one head vector a = max|x|, s = RN(x / a), the nearest code value with an
  * exact tie going to the smaller one (s = 0 where a = 0). A code stands for
- * RN(c[code] a), as in nf4_dequantize. Inputs must be finite.
+ * RN(c[code] a), as in nf4_dequantize. Inputs must be finite: the codes and scales
+ * of a head vector that is not are unspecified, all others are not affected.
  *
  * The cache is paged. A page holds `page_size` positions of every key/value
  * head; position p of sequence b lies in page block_table[b][p / page_size].
@@ -52,7 +53,10 @@ extern "C" {
 
 /* The cache: four caller-owned device buffers. Limits (NF4_ERR_UNSUPPORTED
  * otherwise): head_dim 64, 96, 128, 192 or 256; blocksize 32, 64 or 128
- * dividing head_dim; page_size a multiple of 16. Strides are between pages, of
+ * dividing head_dim; page_size a multiple of 16 with page_size head_dim / 2 <
+ * 2^31; at most 65535 key/value heads and sequences; packed_page_stride < 2^36
+ * and absmax_page_stride < 2^32. A sequence has at most 2^31 - 2^20 positions
+ * (what the table can hold beyond that is not used). Strides are between pages, of
  * keys and values alike: packed_page_stride in bytes (a multiple of 16, at
  * least num_kv_heads page_size head_dim / 2), absmax_page_stride in floats (at
  * least num_kv_heads page_size head_dim / blocksize). */
@@ -112,8 +116,8 @@ int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_
 
 /* Attention of query rows to the cache. q, out: [total_rows][num_heads][
  * head_dim] of `dtype` with strides as in nf4_kv_write; num_heads is a multiple
- * of num_kv_heads, and head h attends to key/value head h / (num_heads /
- * num_kv_heads). Row i of the n_b rows of sequence b sees positions
+ * of num_kv_heads (at most 65535 times as many), and head h attends to
+ * key/value head h / (num_heads / num_kv_heads). Row i of the n_b rows of sequence b sees positions
  *   lo <= p < hi,  hi = causal ? kv_lens[b] - n_b + i + 1 : kv_lens[b],
  *                  lo = window > 0 ? max(0, hi - window) : 0,
  *   out = sum_p e_p v_p / sum_p e_p,  e_p = exp(scale q . k_p - max)
@@ -124,12 +128,15 @@ int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_
  *   relative in the norm), bf16's softmax weights as well;
  *   all: a position's share e_p a / sum e is resolved to 2^-32 of the largest value
  *   scale a that the row sees, which only shows where scales differ by as much.
+ * A query that is not finite spoils its own row only, and a scale in the cache that
+ * is not the rows that see its position.
  * max_rows: the most rows of any sequence (rows past it are left as they are; 0
- * stands for total_rows); ignored without row_offsets. max_len: about the longest kv_lens, which sizes
- * the split of the positions over the device (any value gives a right result;
- * 0 stands for the table's capacity). workspace: at least
- * nf4_kv_attention_workspace_bytes of these sizes (16-byte aligned; NF4_ERR_SCRATCH where it is smaller); it holds no state
- * between calls. Results do not depend on anything but the arguments and the
+ * stands for total_rows); ignored without row_offsets. max_len: about the longest
+ * kv_lens, which sizes the split of the positions over the device (any value gives
+ * a right result; 0 stands for the table's capacity). workspace: at least
+ * nf4_kv_attention_workspace_bytes of these sizes (16-byte aligned; NF4_ERR_SCRATCH
+ * where it is smaller); it holds no state between calls, and calls that may run at
+ * once need one each. Results do not depend on anything but the arguments and the
  * device's CU count, bit for bit. */
 nf4_status nf4_kv_attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, const void *q,
                             int64_t q_row_stride, int64_t q_head_stride, int32_t num_heads,

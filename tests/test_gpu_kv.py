@@ -612,3 +612,93 @@ def test_workspace_too_small_is_refused(nf4):
         st = kv._lib().nf4_kv_attention(cache.desc, rows, q.data_ptr(), 512, 128, 4, 0, 0.1, 1, 0, 1,
                                         1 << 17, q.data_ptr(), 512, 128, ws.data_ptr(), n, None)
         assert st == want
+
+
+ROWS_APART = [
+    # dtype, D, bs, heads, kv heads, lens, rows: waves that share a block of one tile, of
+    # two, and waves with rows of their own
+    ("bf16", 128, 64, 4, 2, [75, 40], [5, 3]),
+    ("fp16", 64, 32, 16, 2, [90], [4]),
+    ("fp32", 256, 128, 2, 1, [60], [6]),
+    ("bf16", 128, 128, 8, 2, [170], [40]),
+    ("fp16", 96, 32, 4, 1, [100, 37], [37, 33]),
+]
+
+
+@pytest.mark.parametrize("split", ["one", "many"])
+@pytest.mark.parametrize("case", ROWS_APART, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_queries_do_not_affect_each_other(nf4, orc, case, split):
+    """One query of infinities, NaN, or near the type's ends: every other row (of the
+    same block, too) is within its bounds, and the odd one is where it is finite."""
+    dtype, d, bs, heads, kvh, lens, rows = case
+    call, pages = ref.make_call(lens, rows, 16, 900)
+    book = ref.codebook(orc, "nf4")
+    nat = ref.random_cache(book, pages, kvh, 16, d, bs, "nf4", 901)
+    cache = device_cache(nf4, nat, bs, "nf4")
+    k64, v64 = (dense(book, *x, bs) for x in nat)
+    info = torch.finfo(DT[dtype])
+    odd = torch.zeros(call.total, heads, dtype=torch.bool)
+    odd[1, 0] = odd[call.total - 1, heads - 1] = True
+    for value in (float("inf"), float("nan"), info.max, -info.max / 3, info.tiny):
+        q = queries(call.total, heads, d, dtype, 902)
+        q[1, 0] = 0
+        q[1, 0, 5] = value
+        q[-1, -1, 3::2] = value
+        out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=max(rows),
+                               max_len=1 if split == "one" else 1 << 17).cpu()
+        clean = torch.where(odd[..., None], torch.zeros((), dtype=DT[dtype]), q)
+        want, spread, reach = ref.attention(call, clean, k64, v64, ref.sqrt_scale(d), True, 0)
+        got = torch.where(odd[..., None], want.to(out.dtype), out)
+        check_attention(got, want, spread, reach, dtype, "nf4", d, max(lens), nat, norm=False)
+        if value == info.tiny:  # scores of about zero: the mean of the values
+            check_attention(out[1:2, :1], *(t[1:2, :1] for t in (want, spread, reach)), dtype,
+                            "nf4", d, max(lens), nat, norm=False)
+        elif not np.isfinite(value):
+            assert not torch.isfinite(out[1, 0]).all() and not torch.isfinite(out[-1, -1]).all()
+
+
+@pytest.mark.parametrize("split", ["one", "many"])
+@pytest.mark.parametrize("case", ROWS_APART, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_positions_affect_only_rows_that_see_them(nf4, orc, case, split):
+    """Scales of infinity and NaN at the newest position, which only the last row of its
+    sequence sees, and at one that a window has left behind for all but the first."""
+    dtype, d, bs, heads, kvh, lens, rows = case
+    call, pages = ref.make_call(lens, rows, 16, 910)
+    book = ref.codebook(orc, "nf4")
+    nat = ref.random_cache(book, pages, kvh, 16, d, bs, "nf4", 911)
+    k64, v64 = (dense(book, *x, bs) for x in nat)
+    q = queries(call.total, heads, d, dtype, 912)
+    b, window = len(lens) - 1, 19
+    kw = dict(max_rows=max(rows), max_len=1 if split == "one" else 1 << 17, window=window)
+    want = ref.attention(call, q, k64, v64, ref.sqrt_scale(d), True, window)
+    first, last = call.total - rows[b], call.total - 1  # rows of sequence b
+    newest = lens[b] - 1
+    oldest = lens[b] - rows[b] + 1 - window             # seen by its first row only
+    for pos, row in ((newest, last), (oldest, first)):
+        if pos < 0:
+            continue
+        keep = [r for r in range(call.total) if r != row]
+        for which in (0, 1):
+            for bad in (float("inf"), float("nan")):
+                cache = device_cache(nf4, nat, bs, "nf4")
+                a = (cache.k_absmax, cache.v_absmax)[which]
+                a[int(call.table[b, pos // 16]), :, pos % 16] = bad
+                out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), **kw).cpu()
+                check_attention(out[keep], *(t[keep] for t in want), dtype, "nf4", d, max(lens),
+                                nat, norm=False)
+                assert not torch.isfinite(out[row]).all()
+
+
+def test_rows_past_max_rows_and_wide_arguments(nf4, orc):
+    """Rows past max_rows stay as they are; windows and lengths past 32 bits are as good
+    as none."""
+    case = ("bf16", "nf4", 128, 64, 8, 2, 16, [100, 33, 60], [6, 2, 3], True, 0)
+    a, want, (call, cache, q, nat) = run_attention(nf4, orc, case, 920)
+    out = torch.full_like(q, 7.0).cuda()
+    nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=3, out=out)
+    kept = [0, 1, 2, 6, 7, 8, 9, 10]
+    assert torch.all(out[3:6] == 7.0)
+    check_attention(out[kept], *(t[kept] for t in want), "bf16", "nf4", 128, 100, nat)
+    wide = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=6, max_len=1 << 40,
+                            window=(1 << 32) + 5)
+    check_attention(wide, *want, "bf16", "nf4", 128, 100, nat)
