@@ -98,11 +98,24 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(Attn
 
 // ------------------------------------------------------------------- host
 
-// From this many rows of a kv head on, a workgroup's waves have rows of their own.
-constexpr int kApartMinRows = 128;
+// Waves have rows of their own where that gives a workgroup for every CU: they then
+// decode a position's codes once for 4 blocks of a CU's rows and merge nothing (2
+// sequences of 1024 rows at 5000 positions, 32 query heads of 8: 205 us, 251 merged; 4
+// of 256 rows at 1000: 51, 64). With fewer the waves that share a block finish sooner
+// (512 rows at 4096: 87 merged, 105 apart; 32 rows at 2048: 18, 24). Sequences of fewer
+// rows than a workgroup's leave its waves without any (64 of one row: 36 merged, 84).
+constexpr int kApartMinRows = 128, kApartMinItems = 256;
 
-// From how many positions on an item is split, and the fewest that a range has.
-constexpr int64_t kSplitFrom = 1536, kMinRange = 512, kMinRangeApart = 1024;
+// From how many positions on an item is split, and the fewest that a range has. The
+// second launch takes about as long as 1500 positions of a workgroup: 1536 positions,
+// one row, 15.0 us whole and 17.8 split, 2048 18.0 either way, 4096 29.6 and 18.0.
+// Ranges of 256, 512 and 1024 differ by less than 1 us. A range of waves with rows of
+// their own costs more to join (1024 rows at 2048 positions: 90.7 whole, 96.1 in two; at
+// 4096 158 either way).
+constexpr int64_t kSplitFrom = 2048, kMinRange = 512;
+constexpr int64_t kSplitFromApart = 4096, kMinRangeApart = 2048;
+// What a range costs besides its positions, in positions.
+constexpr int64_t kRangeCost = 700;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -110,7 +123,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 Plan plan_of(const KvAttentionSizes &z) {
   Plan p;
   const int64_t pairs = (int64_t)z.max_rows * (z.heads / z.kv_heads);
-  p.merge = pairs < kApartMinRows;
+  const int64_t apart_blocks = ceil_div(pairs, 16 * max_tiles(z.head_dim) * kApartWaves);
+  p.merge = pairs < kApartMinRows ||
+            (int64_t)z.batch * z.kv_heads * apart_blocks < kApartMinItems;
   p.tiles = p.merge && pairs <= 16 ? 1 : max_tiles(z.head_dim);
   p.wg_rows = 16 * p.tiles * (p.merge ? 1 : kApartWaves);
   p.wg_blocks = (int)ceil_div(pairs, p.wg_rows);
@@ -121,13 +136,26 @@ Plan plan_of(const KvAttentionSizes &z) {
   int64_t span = z.max_len;
   if (z.window > 0 && span > (int64_t)z.window + z.max_rows) span = (int64_t)z.window + z.max_rows;
   const int64_t weight = z.head_dim * (z.dtype == kFP32 ? 3 : 1);
-  // two workgroups for a CU; a second launch is worth it where a workgroup alone
-  // would take kSplitFrom positions or more
   int64_t s = 1;
-  if (span * weight >= kSplitFrom * 128) {
-    const int64_t want = 2 * (int64_t)device_cu_count();
-    // waves that merge leave room for uneven items; those apart fill what there is
-    s = items > 0 ? (p.merge ? ceil_div(want, items) : want / items) : 1;
+  if (span * weight >= (p.merge ? kSplitFrom : kSplitFromApart) * 128) {
+    // as many ranges as fill the device once, or twice where workgroups of uneven
+    // sequences share a CU, whichever is done first: every round of workgroups takes a
+    // range's time. (Sequences up to 8000, 8 kv heads, one row: 40 of them 64.6 us with
+    // two rounds allowed, 79.0 with one; of equal length 4000, 53.2 and 49.1. Where a
+    // workgroup has a CU to itself, 10 sequences of 16 rows at 4000, 44.4 with one
+    // round, 54.7 with two.)
+    // (as many workgroups of a CU as the kernel's kWavesPerSimd allows)
+    const bool two = !p.merge || (p.tiles == 1 && z.head_dim <= 128 && z.dtype != kFP32);
+    const int64_t slots = (two ? 2 : 1) * (int64_t)device_cu_count();
+    int64_t best = ceil_div(items, slots) * (span + kRangeCost);
+    for (int rounds = 1; items > 0 && rounds <= (p.merge && two ? 2 : 1); ++rounds) {
+      const int64_t c = rounds * slots / items;
+      if (c <= 1) continue;
+      const int64_t cost = ceil_div(items * c, slots) * (span / c + kRangeCost);
+      if (cost >= best) continue;
+      best = cost;
+      s = c;
+    }
     const int64_t least = p.merge ? kMinRange * 128 / weight : kMinRangeApart;
     const int64_t most = ceil_div(span, least > 0 ? least : 1);
     if (s > most) s = most;

@@ -344,6 +344,29 @@ def test_attention(nf4, orc, case, split):
     assert torch.all(out.cpu()[empty] == 0)
 
 
+# Rows of a workgroup's waves are their own from 128 (row, head) pairs a kv head and 256
+# workgroups on; positions are then split where max_len is large and workgroups few.
+MANY_ROWS = [
+    ("bf16", "nf4", 128, 64, 64, 64, 16, [150, 131, 97, 128], [128, 100, 97, 3], True, 0),
+    ("fp16", "fp4", 64, 32, 96, 32, 48, [70, 61, 43, 99, 0, 12, 50, 43], [43, 40, 1, 43, 7, 12, 33, 43], True, 0),
+    ("fp32", "nf4", 256, 128, 32, 32, 16, [129, 140, 128, 77], [128, 100, 128, 77], True, 0),
+    ("bf16", "nf4", 192, 64, 64, 32, 16, [90, 101, 64, 150], [64, 33, 64, 1], True, 20),
+    ("fp16", "nf4", 96, 32, 64, 64, 32, [128, 60, 200, 5], [128, 60, 90, 9], False, 0),
+    ("fp32", "nf4", 128, 32, 64, 64, 16, [128, 300, 33, 64], [128, 64, 33, 64], True, 0),
+    ("bf16", "fp4", 256, 32, 32, 32, 16, [128, 140, 1, 90], [128, 128, 1, 40], True, 0),
+]
+
+
+@pytest.mark.parametrize("split", ["one", "many"])
+@pytest.mark.parametrize("case", MANY_ROWS, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_attention_of_many_rows(nf4, orc, case, split):
+    """As test_attention; rows of sequences shorter than their rows see nothing."""
+    out, want, (_, _, _, nat) = run_attention(nf4, orc, case, 150 + case[2],
+                                              1 if split == "one" else 1 << 17)
+    check_attention(out, *want, case[0], case[1], case[2], max(case[7]), nat)
+    assert torch.all(out.cpu()[want[1].sum(-1) == 0] == 0)
+
+
 def test_attention_is_reproducible_and_split_by_its_arguments(nf4, orc):
     case = ("bf16", "nf4", 128, 64, 8, 2, 16, [1500, 700], [1, 1], True, 0)
     a, want, (call, cache, q, nat) = run_attention(nf4, orc, case, 200)
@@ -616,12 +639,14 @@ def test_workspace_too_small_is_refused(nf4):
 
 ROWS_APART = [
     # dtype, D, bs, heads, kv heads, lens, rows: waves that share a block of one tile, of
-    # two, and waves with rows of their own
+    # two, several such blocks, and waves with rows of their own
     ("bf16", 128, 64, 4, 2, [75, 40], [5, 3]),
     ("fp16", 64, 32, 16, 2, [90], [4]),
     ("fp32", 256, 128, 2, 1, [60], [6]),
     ("bf16", 128, 128, 8, 2, [170], [40]),
     ("fp16", 96, 32, 4, 1, [100, 37], [37, 33]),
+    ("bf16", 128, 128, 64, 64, [140, 150, 131, 40], [128, 128, 100, 3]),
+    ("fp32", 64, 32, 64, 32, [90, 70] * 2, [64, 64] * 2),
 ]
 
 
