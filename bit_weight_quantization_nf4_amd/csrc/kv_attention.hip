@@ -99,11 +99,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(Attn
 // ------------------------------------------------------------------- host
 
 // Waves have rows of their own where that gives a workgroup for every CU: they then
-// decode a position's codes once for 4 blocks of a CU's rows and merge nothing (2
-// sequences of 1024 rows at 5000 positions, 32 query heads of 8: 205 us, 251 merged; 4
-// of 256 rows at 1000: 51, 64). With fewer the waves that share a block finish sooner
-// (512 rows at 4096: 87 merged, 105 apart; 32 rows at 2048: 18, 24). Sequences of fewer
-// rows than a workgroup's leave its waves without any (64 of one row: 36 merged, 84).
+// merge nothing (1024 and 512 rows at 5000 and 2500 positions, 32 query heads of 8: 205
+// us, 251 merged; 4 sequences of 256 rows at 1000: 51, 64). With fewer the waves that
+// share a block finish sooner (512 rows at 4096: 87 merged, 105 apart; 32 rows at 2048:
+// 18, 24). Sequences of fewer rows than a workgroup's leave its waves without any (64 of
+// one row: 36 merged, 84).
 constexpr int kApartMinRows = 128, kApartMinItems = 256;
 
 // From how many positions on an item is split, and the fewest that a range has. The

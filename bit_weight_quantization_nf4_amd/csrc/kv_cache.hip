@@ -15,7 +15,11 @@
 //   W = 4: elements 32 (k0 + i) + 8 j ..         W = 1: 32 k0 + 2 m ..
 //   W = 2: elements 32 (k0 + i % 2) + 8 j + 4 (i / 2) ..
 // Both kernels are bound by HBM. A row's place costs a chain of dependent loads, so a
-// wave takes as many heads of it as leave the launch enough waves.
+// wave takes as many heads of it as leave the launch enough waves (kJobsWanted).
+// Measured on one MI355X, 8 heads of 128 in bf16: prompts of 16396 rows in all written,
+// 153 MB, 32 us, 4.8 TB/s (a copy: 4.99); 73728 rows read, 387 MB, 60-72 us, 5.4-6.4
+// TB/s (three quarters are writes). A single token: 3.6 us of GPU time, launch and
+// arguments.
 #include <type_traits>
 
 #include "kv_internal.h"
@@ -309,7 +313,8 @@ __device__ __forceinline__ Job job_of(const KvRowsArgs &args, int64_t job) {
   return j;
 }
 
-// Heads whose codes a reading wave has in flight.
+// Heads whose codes a reading wave has in flight: 73728 rows of 8 heads take 71.7 us, 85
+// with 4.
 constexpr int kInFlight = 8;
 
 // RN(x / a) given r = RN(1 / a): one product and one residual step (Markstein),
@@ -324,10 +329,16 @@ __device__ __forceinline__ float quotient(float x, float a, float r) {
   return __builtin_fmaf(__builtin_fmaf(-q, a, x), r, q);
 }
 
-// Lookup of s: its cell's entry (threshold, and the codes on either side as in
-// cell_of) and, 64 entries on, the values of these codes. Byte J of `codes` becomes
-// the code in the nibble that SRC selects (2: high, 0: low), `value` its value. J = 0
-// of the first in a byte clears the others.
+// Entries of the lookup: cell floor(RN(128 s + 128) / 8) of s. Any bit pattern of s, a
+// NaN included, has one of the 64.
+constexpr int kLutSize = 64;
+
+// Lookup of s: its cell's entry (a threshold; the codes below and above it in the bytes
+// 0 and 1, shifted to the high nibble in 2 and 3) and, 64 entries on, the values of
+// these codes. t = 2^23 + RN(128 s + 128) in one fma: its low bits masked to a multiple
+// of 8 are the entry's byte offset. Byte J of `codes` becomes the code in the nibble
+// that SRC selects (2: high, 0: low), `value` its value; J = 0 clears the other bytes.
+// (The select of `value` stands between the byte write and its first reader.)
 template <int J, int SRC>
 __device__ __forceinline__ void encode(uint32_t &codes, float &value, float s, const uint2 *lut) {
   const float t = __builtin_fmaf(s, 128.0f, 8388736.0f);  // 2^23 + 128
@@ -492,6 +503,8 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRowsArgs args) {
   }
 }
 
+// Waves' worth of work wanted before a wave takes more heads: prompts written in 32.9 us
+// with 1024 and with 4096, 35.8 with 16384; a few hundred rows are bound by the launch.
 constexpr int64_t kJobsWanted = 4096;
 
 KvRowsArgs make_args(const KvArgs &kv, const KvShape &sh) {

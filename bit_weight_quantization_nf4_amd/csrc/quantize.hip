@@ -76,6 +76,21 @@ __device__ __forceinline__ float normalise(float x, float a, float r) {
   return __builtin_fmaf(e, r, q0);
 }
 
+// Cell lookup: t = 2^23 + RN(128 s + 128) (one fma, the integer exact); its
+// representation's low bits masked to a multiple of 8 are the byte offset of
+// 8-byte entry floor(RN(128 s + 128) / 8). An entry holds a threshold and the
+// codes below / above it, pre-placed as bytes: below, above in bytes 0, 1
+// (low nibble) and below << 4, above << 4 in bytes 2, 3 (high nibble). Any bit
+// pattern of t (a NaN from non-finite input included) stays inside the 64
+// entries.
+constexpr int kLutSize = 64;
+
+__device__ __forceinline__ uint2 cell_of(float s, const uint2 *lut) {
+  const float t = __builtin_fmaf(s, 128.0f, 8388736.0f);  // 2^23 + 128
+  return *reinterpret_cast<const uint2 *>(reinterpret_cast<const char *>(lut) +
+                                          (__float_as_uint(t) & 0x1f8u));
+}
+
 // Byte J of acc = (s > threshold) ? byte SRC + 1 : byte SRC of the entry's
 // codes; J = 0 clears the other bytes, later J keep them. One compare and
 // one byte-select (SDWA) per code.
@@ -664,6 +679,13 @@ __device__ __forceinline__ void load8_elems(float (&x)[8], const void *w, int64_
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = DT == kFP16 ? widen16<kFP16>(h[j]) : widen16<kBF16>(h[j]);
   }
+}
+
+// code of s through the cell lookup: the one threshold inside s's cell
+// decides between the codes below and above it
+__device__ __forceinline__ uint32_t code_of(float s, const uint2 *lut) {
+  const uint2 e = cell_of(s, lut);
+  return s > __uint_as_float(e.x) ? (e.y >> 8) & 0xfu : e.y & 0xfu;
 }
 
 template <int DT, int BS>
