@@ -31,13 +31,16 @@
 // Rounding. c' = c mu is held as two fp16 values c1 + c2 (mu carries 2^7, which
 // keeps c2 normal). Values take both: the error of c1 alone is the same at every
 // position of a code, so its mean over the codes stays while the sum of many
-// positions averages out (5e-3 of the result at 70000 positions). Keys of 16-bit
+// positions averages out (5e-3 of the result at 70000 positions). Keys of bf16
 // rows take c1: there such a mean shifts all scores alike. mu = 1.6776896 2^7 makes
 // the 2-norm of NF4's c1 errors 6.2e-5 of the values' (1.6e-4 at mu = 2^7; a search
 // over 2^20 factors); E2M1 values are exact (mu = 6 2^7). 16-bit queries are exact
-// in fp16 after a power of two of the row's own, so no row depends on another's size. w: one fp16 for bf16 rows (2^-12), two for fp16
-// rows, whose output resolves 2^-11. fp32 rows: q, c' and w in two parts each, the
-// three leading products. Accumulators and statistics are fp32.
+// in fp16 after a power of two of the row's own, so no row depends on another's size.
+// w: one fp16 for bf16 rows (2^-12), two for fp16 rows, whose output resolves 2^-11; so
+// do their keys (one part costs 3e-4 of the result at scores of size 3, and takes 29.5
+// us instead of 32.6 at 8 sequences up to 4000 positions, 32 of 32 heads). fp32 rows: q,
+// c' and w in two parts each, the three leading products. Accumulators and statistics
+// are fp32.
 //
 // Work. An item is a workgroup's block of rows of one sequence and kv head; where
 // items are few its positions are split into equal ranges, whose partial sums a second
@@ -55,9 +58,6 @@
 //     instructions do not overlap well within a SIMD and take about its whole time.
 //   - short calls: 9 us, of which the arguments' way, the table and the merge of the
 //     waves are 6.
-//   - two-part keys for fp16 rows would cost 11 % (29.5 -> 32.6 us, 8 sequences up to 4000
-//     positions, 32 of 32 heads) and bring the error from 2.9e-4 to the output's own
-//     rounding, 2.1e-4.
 #pragma once
 
 #include <type_traits>
@@ -329,7 +329,8 @@ struct Attn {
   static constexpr int PB = BS / 32;        // pieces of a block
   static constexpr int NS = (8 * NB + 15) / 16;  // scales a lane holds of a step
   static constexpr bool kSplitW = DT != kBF16;   // two-part weights
-  static constexpr bool kSplitQ = DT == kFP32;   // two-part queries and keys' code values
+  static constexpr bool kSplitK = DT != kBF16;   // two-part code values of keys
+  static constexpr bool kSplitQ = DT == kFP32;   // two-part queries
   static constexpr int kRows = 16 * NR;
   // waves for which registers are shared out: two workgroups of a CU where they
   // suffice (128 registers), else one of 8 waves or two of 4 (256)
@@ -709,11 +710,11 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
           else k1 = look_up_k(tc, cc, lane_off);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) acc[nr] = mfma16x16x32<kFP16>(k1, qh[nr][C], acc[nr]);
-          if constexpr (A::kSplitQ) {
+          if constexpr (A::kSplitK) {
             const uint4 k2 = look_up_k(tc, cc, lane_off + 128u);
             unroll<0, NR>([&](auto nrc) {
               constexpr int nr = nrc;
-              acc[nr] = mfma16x16x32<kFP16>(k1, q_low(nrc, cc), acc[nr]);
+              if constexpr (A::kSplitQ) acc[nr] = mfma16x16x32<kFP16>(k1, q_low(nrc, cc), acc[nr]);
               acc[nr] = mfma16x16x32<kFP16>(k2, qh[nr][C], acc[nr]);
             });
           }

@@ -124,8 +124,9 @@ int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_
  * and a row that sees nothing is zeros. Keys and values enter as c[code] a with
  * no rounding to dtype in between; sums and softmax statistics are fp32.
  *   fp32 rows: as in fp32 arithmetic (relative error about 1e-6);
- *   bf16 and fp16 rows: the keys' code values carry 11 significant bits (6e-5
- *   relative in the norm), bf16's softmax weights as well;
+ *   fp16 rows: likewise, but for the output's rounding;
+ *   bf16 rows: the keys' code values (6e-5 relative in the norm) and the softmax
+ *   weights carry 11 significant bits;
  *   all: a position's share e_p a / sum e is resolved to 2^-32 of the largest value
  *   scale a that the row sees, which only shows where scales differ by as much.
  * A query that is not finite spoils its own row only, and a scale in the cache that

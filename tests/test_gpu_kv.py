@@ -11,8 +11,9 @@ bit-exact. Attention is held to two derived bounds per case:
    its argument near the maximum; a softmax weight is off by twice that at most
    (numerator and denominator), w its own rounding; 2^-22 that of the values'
    codes (two fp16 parts); T positions are summed; h the rounding of the output
-   (half a step). c: fp16's half step 2^-11 for 16-bit rows (0 for E2M1 codes,
-   which are exact), 2^-22 for fp32 rows, whose queries have two parts too. w:
+   (half a step). c: fp16's half step 2^-11 for bf16 rows (0 for E2M1 codes,
+   which are exact), 2^-22 for fp16 rows and for fp32 rows, whose queries have two
+   parts too. w:
    2^-11 for bf16 rows, 2^-22 (two parts) otherwise.
    A floor is added, which shows where the largest weights meet zeros. The weight
    of position p enters the matrix cores as w = 2^(t - m) a / A 2^8 in fp16, whose
@@ -296,7 +297,7 @@ def queries(total, heads, d, dtype, seed):
 
 
 def check_attention(got, want, spread, reach, dtype, quant, d, longest, nat, norm=True):
-    c = {"bf16": 2.0 ** -11, "fp16": 2.0 ** -11, "fp32": 2.0 ** -22}[dtype]
+    c = {"bf16": 2.0 ** -11, "fp16": 2.0 ** -22, "fp32": 2.0 ** -22}[dtype]
     c = 0.0 if quant == "fp4" else c
     w = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22
     r = (c + (d + 16) * 2.0 ** -24) * reach + 2.0 ** -21
