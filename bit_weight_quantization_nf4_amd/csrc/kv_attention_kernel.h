@@ -37,10 +37,9 @@
 // over 2^20 factors); E2M1 values are exact (mu = 6 2^7). 16-bit queries are exact
 // in fp16 after a power of two of the row's own, so no row depends on another's size.
 // w: one fp16 for bf16 rows (2^-12), two for fp16 rows, whose output resolves 2^-11; so
-// do their keys (one part costs 3e-4 of the result at scores of size 3, and takes 29.5
-// us instead of 32.6 at 8 sequences up to 4000 positions, 32 of 32 heads). fp32 rows: q,
-// c' and w in two parts each, the three leading products. Accumulators and statistics
-// are fp32.
+// do their keys (one part would cost 3e-4 of the result at scores of size 3). fp32 rows:
+// q, c' and w in two parts each, the three leading products. Accumulators and
+// statistics are fp32.
 //
 // Work. An item is a workgroup's block of rows of one sequence and kv head; where
 // items are few its positions are split into equal ranges, whose partial sums a second
@@ -262,12 +261,6 @@ __device__ __forceinline__ float sum_over_groups(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Half H of four fp16 pairs, each pair twice.
-template <int H>
-__device__ __forceinline__ uint4 twice(uint4 v) {
-  return H == 0 ? make_uint4(v.x, v.x, v.y, v.y) : make_uint4(v.z, v.z, v.w, v.w);
-}
-
 template <int I, int N, typename F>
 __device__ __forceinline__ void unroll(F &&f) {
   if constexpr (I < N) {
@@ -275,6 +268,10 @@ __device__ __forceinline__ void unroll(F &&f) {
     unroll<I + 1, N>(static_cast<F &&>(f));
   }
 }
+
+// Which parts of the table's entries a lookup takes.
+constexpr std::integral_constant<int, 0> kFirst;
+constexpr std::integral_constant<int, 1> kSecond;
 
 // What an fp16 pair leaves of two fp32, as another.
 __device__ __forceinline__ uint32_t rest_f16x2(float a, float b, uint32_t h) {
@@ -677,20 +674,28 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
 
     // ---- S^T = K Q^T, combined over blocks into log2 units past m_use
     f32x4 t[NR][2];
+    // An entry's second parts. (volatile: fetched in one instruction with the first, they
+    // would come beside them and be copied; 32.8 us instead of 30.8 at 8 sequences up to
+    // 4000 positions, fp16, 32 of 32 heads.)
+    auto second_part = [&](uint32_t address) -> uint32_t {
+      return *(const volatile __attribute__((address_space(3))) uint32_t *)(
+          (const __attribute__((address_space(3))) char *)lds + address + 128);
+    };
     // four code pairs of piece c: the byte of elements 32 c + 8 g + 2 i is i P + c of
     // the lane's run
-    auto look_up_k = [&](auto tc, auto cc, uint32_t off) {
+    auto look_up_k = [&](auto tc, auto cc, auto x) {
       uint32_t e[4];
       unroll<0, 4>([&](auto ic) {
         constexpr int O = ic * P + cc;
-        e[ic] = *reinterpret_cast<const uint32_t *>(
-            lds + table_address<O % 4>(in.k[tc][O / 4], off));
+        const uint32_t ad = table_address<O % 4>(in.k[tc][O / 4], lane_off);
+        if constexpr (x == 0) e[ic] = *reinterpret_cast<const uint32_t *>(lds + ad);
+        else e[ic] = second_part(ad);
       });
       return make_uint4(e[0], e[1], e[2], e[3]);
     };
     uint4 ahead[A::kAhead ? 2 : 1][A::kAhead ? P : 1];
     auto look_up_tile = [&](auto tc) {
-      unroll<0, P>([&](auto cc) { ahead[tc][cc] = look_up_k(tc, cc, lane_off); });
+      unroll<0, P>([&](auto cc) { ahead[tc][cc] = look_up_k(tc, cc, kFirst); });
       __builtin_amdgcn_sched_barrier(0);
     };
     if constexpr (A::kAhead) look_up_tile(std::integral_constant<int, 0>{});
@@ -707,11 +712,11 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
           const std::integral_constant<int, C> cc;
           uint4 k1;
           if constexpr (A::kAhead) k1 = ahead[T][C];
-          else k1 = look_up_k(tc, cc, lane_off);
+          else k1 = look_up_k(tc, cc, kFirst);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) acc[nr] = mfma16x16x32<kFP16>(k1, qh[nr][C], acc[nr]);
           if constexpr (A::kSplitK) {
-            const uint4 k2 = look_up_k(tc, cc, lane_off + 128u);
+            const uint4 k2 = look_up_k(tc, cc, kSecond);
             unroll<0, NR>([&](auto nrc) {
               constexpr int nr = nrc;
               if constexpr (A::kSplitQ) acc[nr] = mfma16x16x32<kFP16>(k1, q_low(nrc, cc), acc[nr]);
@@ -853,22 +858,24 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
         });
       });
     };
-    // both parts of two pairs of positions side by side
-    auto look_up_v = [&](auto kk, auto jc, auto tc) {
+    // the first parts of the positions' pairs (x = 0) or the second ones
+    auto look_up_v = [&](auto kk, auto jc, auto x) {
       uint32_t e[4];
-      unroll<0, 2>([&](auto ic) {
-        const uint32_t ad = table_address<kk % 4>(jc == 0 ? even[tc][ic] : odd[tc][ic], lane_off);
-        e[2 * ic] = *reinterpret_cast<const uint32_t *>(lds + ad);
-        e[2 * ic + 1] = *reinterpret_cast<const uint32_t *>(lds + ad + 128);
+      unroll<0, 4>([&](auto ic) {
+        constexpr int T = ic / 2, I = ic % 2;
+        const uint32_t ad =
+            table_address<kk % 4>(jc == 0 ? even[T][I] : odd[T][I], lane_off);
+        if constexpr (x == 0) e[ic] = *reinterpret_cast<const uint32_t *>(lds + ad);
+        else e[ic] = second_part(ad);
       });
       return make_uint4(e[0], e[1], e[2], e[3]);
     };
-    // [tile of elements][tile of positions], of this piece and the next
+    // [tile of elements][part], of this piece and the next
     uint4 vc[A::kAhead ? 2 : 1][2][2];
     auto look_up_piece = [&](auto kk) {
       if constexpr (kk % 4 == 0) merge_nibbles(std::integral_constant<int, kk / 4>{});
-      unroll<0, 2>([&](auto tc) {
-        unroll<0, 2>([&](auto jc) { vc[kk & 1][jc][tc] = look_up_v(kk, jc, tc); });
+      unroll<0, 2>([&](auto xc) {
+        unroll<0, 2>([&](auto jc) { vc[kk & 1][jc][xc] = look_up_v(kk, jc, xc); });
       });
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -878,17 +885,17 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       constexpr int B = K / PB;
       if constexpr (!A::kAhead && K % 4 == 0) merge_nibbles(std::integral_constant<int, K / 4>{});
       if constexpr (A::kAhead && K + 1 < P) look_up_piece(std::integral_constant<int, K + 1>{});
-      // weights twice, as both parts of a pair take the same
-      unroll<0, 2>([&](auto tc) {
+      unroll<0, 2>([&](auto xc) {
         unroll<0, 2>([&](auto jc) {
           uint4 v;
-          if constexpr (A::kAhead) v = vc[K & 1][jc][tc];
-          else v = look_up_v(kk, jc, tc);
+          if constexpr (A::kAhead) v = vc[K & 1][jc][xc];
+          else v = look_up_v(kk, jc, xc);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) {
             f32x4 &acc = o[nr][2 * K + jc];
-            acc = mfma16x16x32<kFP16>(v, twice<tc>(wh[nr][B]), acc);
-            if constexpr (A::kSplitW) acc = mfma16x16x32<kFP16>(v, twice<tc>(wl[nr][B]), acc);
+            acc = mfma16x16x32<kFP16>(v, wh[nr][B], acc);
+            // (the second parts' product, 2^-22 of a term at most, is left out)
+            if constexpr (xc == 0 && A::kSplitW) acc = mfma16x16x32<kFP16>(v, wl[nr][B], acc);
           }
         });
       });

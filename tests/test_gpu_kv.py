@@ -14,7 +14,9 @@ bit-exact. Attention is held to two derived bounds per case:
    (half a step). c: fp16's half step 2^-11 for bf16 rows (0 for E2M1 codes,
    which are exact), 2^-22 for fp16 rows and for fp32 rows, whose queries have two
    parts too. w:
-   2^-11 for bf16 rows, 2^-22 (two parts) otherwise.
+   2^-11 for bf16 rows, 2^-22 (two parts) otherwise, and for these 2^-22 more: the
+   product of the weights' and the values' second parts, each at most 2^-11 of the
+   whole, is left out.
    A floor is added, which shows where the largest weights meet zeros. The weight
    of position p enters the matrix cores as w = 2^(t - m) a / A 2^8 in fp16, whose
    half step below 2^-14 (and that of the second part of a two-part weight) is
@@ -299,7 +301,7 @@ def queries(total, heads, d, dtype, seed):
 def check_attention(got, want, spread, reach, dtype, quant, d, longest, nat, norm=True):
     c = {"bf16": 2.0 ** -11, "fp16": 2.0 ** -22, "fp32": 2.0 ** -22}[dtype]
     c = 0.0 if quant == "fp4" else c
-    w = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22
+    w = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -21
     r = (c + (d + 16) * 2.0 ** -24) * reach + 2.0 ** -21
     if dtype == "fp32":
         r = r + 2.0 ** -22 * reach  # the queries' two parts
