@@ -730,3 +730,83 @@ def test_rows_past_max_rows_and_wide_arguments(nf4, orc):
     wide = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=6, max_len=1 << 40,
                             window=(1 << 32) + 5)
     check_attention(wide, *want, "bf16", "nf4", 128, 100, nat)
+
+
+def test_a_captured_step_follows_its_lengths(nf4):
+    """One captured step (write and attention) replayed while the lengths grow in place
+    past page ends, with a sequence that is padding (no pages, length 0) and rows behind
+    the last offset: bitwise the eager steps on another cache, padding rows zeros."""
+    g = torch.Generator(device="cuda").manual_seed(950)
+    caches = [nf4.KVCache.empty(40, 16, 2, 128) for _ in range(2)]
+    wide = torch.full((4, 12), -1, dtype=torch.int32)
+    wide[:3, 2:11] = torch.randperm(40)[:27].view(3, 9).to(torch.int32)
+    table = wide.cuda()[:, 2:11]  # a slice of a wider table
+    lens = torch.tensor([14, 100, 1, 0], dtype=torch.int32).cuda()
+    grow = torch.tensor([1, 1, 1, 0], dtype=torch.int32).cuda()
+    off = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32).cuda()
+    k, v = (torch.empty(6, 2, 128, device="cuda", dtype=torch.float16) for _ in range(2))
+    q = torch.empty(6, 8, 128, device="cuda", dtype=torch.float16)
+    start = torch.randn(2, 115, 2, 128, generator=g, device="cuda").half()
+    start_off = torch.tensor([0, 14, 114, 115, 115], dtype=torch.int32).cuda()
+    for c in caches:
+        nf4.kv_write(c, start[0], start[1], table, lens, start_off)
+    outs = [torch.empty_like(q) for _ in caches]
+
+    def step(i):
+        nf4.kv_write(caches[i], k, v, table, lens, off)
+        nf4.kv_attention(q, caches[i], table, lens, off, max_rows=1, max_len=1 << 14, out=outs[i])
+
+    def inputs():
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+
+    inputs()
+    lens += grow
+    step(0)
+    step(1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(0)
+    for i in range(36):
+        inputs()
+        lens += grow
+        for o in outs:
+            o.fill_(5.0)
+        graph.replay()
+        step(1)
+        torch.cuda.synchronize()
+        assert same(*outs), i
+        assert torch.all(outs[0][3] == 0) and torch.all(outs[0][4:] == 5.0)
+        assert torch.isfinite(outs[0]).all()
+    # the same pages in both caches (those of the table: others are uninitialised)
+    used = table[:3].long().unique()
+    n = torch.zeros(40, 16, dtype=torch.bool, device="cuda")
+    for b in range(3):
+        for p in range(int(lens[b])):
+            n[table[b, p // 16].long(), p % 16] = True
+    for name in ("k_absmax", "v_absmax"):
+        a, b = (getattr(c, name) for c in caches)
+        at = n[:, None, :, None].expand_as(a)
+        assert same(a[at], b[at])
+    assert len(used) == 27
+
+
+def test_calls_at_once_on_one_cache(nf4, orc):
+    """Several calls in flight on streams of their own, each split and with a workspace of
+    its own: each is what it is alone."""
+    case = ("bf16", "nf4", 128, 64, 8, 2, 16, [3000, 2500], [1, 1], True, 0)
+    a, want, (call, cache, q, nat) = run_attention(nf4, orc, case, 960, max_len=3000)
+    where = gpu_call(call)
+    qs = [(q.float() * f).to(q.dtype).cuda() for f in (1.0, 0.5, 0.25, 2.0)]
+    alone = [nf4.kv_attention(x, cache, *where, max_rows=1, max_len=3000) for x in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(5):
+        got = []
+        for s, x in zip(streams, qs):
+            with torch.cuda.stream(s):
+                got.append(nf4.kv_attention(x, cache, *where, max_rows=1, max_len=3000))
+        torch.cuda.synchronize()
+        assert all(same(x, y) for x, y in zip(alone, got))
+    assert same(alone[0], a)
