@@ -158,6 +158,7 @@ def test_workspace_query(kv):
         assert q(*bad) == -1, bad
     assert q(1, 1, 1, 8, 8, 128, window=-1) == -1
     assert kv._lib().nf4_kv_attention_workspace_bytes(1, 1, 1, 8, 8, 128, 3, 0) == -1
+    assert q(1, 1, 1, 65536, 1, 128) == -1 and q(1, 1, 1, 65535, 1, 128) >= 0
     assert q(0, 1, 100, 8, 8, 128) == 0 and q(1, 0, 100, 8, 8, 128) == 0
     assert q(1, 1, 1, 8, 8, 128) == 0
     # a long sequence and few heads is split: fp32 sums of 128 columns and two statistics a row
