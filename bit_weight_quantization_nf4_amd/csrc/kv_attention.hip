@@ -31,7 +31,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(Attn
   const Block blk = block_of(args, sequence_of(args, seq), wb * args.wg_rows, args.wg_rows);
   if (pair >= blk.pairs) return;
   const int range = range_of(blk, args.splits, align);
-  const int pieces = range > 0 ? (blk.hi - blk.lo + range - 1) / range : 0;
+  const int pieces = range > 0 ? (blk.hi - blk.lo - 1) / range + 1 : 0;  // (no sum past 2^31)
   const int64_t base = item_of(args, seq, h, wb) * args.splits * args.part_rows + row;
   auto part_row = [&](int i) { return base + (int64_t)i * args.part_rows; };
 

@@ -810,3 +810,32 @@ def test_calls_at_once_on_one_cache(nf4, orc):
         torch.cuda.synchronize()
         assert all(same(x, y) for x, y in zip(alone, got))
     assert same(alone[0], a)
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_the_longest_sequence(nf4, rows):
+    """2^31 - 2^20 positions (the most) and a length past them, in a table that repeats one
+    page and ends in another: every score is 0, values are 1 and in the last page 2^15.
+    A lane adds up 2^31 / (512 ranges 8 waves 32) = 2^14 steps of 8 positions, each addition
+    off by 2^-24 of the sum, so sums and their quotient by 2^-9 at most."""
+    page, most = 1 << 16, (1 << 31) - (1 << 20)
+    cols = most // page
+    cache = nf4.KVCache.empty(2, page, 1, 64, 64)
+    cache.k_packed.fill_(0x35)
+    cache.k_absmax.fill_(1.0)
+    cache.v_packed.fill_(0xff)  # twice the code of 1
+    cache.v_absmax[0] = 1.0
+    cache.v_absmax[1] = 2.0 ** 15
+    table = torch.zeros(1, cols + 40, dtype=torch.int32, device="cuda")
+    table[0, cols - 1:] = 1
+    q = torch.zeros(rows, 1, 64, device="cuda")
+    want = torch.tensor(((most - page) + page * 2.0 ** 15) / most)
+    for n in (most, (1 << 31) - 1):
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        o = nf4.kv_attention(q, cache, table, lens, causal=False).cpu()
+        assert torch.all((o - want).abs() <= 2.0 ** -9 * want), (n, o[0, 0, 0])
+        # the window of the last positions alone
+        o = nf4.kv_attention(q, cache, table, lens, causal=False, window=1000).cpu()
+        assert torch.all((o - 2.0 ** 15).abs() <= 2.0 ** -9 * 2.0 ** 15)
+    k, v = nf4.kv_read(cache, rows, table, lens, dtype=torch.float32)
+    assert torch.all(v == 2.0 ** 15)
