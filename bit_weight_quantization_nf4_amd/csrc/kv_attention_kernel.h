@@ -336,9 +336,11 @@ struct Attn {
   // with four the others fill the wait, and the registers are needed
   static constexpr bool kAhead = kWavesPerSimd < 4 && !(kSplitQ && D > 128);
   // the merge of the waves' results handles this many rows and columns at once, so
-  // that its buffer and the table leave room for a second workgroup where there is one
+  // that its buffer and the table leave room for a second workgroup where there is one.
+  // It goes by whole 32-wide pieces: half of 96 columns would end inside one
   static constexpr int kMergeRows = kWavesPerSimd == 4 ? 4 : 16;
-  static constexpr int kMergeCols = kWavesPerSimd == 4 || D > 128 ? D / 2 : D;
+  static constexpr int kMergeCols = (kWavesPerSimd == 4 || D > 128) && P % 2 == 0 ? D / 2 : D;
+  static_assert(kMergeCols % 32 == 0 && D % kMergeCols == 0, "whole pieces");
   static constexpr int kMergeStride = kMergeCols + 4;
   static constexpr int kMergeFloats = MERGE ? kWaves * kMergeRows * kMergeStride : 1;
 };
@@ -366,6 +368,10 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   __shared__ float wave_l[MERGE ? kWaves : 1][A::kRows];
   __shared__ float total_l[A::kRows];
   __shared__ float wave_top[kWaves][16];
+  // as many workgroups of a CU's 160 KB as the registers allow
+  static_assert(A::kWavesPerSimd * 4 / kWaves *
+                        (sizeof(lds) + sizeof(merge_buf) + sizeof(wave_m) + sizeof(wave_l) +
+                         sizeof(total_l) + sizeof(wave_top)) <= 160 * 1024, "LDS");
 
   fetch_args();
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
