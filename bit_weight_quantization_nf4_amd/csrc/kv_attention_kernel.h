@@ -7,9 +7,10 @@
 //   out_i = sum_j 2^(t_ij - m_i) av_j c'v_j / (mu sum_j 2^(t_ij - m_i)),
 // one pass over the positions with a running reference m_i. m_i follows the
 // maximum only when a score passes it by 4 (2^4 still fits everything below),
-// so the accumulators are rarely rescaled; V's scales have such a reference A,
-// a power of two that follows their maximum when it is passed 8-fold. The
-// weights w = 2^(t - m) av / A 2^8 <= 2^15 go to the matrix cores in fp16.
+// so the accumulators are rarely rescaled; V's scales have such a reference A_i,
+// a power of two that follows the maximum over the positions that the row sees when it
+// is passed 8-fold. The weights w = 2^(t - m_i) av / A_i 2^8 <= 2^15 go to the matrix
+// cores in fp16: a position that a row does not see has no part in its rounding.
 //
 // Both products run transposed on 16x16x32 fp16 MFMA tiles: S^T = K Q^T leaves
 // lane (n = lane & 15, g = lane >> 4) with query row n and positions 16 t + 4 g +
@@ -443,8 +444,8 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   // both tiles of a step in one page, which holds an even number of them
   const bool paired = (tiles_per_page & 1) == 0;
   const int tile0 = (begin >> 4) + 2 * tw;
-  int col = nsteps > 0 ? tile0 / tiles_per_page : 0;
-  int in_page = tile0 - col * tiles_per_page;
+  const int first_col = nsteps > 0 ? tile0 / tiles_per_page : 0;
+  int col = first_col, in_page = tile0 - first_col * tiles_per_page;
   const int step_cols = pin(2 * TW / tiles_per_page);
   const int step_in_page = pin(2 * TW - step_cols * tiles_per_page);
   auto advance = [&] {
@@ -498,14 +499,26 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     }
     return p;
   };
+  // where a window leaves no position of the wave's first step to all rows, that step comes
+  // last: their common A is then known (52 rows of 16 sequences in a window of 1024: 14.2
+  // us, 15.2 in order)
+  int step = nsteps > 1 && blk.all_lo >= begin + kStep * (tw + 1) ? 1 : 0;
+  if (step > 0) advance();
   StepIn<D, BS> in;
   // the scales that the lane holds: values 16 u + n of the DPP row's 8 positions
+  auto scale_index = [&](int u) {
+    const int v = 16 * u + n;
+    return v < 8 * NB ? v : v % (8 * NB);
+  };
+  // and their positions in the step
+  auto position_of = [&](int u) {
+    const int tk = scale_index(u) / NB;
+    return 16 * (tk >> 2) + 4 * g + (tk & 3);
+  };
   auto load_scales = [&](float (&s)[NS], const GlobalF32 (&base)[2]) {
 #pragma unroll
     for (int u = 0; u < NS; ++u) {
-      int v = 16 * u + n;
-      v = v < 8 * NB ? v : v % (8 * NB);
-      const int tk = v / NB;
+      const int v = scale_index(u), tk = v / NB;
       s[u] = (tk < 4 ? base[0] : base[1])[(uint32_t)((4 * g + (tk & 3)) * NB + (v - tk * NB))];
     }
   };
@@ -654,7 +667,16 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     else return ql[nrc][cc];
   };
 
-  // ---- state: m_ref is -inf before a row has seen anything; m_use stands for it
+  // ---- state. Of a row: its reference m is held as m_use = m - e and l_sum carries 2^e,
+  // where 2^(a_exp - e) is its A: the scales, which the wave's rows share, are multiplied
+  // by 2^(8 - a_exp), and a row's part 2^e of 2^8 / A comes with its exponentials. m_limit
+  // is 4 + e (kNothing, kZeros: e = 0), so the three are all there is; e is 0 but where
+  // rows have seen scales of different size.
+  constexpr float kNothing = -__builtin_inff();  // no position seen
+  constexpr float kZeros = 3.5f;                 // only scales of 0 (A is still open)
+  auto e_of = [](float limit) {
+    return limit == kNothing || limit == kZeros ? 0.0f : limit - 4.0f;
+  };
   f32x4 o[NR][2 * P];
   float m_use[NR], m_limit[NR], l_sum[NR];
 #pragma unroll
@@ -662,17 +684,30 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
 #pragma unroll
     for (int j = 0; j < 2 * P; ++j) o[nr][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     m_use[nr] = 0.0f;
-    m_limit[nr] = -__builtin_inff();  // a score past m_use by more moves the reference
+    m_limit[nr] = kNothing;  // a score past m_use by more moves the reference
     l_sum[nr] = 0.0f;
   }
-  int a_exp = -1000;      // A = 2^a_exp
-  float a_inv = 0.0f;     // 2^8 / A
-  float a_limit = -1.0f;  // 8 A
+  constexpr int kStart = -1000;  // before any row has seen a scale that is not 0
+  // from -119 to 127: 2^(8 - a_exp) is finite, and smaller scales are exact in fp16 steps
+  // finer than the result's
+  constexpr int kLeast = -119, kMost = 127;
+  int a_exp = kStart;
+  float a_inv = 1.0f;    // 2^(8 - a_exp)
+  float a_limit = 0.0f;  // 8 times the least A of a row
+  bool even = true;      // one A for all rows, e = 0
 
-  const int all_lo = pin(blk.all_lo), all_hi = pin(blk.all_hi), len = pin(blk.len);
+  const int all_lo = pin(blk.all_lo), all_hi = pin(blk.all_hi);
+  const int any_hi = pin(blk.hi);
   for (int s = 0; s < nsteps; ++s) {
-    const int pos0 = begin + kStep * (tw + TW * s);
-    if (s + 1 < nsteps) advance();  // the last step loads its own inputs again
+    const int pos0 = begin + kStep * (tw + TW * step);
+    if (s + 1 < nsteps) {  // the last one loads its own inputs again
+      advance();
+      if (++step == nsteps) {
+        step = 0;
+        col = first_col;
+        in_page = tile0 - first_col * tiles_per_page;
+      }
+    }
     const Where next_at = locate();
     const bool ok[2] = {ok0, ok1};
     // every row sees the whole step (uniform)
@@ -766,20 +801,17 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
             const bool see = ok[T] && p >= row_lo[nr] && p < row_hi[nr];
             t[nr][T][r] = see ? t[nr][T][r] : -__builtin_inff();
           }
-      // scales of positions that are not there may be anything
+      // scales of positions that no row sees may be anything
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
-        int v = 16 * u + n;
-        v = v < 8 * NB ? v : v % (8 * NB);
-        const int tk = v / NB;
-        const int p = pos0 + 16 * (tk >> 2) + 4 * g + (tk & 3);
-        vs[u] = p < len && (tk < 4 ? ok[0] : ok[1]) ? vs[u] : 0.0f;
+        const int p = position_of(u);
+        vs[u] = pos0 + p < any_hi && (p < 16 ? ok[0] : ok[1]) ? vs[u] : 0.0f;
       }
     }
 
     // ---- references
     float top[NR];
-    bool far = false;
+    bool far = false, far_scale = false;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
       const f32x4 u = t[nr][0], v = t[nr][1];
@@ -787,39 +819,127 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       far = far || top[nr] > m_limit[nr];
     }
 #pragma unroll
-    for (int u = 0; u < NS; ++u) far = far || fabsf(vs[u]) > a_limit;
-    if (__builtin_amdgcn_ballot_w64(far) != 0) {
-      float av = 0.0f;  // of the finite ones: an infinity is its own rows' matter
+    for (int u = 0; u < NS; ++u) far_scale = far_scale || fabsf(vs[u]) > a_limit;
+    if (__builtin_amdgcn_ballot_w64(far || far_scale) != 0) {
+      // the scales, of the finite ones: an infinity is its own rows' matter
+      auto size = [&](int u) {
+        return fabsf(vs[u]) < __builtin_inff() ? fabsf(vs[u]) : 0.0f;
+      };
+      int ex = a_exp;
+      bool common = even;
+      if (__builtin_amdgcn_ballot_w64(far_scale) != 0) {
+        // one A for all rows, by the positions that all of them see, serves where no other
+        // scale is 8 times as large. (A of each row's own, which is longer, only where some
+        // position that not all rows see has a larger one.)
+        float av = 0.0f, any = 0.0f;
 #pragma unroll
-      for (int u = 0; u < NS; ++u)
-        av = fabsf(vs[u]) < __builtin_inff() ? max2(av, fabsf(vs[u])) : av;
-      av = max_over_groups(row16_max(av));
-      // 2^8 / A stays finite: from 2^127 on, smaller scales are exact in fp16 steps
-      // finer than the result's
-      int ex = __builtin_amdgcn_readfirstlane(av > 0.0f ? __builtin_amdgcn_frexp_expf(av) : -119);
-      ex = clamp_to(ex, -119, 127);
-      ex = ex > a_exp ? ex : a_exp;
-      const int shift = a_exp - ex;
-      a_exp = ex;
-      a_inv = __builtin_amdgcn_ldexpf(1.0f, 8 - ex);
-      a_limit = __builtin_amdgcn_ldexpf(8.0f, ex);
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-        const float mx = max_over_groups(top[nr]);
-        const bool fresh = m_limit[nr] != 4.0f;         // nothing seen before
-        const bool some = mx != -__builtin_inff();
-        // how far the reference moves: to the maximum, never back
-        const float move = !some ? 0.0f : (fresh ? mx : fmaxf(mx, 0.0f));
-        const float alpha = fresh ? 0.0f : __builtin_amdgcn_exp2f(-move);
-        const float beta = __builtin_amdgcn_ldexpf(alpha, shift);
-        m_use[nr] += move;
-        m_limit[nr] = some ? 4.0f : m_limit[nr];
-        l_sum[nr] *= alpha;
-#pragma unroll
-        for (int T = 0; T < 2; ++T) t[nr][T] -= move;
-#pragma unroll
-        for (int j = 0; j < 2 * P; ++j) o[nr][j] *= beta;
+        for (int u = 0; u < NS; ++u) {
+          any = max2(any, size(u));
+          const int p = pos0 + position_of(u);
+          av = max2(av, whole || (p >= all_lo && p < all_hi) ? size(u) : 0.0f);
+        }
+        av = max_over_groups(row16_max(av));
+        ex = __builtin_amdgcn_readfirstlane(
+            av > 0.0f ? clamp_to(__builtin_amdgcn_frexp_expf(av), kLeast, kMost) : kStart);
+        ex = ex > a_exp ? ex : a_exp;
+        common = even && __builtin_amdgcn_ballot_w64(any > __builtin_amdgcn_ldexpf(8.0f, ex)) == 0;
       }
+      if (common) {
+        const int fall = a_exp - ex;
+        a_exp = ex;
+        a_limit = __builtin_amdgcn_ldexpf(8.0f, ex);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          const float mx = max_over_groups(top[nr]);
+          const bool first = m_limit[nr] == kNothing;
+          const bool some = mx != -__builtin_inff();
+          // how far the reference moves: to the maximum, never back
+          const float move = !some ? 0.0f : (first ? mx : fmaxf(mx, 0.0f));
+          const float alpha = first ? 0.0f : __builtin_amdgcn_exp2f(-move);
+          const float beta = __builtin_amdgcn_ldexpf(alpha, fall);
+          m_use[nr] += move;
+          m_limit[nr] = some ? 4.0f : m_limit[nr];
+          l_sum[nr] *= alpha;
+#pragma unroll
+          for (int T = 0; T < 2; ++T) t[nr][T] -= move;
+#pragma unroll
+          for (int j = 0; j < 2 * P; ++j) o[nr][j] *= beta;
+        }
+      } else {
+        // ---- A by row: the largest scale that a row sees
+        float sizes[NS], seen[NR];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) sizes[u] = size(u);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) seen[nr] = 0.0f;
+        unroll<0, 8>([&](auto ic) {
+          constexpr int T = ic / 4, R = ic % 4;
+          float scale = row_scale<ic * NB>(sizes);
+          unroll<1, NB>([&](auto bc) { scale = max2(scale, row_scale<ic * NB + bc>(sizes)); });
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+            seen[nr] = max2(seen[nr], t[nr][T][R] == -__builtin_inff() ? 0.0f : scale);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        // exponents of the rows' A before and after this step, and their range over the rows
+        constexpr float kNone = -1000.0f;
+        float was[NR], now[NR], lo = -kNone, hi = kNone;
+        bool without = false;  // a row that may come to see a scale, but has not
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          seen[nr] = max_over_groups(seen[nr]);
+          was[nr] = m_limit[nr] == kNothing || m_limit[nr] == kZeros || a_exp == kStart
+                        ? kNone
+                        : (float)a_exp - e_of(m_limit[nr]);
+          now[nr] = seen[nr] > 0.0f
+                        ? fmaxf(was[nr], (float)__builtin_amdgcn_frexp_expf(seen[nr]))
+                        : was[nr];
+          lo = now[nr] != kNone ? fminf(lo, now[nr]) : lo;
+          hi = fmaxf(hi, now[nr]);
+          without = without || (now[nr] == kNone && row_hi[nr] > 0);
+        }
+        lo = -row16_max(-lo);
+        hi = row16_max(hi);
+        // e = a_exp - (exponent of A) is 0 for the rows of the least A, unless a row's is
+        // more than 2^64 times that: then -64 for the greatest. It is 89 at most (the sum of
+        // 2^31 weights up to 2^(4 + 89) is in fp32's range), so A is more than a row's own
+        // scales ask for where another row's are 2^153 times as large.
+        ex = a_exp;
+        if (hi != kNone) ex = clamp_to((int)fmaxf(lo, hi - 64.0f), kLeast, kMost);
+        ex = __builtin_amdgcn_readfirstlane(ex);
+        // rows whose A are within the 8-fold of the least all take that one
+        even = __builtin_amdgcn_ballot_w64(without) == 0 &&
+               __builtin_amdgcn_readfirstlane((int)hi) <= ex + 3;
+        float least = -kNone;
+        bool open = false;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          const float mx = max_over_groups(top[nr]);
+          const bool first = m_limit[nr] == kNothing;
+          const bool some = mx != -__builtin_inff();
+          const bool scaled = now[nr] != kNone;
+          const float e_was = e_of(m_limit[nr]);
+          const float e = scaled && !even ? fminf((float)ex - now[nr], 89.0f) : 0.0f;
+          const float move = !some ? 0.0f : (first ? mx : fmaxf(mx - e_was, 0.0f));
+          const float alpha = first ? 0.0f : __builtin_amdgcn_exp2f(-move);
+          const float beta = __builtin_amdgcn_ldexpf(alpha, (int)(was[nr] - ((float)ex - e)));
+          const float shift = move - (e - e_was);
+          m_use[nr] += shift;
+          m_limit[nr] = first && !some ? kNothing : (scaled ? 4.0f + e : kZeros);
+          l_sum[nr] *= __builtin_amdgcn_ldexpf(alpha, (int)(e - e_was));
+          least = scaled ? fminf(least, (float)ex - e) : least;
+          open = open || m_limit[nr] == kZeros;
+#pragma unroll
+          for (int T = 0; T < 2; ++T) t[nr][T] -= shift;
+#pragma unroll
+          for (int j = 0; j < 2 * P; ++j) o[nr][j] *= beta;
+        }
+        a_exp = ex;
+        const int least_exp = __builtin_amdgcn_readfirstlane((int)-row16_max(-least));
+        a_limit = __builtin_amdgcn_ballot_w64(open) != 0 ? 0.0f
+                                                         : __builtin_amdgcn_ldexpf(8.0f, least_exp);
+      }
+      a_inv = __builtin_amdgcn_ldexpf(1.0f, 8 - (a_exp > kLeast ? a_exp : kLeast));
     }
 
     // ---- weights. A scale of infinity or NaN stands as the largest number: times the
@@ -917,10 +1037,14 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
 
   // ---- results: a row's output, or its partial sums
   float l_row[NR], m_ref[NR];
+  int a_row[NR];  // exponents of 2^8 / A, undone apart from other factors: their product
+                  // may be subnormal
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) {
-    l_row[nr] = sum_over_groups(l_sum[nr]);
-    m_ref[nr] = m_limit[nr] == 4.0f ? m_use[nr] : -__builtin_inff();
+    const float e = e_of(m_limit[nr]);
+    l_row[nr] = __builtin_amdgcn_ldexpf(sum_over_groups(l_sum[nr]), -(int)e);
+    m_ref[nr] = m_limit[nr] == kNothing ? kNothing : m_use[nr] + e;
+    a_row[nr] = a_exp - (int)e - 8;
   }
   KernelArgs &end_args = *kernel_args();
   const int tid = fresh((int)threadIdx.x);
@@ -938,8 +1062,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       const int64_t part_row = part_row0 + wave * A::kRows + 16 * nr + n;
       const float f = !whole_item ? end_args.inv_mu
                                   : (l_row[nr] > 0.0f ? end_args.inv_mu / l_row[nr] : 0.0f);
-      // undo A apart from the factor: their product may be subnormal
-      auto undo = [&](float v) { return __builtin_amdgcn_ldexpf(v * f, a_exp - 8); };
+      auto undo = [&](float v) { return __builtin_amdgcn_ldexpf(v * f, a_row[nr]); };
       if (!whole_item && g == 0) end_args.stats[part_row] = make_float2(m_ref[nr], l_row[nr]);
       float *part = end_args.part + part_row * D + 8 * g;
       const int64_t at = out_at(16 * nr + n) + 8 * g;
@@ -1002,9 +1125,8 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
             unroll<0, MC / 32>([&](auto kc) {
               constexpr int K = K0 + kc;
               float *dst = merge_buf + (wave * MR + n - r0) * ML + 32 * kc + 8 * g;
-              // undo A apart from the factor: their product may be subnormal
               auto undo = [&](float v) {
-                return __builtin_amdgcn_ldexpf(v * factor[nr], a_exp - 8);
+                return __builtin_amdgcn_ldexpf(v * factor[nr], a_row[nr]);
               };
               const f32x4 e = o[nr][2 * K], d = o[nr][2 * K + 1];
               reinterpret_cast<f32x4 *>(dst)[0] =

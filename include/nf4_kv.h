@@ -128,7 +128,8 @@ int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_
  *   bf16 rows: the keys' code values (6e-5 relative in the norm) and the softmax
  *   weights carry 11 significant bits;
  *   all: a position's share e_p a / sum e is resolved to 2^-32 of the largest value
- *   scale a that the row sees, which only shows where scales differ by as much.
+ *   scale a that the row sees, which only shows where scales differ by as much. (Of
+ *   2^-150 of the largest one that any row sees, if that is more.)
  * A query that is not finite spoils its own row only, and a scale in the cache that
  * is not the rows that see its position.
  * max_rows: the most rows of any sequence (rows past it are left as they are; 0

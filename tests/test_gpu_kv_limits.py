@@ -1,0 +1,158 @@
+"""The 4-bit key/value cache at the ends of what include/nf4_kv.h promises. Bounds are
+test_gpu_kv.py's; the floor of a row (a position's weight in fp16 steps of 2^-32 of the
+largest value scale) is taken from the scales that this row sees.
+"""
+import pytest
+import torch
+
+import kv_reference as ref
+from test_gpu_kv import (DT, HALF, dense, device_cache, gpu_call, natural, nf4,  # noqa: F401
+                         queries, row_values, same)
+
+pytestmark = pytest.mark.gpu
+
+
+def largest_seen(call, a, heads, causal, window):
+    """[rows, heads, 1]: the largest scale of the positions that a row sees; a: the value
+    scales [pages, kv heads, page, blocks]."""
+    kvh = a.shape[1]
+    top = a.double().amax(-1)[..., None]
+    out = torch.zeros(call.total, kvh, 1, dtype=torch.float64)
+    row = 0
+    for b, n in enumerate(call.rows):
+        s, there = ref.sequence(call, top, b, kvh)
+        for i in range(n):
+            hi = call.lens[b] - n + i + 1 if causal else call.lens[b]
+            lo = max(0, hi - window) if window else 0
+            if hi > lo and there[lo:hi].any():
+                out[row] = s[:, lo:hi][:, there[lo:hi]].amax(1)
+            row += 1
+    return out.repeat_interleave(heads // kvh, 1)
+
+
+def check_rows(got, want, spread, reach, seen, dtype, quant, d, longest, rows=slice(None)):
+    """test_gpu_kv.py's bound element by element, with each row's own floor, and 2^-16 more
+    of a score: where value scales differ by powers of two, so may the reference that a
+    row's exponents are taken from, by less than 2^7, and four roundings of numbers below
+    that are half of 2^-17 each at most."""
+    c = 0.0 if quant == "fp4" else {"bf16": 2.0 ** -11, "fp16": 2.0 ** -22, "fp32": 2.0 ** -22}[dtype]
+    w = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -21
+    r = (c + (d + 16) * 2.0 ** -24) * reach + 2.0 ** -21 + 2.0 ** -16
+    if dtype == "fp32":
+        r = r + 2.0 ** -22 * reach
+    bound = spread * (2 * r + w + 2.0 ** -22 + 2 * (longest + 64) * 2.0 ** -24) + HALF[dtype] * want.abs()
+    if dtype == "fp16":
+        bound = bound + 2.0 ** -25
+    bound = bound + longest * 2.0 ** -32 * seen
+    got = got.double().cpu()
+    err = (got - want).abs()
+    assert torch.isfinite(got[rows]).all()
+    assert torch.all(err[rows] <= bound[rows]), ((err - bound)[rows]).max().item()
+
+
+# dtype, D, bs, heads, kv heads, lens, rows: waves that share a block of one tile, of two,
+# and waves with rows of their own
+BLOCKS = [
+    ("bf16", 128, 64, 4, 2, [75, 40], [5, 3]),
+    ("fp16", 64, 32, 4, 1, [90], [4]),
+    ("fp32", 128, 64, 4, 2, [75, 40], [5, 3]),
+    ("fp32", 256, 128, 2, 1, [60], [6]),
+    ("bf16", 128, 128, 8, 2, [170], [40]),
+    ("fp16", 96, 32, 4, 1, [100, 37], [37, 33]),
+    ("bf16", 128, 128, 64, 64, [140, 150, 131, 40], [128, 128, 100, 3]),
+    ("fp32", 64, 32, 64, 32, [90, 70] * 2, [64, 64] * 2),
+]
+
+
+@pytest.mark.parametrize("split", ["one", "many"])
+@pytest.mark.parametrize("case", BLOCKS, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_large_value_scales_reach_only_rows_that_see_them(nf4, orc, case, split):  # noqa: F811
+    """A value scale of 2^20, 2^40 or 3e38 at the newest position, which only the last row
+    of its sequence sees, and at one that a window has left behind for all but the first:
+    all other rows stay within the bounds of what they see. So does the row itself where
+    its type holds the result."""
+    dtype, d, bs, heads, kvh, lens, rows = case
+    call, pages = ref.make_call(lens, rows, 16, 920)
+    book = ref.codebook(orc, "nf4")
+    nat = ref.random_cache(book, pages, kvh, 16, d, bs, "nf4", 921)
+    k64 = dense(book, *nat[0], bs)
+    q = queries(call.total, heads, d, dtype, 922)
+    b, window = len(lens) - 1, 19
+    kw = dict(max_rows=max(rows), max_len=1 if split == "one" else 1 << 17, window=window)
+    first, last = call.total - rows[b], call.total - 1
+    for pos, row in ((lens[b] - 1, last), (lens[b] - rows[b] + 1 - window, first)):
+        if pos < 0:
+            continue
+        keep = [r for r in range(call.total) if r != row]
+        for big in (2.0 ** 20, 2.0 ** 40, 3e38):
+            codes, a = nat[1]
+            a = a.clone()
+            a[int(call.table[b, pos // 16]), :, pos % 16] = big
+            cache = device_cache(nf4, (nat[0], (codes, a)), bs, "nf4")
+            out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), **kw).cpu()
+            want = ref.attention(call, q, k64, dense(book, codes, a, bs), ref.sqrt_scale(d), True, window)
+            seen = largest_seen(call, a, heads, True, window)
+            check_rows(out, *want, seen, dtype, "nf4", d, max(lens), keep)
+            if dtype != "fp16" and big < 1e30:
+                check_rows(out, *want, seen, dtype, "nf4", d, max(lens), [row])
+
+
+@pytest.mark.parametrize("split", ["one", "many"])
+@pytest.mark.parametrize("case", BLOCKS, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_value_scales_that_grow_from_row_to_row(nf4, orc, case, split):  # noqa: F811
+    """The positions of the call's rows have scales that grow by 2^9 (or fall, or are zero
+    for some) from one to the next: every row is within the bounds of what it sees."""
+    dtype, d, bs, heads, kvh, lens, rows = case
+    call, pages = ref.make_call(lens, rows, 16, 930)
+    book = ref.codebook(orc, "nf4")
+    nat = ref.random_cache(book, pages, kvh, 16, d, bs, "nf4", 931)
+    k64 = dense(book, *nat[0], bs)
+    q = queries(call.total, heads, d, dtype, 932)
+    top = 12 if dtype == "fp16" else 108
+    for kind in ("grow", "fall", "zeros first"):
+        codes, a = nat[1]
+        a = a.clone()
+        for _, b, p, pg, at in call.places():
+            if pg < 0:
+                continue
+            i = p - (lens[b] - rows[b])
+            step = {"grow": 9 * i, "fall": -9 * i, "zeros first": 9 * i - 27}[kind]
+            a[pg, :, at] *= 2.0 ** max(-top, min(top, step))
+        if kind == "zeros first":  # what lies before the rows of the call
+            for b in range(len(lens)):
+                for p in range(lens[b] - rows[b] + 1):
+                    a[int(call.table[b, p // 16]), :, p % 16] = 0.0
+        cache = device_cache(nf4, (nat[0], (codes, a)), bs, "nf4")
+        out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=max(rows),
+                               max_len=1 if split == "one" else 1 << 17)
+        want = ref.attention(call, q, k64, dense(book, codes, a, bs), ref.sqrt_scale(d), True, 0)
+        check_rows(out, *want, largest_seen(call, a, heads, True, 0), dtype, "nf4", d, max(lens))
+
+
+@pytest.mark.parametrize("d,bs,heads,kvh,rows,window,lens", [
+    (64, 32, 8, 2, 5, 600, list(range(700, 733))),  # waves that share a block of two tiles
+    (128, 64, 4, 2, 3, 600, list(range(700, 733))),  # of one
+    (64, 64, 512, 128, 32, 100, [201, 219, 230]),  # rows of a wave's own
+])
+def test_windows_that_begin_anywhere_in_a_step(nf4, orc, d, bs, heads, kvh, rows, window, lens):  # noqa: F811
+    """Windows whose first positions are seen by some rows of a block alone, at every place
+    in a step; some of these positions have value scales of 2^30."""
+    call, pages = ref.make_call(lens, [rows] * len(lens), 16, 970)
+    book = ref.codebook(orc, "nf4")
+    nat = ref.random_cache(book, pages, kvh, 16, d, bs, "nf4", 971)
+    q = queries(call.total, heads, d, "bf16", 972)
+    k64 = dense(book, *nat[0], bs)
+    codes, a = nat[1]
+    for big in (False, True):
+        if big:
+            a = a.clone()
+            for b in range(0, len(lens), 2):
+                p = lens[b] - rows + 1 - window
+                a[int(call.table[b, p // 16]), :, p % 16] = 2.0 ** 30
+        cache = device_cache(nf4, (nat[0], (codes, a)), bs, "nf4")
+        want = ref.attention(call, q, k64, dense(book, codes, a, bs), ref.sqrt_scale(d), True, window)
+        seen = largest_seen(call, a, heads, True, window)
+        for max_len in (1, 1 << 17):
+            out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=rows,
+                                   max_len=max_len, window=window)
+            check_rows(out, *want, seen, "bf16", "nf4", d, window)
