@@ -560,7 +560,11 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   uint4 qh[NR][P];
   uint4 ql[A::kSplitQ && !MERGE ? NR : 1][A::kSplitQ && !MERGE ? P : 1];
   int row_lo[NR], row_hi[NR];  // positions the row sees
+  // a row's scores are its products times this. The products, below 2^31 times a key scale,
+  // are kept in range by 2^-31 with the key scales, unless a query of the wave's reaches
+  // 2^64: large scales have no finite scores there.
   float qscale[NR];
+  float key_factor = 1.0f;
   uint4 *const q_shared = reinterpret_cast<uint4 *>(merge_buf);  // [first, second parts][fragment][lane]
   {
     struct Raw { uint4 v[DT == kFP32 ? 2 : 1]; };
@@ -593,6 +597,16 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     auto exponent = [](float top) {
       return top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
     };
+    // qscale and key_factor from the rows' exponents
+    auto set_scales = [&](const int (&ex)[NR]) {
+      bool large = false;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) large = large || ex[nr] > 64;
+      const int down = __builtin_amdgcn_ballot_w64(large) != 0 ? 0 : 31;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) qscale[nr] = __builtin_amdgcn_ldexpf(args.f, ex[nr] - 15 + down);
+      key_factor = __uint_as_float(pin(down == 0 ? 0x3f800000u : 0x30000000u));  // 1, 2^-31
+    };
     auto convert = [&](const Raw &r, int ex, uint4 &hi, uint4 &lo) {
       uint32_t h16[4], l16[4];
 #pragma unroll
@@ -622,20 +636,21 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
         if (g == 0) wave_top[wave][n] = top;
       }
       lds_barrier();
+      int ex[NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         float top = wave_top[i * P][n];
 #pragma unroll
         for (int j = 1; j < P; ++j) top = max2(top, wave_top[i * P + j][n]);
-        const int ex = exponent(top);
-        qscale[i] = __builtin_amdgcn_ldexpf(args.f, ex - 15);
+        ex[i] = exponent(top);
         if (wave < NR * P && nr == i) {
           uint4 hi, lo;
-          convert(raw, ex, hi, lo);
+          convert(raw, ex[i], hi, lo);
           q_shared[64 * wave + lane] = hi;
           if constexpr (A::kSplitQ) q_shared[64 * (NR * P + wave) + lane] = lo;
         }
       }
+      set_scales(ex);
       lds_barrier();
 #pragma unroll
       for (int f = 0; f < NR * P; ++f) qh[f / P][f % P] = q_shared[64 * f + lane];
@@ -648,17 +663,18 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
           if (have_rows) raw[nr][c] = load_raw(nr, c);
       write_table();
       lds_barrier();
+      int ex[NR];
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         float top = 0.0f;
 #pragma unroll
         for (int c = 0; c < P; ++c) top = max2(top, largest(raw[nr][c]));
-        const int ex = exponent(max_over_groups(top));
-        qscale[nr] = __builtin_amdgcn_ldexpf(args.f, ex - 15);
+        ex[nr] = exponent(max_over_groups(top));
 #pragma unroll
         for (int c = 0; c < P; ++c)
-          convert(raw[nr][c], ex, qh[nr][c], ql[A::kSplitQ ? nr : 0][A::kSplitQ ? c : 0]);
+          convert(raw[nr][c], ex[nr], qh[nr][c], ql[A::kSplitQ ? nr : 0][A::kSplitQ ? c : 0]);
       }
+      set_scales(ex);
     }
   }
   // the second parts of a fragment
@@ -715,6 +731,9 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
 
     // ---- S^T = K Q^T, combined over blocks into log2 units past m_use
     f32x4 t[NR][2];
+    float ks[NS];
+#pragma unroll
+    for (int u = 0; u < NS; ++u) ks[u] = in.ks[u] * key_factor;
     // An entry's second parts. (volatile: fetched in one instruction with the first, they
     // would come beside them and be copied; 32.8 us instead of 30.8 at 8 sequences up to
     // 4000 positions, fp16, 32 of 32 heads.)
@@ -767,7 +786,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
         });
         unroll<0, 4>([&](auto rc) {
           constexpr int R = rc;
-          const float a = row_scale<(4 * T + R) * NB + B>(in.ks);
+          const float a = row_scale<(4 * T + R) * NB + B>(ks);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
             t[nr][T][R] = B == 0    ? acc[nr][R] * a

@@ -131,7 +131,8 @@ int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_
  *   scale a that the row sees, which only shows where scales differ by as much. (Of
  *   2^-150 of the largest one that any row sees, if that is more.)
  * A query that is not finite spoils its own row only, and a scale in the cache that
- * is not the rows that see its position.
+ * is not the rows that see its position. (Key scales of 2^96 and more overflow in up to
+ * 32 neighbouring rows of which one has a query of 2^64 or more; else in none.)
  * max_rows: the most rows of any sequence (rows past it are left as they are; 0
  * stands for total_rows); ignored without row_offsets. max_len: about the longest
  * kv_lens, which sizes the split of the positions over the device (any value gives

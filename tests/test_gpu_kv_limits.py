@@ -156,3 +156,45 @@ def test_windows_that_begin_anywhere_in_a_step(nf4, orc, d, bs, heads, kvh, rows
             out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=rows,
                                    max_len=max_len, window=window)
             check_rows(out, *want, seen, "bf16", "nf4", d, window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_key_scales_near_the_ends_of_fp32(nf4, orc, dtype):  # noqa: F811
+    """Keys of 2^n and queries of 2^-n (or the other way round) have ordinary scores. Keys
+    of 2^110 under ordinary queries have scores far apart: a row is the value of its
+    nearest key (E2M1 codes, whose products are exact, and a gap of 5e-4 of the largest
+    score at least, against 160 2^-24 of it that fp32 sums can be off by)."""
+    d, bs, heads, kvh, quant = 128, 64, 4, 2, "fp4"
+    call, pages = ref.make_call([75, 40], [5, 3], 16, 940)
+    book = ref.codebook(orc, quant)
+    nat = ref.random_cache(book, pages, kvh, 16, d, bs, quant, 941)
+    v64 = dense(book, *nat[1], bs)
+    seen = largest_seen(call, nat[1][1], heads, True, 0)
+    for n in (60, 100, 118, -60, -100):
+        codes, a = nat[0]
+        a = a * 2.0 ** n
+        q = (queries(call.total, heads, d, "fp32", 942) * 2.0 ** -n).to(DT[dtype])
+        cache = device_cache(nf4, ((codes, a), nat[1]), bs, quant)
+        for max_len in (1, 1 << 17):
+            out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=5, max_len=max_len)
+            want = ref.attention(call, q, dense(book, codes, a, bs), v64, ref.sqrt_scale(d), True, 0)
+            check_rows(out, *want, seen, dtype, quant, d, 75)
+    q = queries(call.total, heads, d, dtype, 943)
+    codes, a = nat[0]
+    a = a * 2.0 ** 110
+    k64 = dense(book, codes, a, bs)
+    row = 0
+    for b, n in enumerate(call.rows):  # the gaps, on the CPU
+        k, _ = ref.sequence(call, k64, b, kvh)
+        for i in range(n):
+            qr = q[row].double().reshape(kvh, heads // kvh, d)
+            ks = k[:, :call.lens[b] - n + i + 1]
+            two = torch.einsum("hgd,htd->hgt", qr, ks).topk(2, -1).values
+            reach = torch.einsum("hgd,htd->hgt", qr.abs(), ks.abs()).amax(-1)
+            assert torch.all(two[..., 0] - two[..., 1] >= 5e-4 * reach)
+            row += 1
+    cache = device_cache(nf4, ((codes, a), nat[1]), bs, quant)
+    want = ref.attention(call, q, k64, v64, ref.sqrt_scale(d), True, 0)
+    for max_len in (1, 1 << 17):
+        out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=5, max_len=max_len)
+        check_rows(out, want[0], want[1], torch.zeros_like(want[2]), seen, dtype, quant, d, 75)
