@@ -62,6 +62,16 @@ def kv_exported_names() -> list[str]:
     return [s[0] for s in _SIGNATURES]
 
 
+def _page_stride(shape, stride) -> int:
+    """Elements between pages of [pages, heads, positions, width], -1 where a page is not
+    contiguous. A dimension of one element may have any stride: it addresses nothing."""
+    pages, heads, n, w = shape
+    if pages and not ((stride[1] == n * w or heads == 1) and (stride[2] == w or n == 1) and
+                      (stride[3] == 1 or w == 1)):
+        return -1
+    return stride[0] if pages > 1 else heads * n * w
+
+
 class KVCache:
     """A paged 4-bit key/value cache: uint8 ``k_packed`` and ``v_packed`` [pages,
     kv heads, page_size, head_dim / 2] and fp32 ``k_absmax`` and ``v_absmax``
@@ -71,22 +81,25 @@ class KVCache:
 
     def __init__(self, k_packed: torch.Tensor, k_absmax: torch.Tensor, v_packed: torch.Tensor,
                  v_absmax: torch.Tensor, blocksize: int = 64, quant_type: str = "nf4"):
-        shape, stride = k_packed.shape, k_packed.stride()
-        sshape, sstride = k_absmax.shape, k_absmax.stride()
+        shape, sshape = k_packed.shape, k_absmax.shape
         if len(shape) != 4 or k_packed.dtype is not torch.uint8 or \
                 v_packed.dtype is not torch.uint8:
             raise ValueError("KVCache expects uint8 codes [pages, kv heads, page_size, head_dim / 2]")
         pages, heads, page_size, half = shape
         nb = 2 * half // blocksize if blocksize > 0 else 0
-        if v_packed.shape != shape or v_packed.stride() != stride or (
-                pages and stride[1:] != (page_size * half, half, 1)):
+        if v_packed.shape != shape:
+            raise ValueError("KVCache expects codes of one shape, contiguous in a page")
+        stride = _page_stride(shape, k_packed.stride())
+        if stride < 0 or _page_stride(shape, v_packed.stride()) != stride:
             raise ValueError("KVCache expects codes of one shape, contiguous in a page")
         if k_absmax.dtype is not torch.float32 or v_absmax.dtype is not torch.float32 or \
-                sshape != (pages, heads, page_size, nb) or \
-                v_absmax.shape != sshape or v_absmax.stride() != sstride or (
-                    pages and sstride[1:] != (page_size * nb, nb, 1)):
+                sshape != (pages, heads, page_size, nb) or v_absmax.shape != sshape:
             raise ValueError("KVCache expects fp32 scales [pages, kv heads, page_size, "
-                             "head_dim / blocksize], contiguous in a page")
+                             "head_dim / blocksize]")
+        sstride = _page_stride(sshape, k_absmax.stride())
+        if sstride < 0 or _page_stride(sshape, v_absmax.stride()) != sstride:
+            raise ValueError("KVCache expects scales contiguous in a page, keys' and values' "
+                             "pages equally far apart")
         index = k_packed.get_device()
         if index < 0 or k_absmax.get_device() != index or v_packed.get_device() != index or \
                 v_absmax.get_device() != index:
@@ -98,7 +111,7 @@ class KVCache:
         self.head_dim = 2 * half
         self.index = index  # of the GPU
         self.desc = KVCacheDesc(k_packed.data_ptr(), k_absmax.data_ptr(), v_packed.data_ptr(),
-                                v_absmax.data_ptr(), pages, stride[0], sstride[0], page_size, heads,
+                                v_absmax.data_ptr(), pages, stride, sstride, page_size, heads,
                                 2 * half, blocksize, _QT[quant_type])
 
     @property
@@ -143,11 +156,20 @@ def _rows(cache: KVCache, total: int, block_table, kv_lens, row_offsets, what: s
                       stride if batch > 1 else cols, cols, batch, total)
 
 
-def _strided(t: torch.Tensor) -> bool:
-    """Whether the ABI takes [rows, heads, head_dim] as it is."""
+def _strides(t: torch.Tensor):
+    """(row, head) strides of [rows, heads, head_dim] for the ABI, None where it does not
+    take the tensor as it is. The stride of a single row or head addresses nothing and may
+    be anything."""
     r, h, e = t.stride()
-    d, es = t.shape[2], t.element_size()
-    return (e == 1 and r >= d and h >= d and not (r * es | h * es | t.data_ptr()) & 15)
+    n, heads, d = t.shape
+    if n <= 1:
+        r = heads * d
+    if heads <= 1:
+        h = d
+    es = t.element_size()
+    if e == 1 and r >= d and h >= d and not (r * es | h * es | t.data_ptr()) & 15:
+        return r, h
+    return None
 
 
 def _empty_rows(t: torch.Tensor) -> torch.Tensor:
@@ -162,8 +184,9 @@ def _check_rows(t: torch.Tensor, cache: KVCache, what: str) -> None:
 
 
 def _aligned_copy(t: torch.Tensor) -> torch.Tensor:
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
+    u = t.contiguous()  # t itself where it was
+    dense = t.shape[1] * t.shape[2], t.shape[2]
+    return u if _strides(u) == dense else t.clone(memory_format=torch.contiguous_format)
 
 
 # the raw handle of a device's current stream: building a Stream object takes longer
@@ -193,11 +216,13 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torc
         _check_rows(t, cache, "kv_write")
     if k.dtype != v.dtype or k.shape != v.shape or k.shape[1] != cache.num_kv_heads:
         raise ValueError("kv_write expects k and v [rows, kv heads, head_dim] of one dtype")
-    if not (k.stride() == v.stride() and _strided(k) and _strided(v)):
+    strides = _strides(k)
+    if strides is None or _strides(v) != strides:
         k, v = _aligned_copy(k), _aligned_copy(v)
+        strides = _strides(k)
     rows = _rows(cache, k.shape[0], block_table, kv_lens, row_offsets, "kv_write")
     kq, vq = (_empty_rows(k), _empty_rows(k)) if values else (None, None)
-    rs, hs, _ = k.stride()
+    rs, hs = strides
     _call(cache, lambda stream: (_lib().nf4_kv_write(
         cache.desc, rows, k.data_ptr(), v.data_ptr(), rs, hs, _DT[k.dtype],
         kq.data_ptr() if values else None, vq.data_ptr() if values else None, stream),
@@ -220,12 +245,12 @@ def kv_read(cache: KVCache, rows: int, block_table: torch.Tensor, kv_lens: torch
         k, v = out
         for t in out:
             _check_rows(t, cache, "kv_read")
-            if t.shape != shape or t.dtype != k.dtype or t.stride() != k.stride() or \
-                    not _strided(t):
+            if t.shape != shape or t.dtype != k.dtype or _strides(t) is None or \
+                    _strides(t) != _strides(k):
                 raise ValueError("kv_read: out must be two [rows, kv heads, head_dim] tensors of "
                                  "one dtype and layout, with 16-byte aligned heads")
     desc = _rows(cache, rows, block_table, kv_lens, row_offsets, "kv_read")
-    rs, hs, _ = k.stride()
+    rs, hs = _strides(k)
     _call(cache, lambda stream: (_lib().nf4_kv_read(
         cache.desc, desc, _DT[k.dtype], k.data_ptr(), v.data_ptr(), rs, hs, stream),
         "nf4_kv_read"))
@@ -255,12 +280,16 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
     total, heads, d = q.shape
     if out is None:
         out = _empty_rows(q)
+        out_strides = heads * d, d
     else:
         _check_rows(out, cache, "kv_attention")
-        if out.shape != q.shape or out.dtype != q.dtype or not _strided(out):
+        out_strides = _strides(out)
+        if out.shape != q.shape or out.dtype != q.dtype or out_strides is None:
             raise ValueError("kv_attention: out must be like q, with 16-byte aligned heads")
-    if not _strided(q):
+    strides = _strides(q)
+    if strides is None:
         q = _aligned_copy(q)
+        strides = _strides(q)
     rows = _rows(cache, total, block_table, kv_lens, row_offsets, "kv_attention")
     if heads % cache.num_kv_heads:
         raise ValueError("kv_attention expects a multiple of the cache's heads")
@@ -272,8 +301,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
         max_len = rows.table_cols * cache.page_size
     # what does not fit 32 bits is past every position
     max_rows, max_len, window = (min(n, 0x7ff00000) for n in (max_rows, max_len, window))
-    qr, qh, _ = q.stride()
-    orow, ohead, _ = out.stride()
+    qr, qh = strides
+    orow, ohead = out_strides
     kv_heads, dt = cache.num_kv_heads, _DT[q.dtype]
 
     def run(stream):

@@ -198,3 +198,58 @@ def test_key_scales_near_the_ends_of_fp32(nf4, orc, dtype):  # noqa: F811
     for max_len in (1, 1 << 17):
         out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=5, max_len=max_len)
         check_rows(out, want[0], want[1], torch.zeros_like(want[2]), seen, dtype, quant, d, 75)
+
+
+def test_strides_of_one_row_and_one_head_do_not_matter(nf4, orc):  # noqa: F811
+    """A dimension of one element may have any stride: keys, values, queries, outputs and
+    caches that differ there alone give what dense ones give, with no copy of an output."""
+    d, bs, page, heads, kvh = 128, 64, 16, 4, 2
+    call, pages = ref.make_call([20], [1], page, 960)
+    book = ref.codebook(orc, "nf4")
+    nat = ref.random_cache(book, pages, kvh, page, d, bs, "nf4", 961)
+    one, two = device_cache(nf4, nat, bs, "nf4"), device_cache(nf4, nat, bs, "nf4")
+    where = gpu_call(call)
+
+    def odd(t):  # the same elements, the row 3 elements off a multiple of 16 bytes
+        room = torch.zeros(3 * (t.shape[1] * d + 3), dtype=t.dtype, device="cuda")
+        view = room.as_strided((3, t.shape[1], d), (t.shape[1] * d + 3, d, 1))[:1]
+        view.copy_(t)
+        return view
+
+    k, v = (row_values((1, kvh, d), "bf16", 962 + i).cuda() for i in range(2))
+    q = queries(1, heads, d, "bf16", 964).cuda()
+    want = nf4.kv_write(one, k, v, *where, values=True)
+    got = nf4.kv_write(two, odd(k), odd(v), *where, values=True)
+    assert all(same(a, b) for a, b in zip(want, got))
+    for (c0, a0), (c1, a1) in zip(natural(one), natural(two)):
+        assert torch.equal(c0, c1) and same(a0, a1)
+    o = nf4.kv_attention(q, one, *where)
+    assert same(nf4.kv_attention(odd(q), one, *where), o)
+    out = odd(torch.zeros_like(q))
+    assert nf4.kv_attention(q, one, *where, out=out) is out and same(out, o)
+    pair = odd(torch.zeros_like(k)), torch.zeros_like(v)
+    nf4.kv_read(one, 1, *where, out=pair)
+    assert same(pair[0], want[0]) and same(pair[1], want[1])
+    # one kv head: pages [pages, page_size, 1, ...] seen as [pages, 1, page_size, ...]
+    nat = ref.random_cache(book, pages, 1, page, d, 128, "nf4", 965)
+    plain = device_cache(nf4, nat, 128, "nf4")
+    turned = nf4.KVCache(*(t.squeeze(1).unsqueeze(2).transpose(1, 2) for t in
+                           (plain.k_packed, plain.k_absmax, plain.v_packed, plain.v_absmax)), 128, "nf4")
+    assert turned.k_packed.stride(1) == d // 2
+    assert same(nf4.kv_attention(q, turned, *where), nf4.kv_attention(q, plain, *where))
+    # one head of queries, its stride odd
+    q1 = q[:, :1]
+    lone = torch.zeros(1, 1, d, dtype=q.dtype, device="cuda").as_strided((1, 1, d), (5, 3, 1))
+    lone.copy_(q1)
+    assert same(nf4.kv_attention(lone, plain, *where), nf4.kv_attention(q1.contiguous(), plain, *where))
+    # one page
+    single = nf4.KVCache.empty(1, page, kvh, d, bs)
+    for t in (single.k_packed, single.v_packed):
+        t.fill_(0x5a)
+    for t in (single.k_absmax, single.v_absmax):
+        t.fill_(0.5)
+    loose = nf4.KVCache(*(t.as_strided(t.shape, (7, *t.stride()[1:])) for t in
+                          (single.k_packed, single.k_absmax, single.v_packed, single.v_absmax)), bs, "nf4")
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([9], dtype=torch.int32, device="cuda")
+    assert same(nf4.kv_attention(q, loose, table, lens), nf4.kv_attention(q, single, table, lens))
