@@ -683,15 +683,16 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     else return ql[nrc][cc];
   };
 
-  // ---- state. Of a row: its reference m is held as m_use = m - e and l_sum carries 2^e,
-  // where 2^(a_exp - e) is its A: the scales, which the wave's rows share, are multiplied
-  // by 2^(8 - a_exp), and a row's part 2^e of 2^8 / A comes with its exponentials. m_limit
-  // is 4 + e (kNothing, kZeros: e = 0), so the three are all there is; e is 0 but where
-  // rows have seen scales of different size.
+  // ---- state. A row's A is 2^(a_exp - e): the scales, which the wave's rows share, are
+  // multiplied by 2^(8 - a_exp), and a row's part 2^e of 2^8 / A goes to its exponentials
+  // (l_sum carries it too). e is 0 but where rows have seen scales of different size (`even`
+  // is false). It is kept in m_limit, as e + 128 of the last steps past 4: no register of its
+  // own. There 0 stands for a row that has seen scales of 0 only (its A is still open, e = 0).
   constexpr float kNothing = -__builtin_inff();  // no position seen
-  constexpr float kZeros = 3.5f;                 // only scales of 0 (A is still open)
+  auto limit_of = [](int e) { return __uint_as_float(0x40800000u + (uint32_t)(e + 128)); };
+  constexpr float kZeros = 4.0f;
   auto e_of = [](float limit) {
-    return limit == kNothing || limit == kZeros ? 0.0f : limit - 4.0f;
+    return limit == kNothing || limit == kZeros ? 0 : (int)(__float_as_uint(limit) & 255u) - 128;
   };
   f32x4 o[NR][2 * P];
   float m_use[NR], m_limit[NR], l_sum[NR];
@@ -709,7 +710,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   constexpr int kLeast = -119, kMost = 127;
   int a_exp = kStart;
   float a_inv = 1.0f;    // 2^(8 - a_exp)
-  float a_limit = 0.0f;  // 8 times the least A of a row
+  float a_limit = 0.0f;  // 8 A, where it is the same for all rows
   bool even = true;      // one A for all rows, e = 0
 
   const int all_lo = pin(blk.all_lo), all_hi = pin(blk.all_hi);
@@ -877,7 +878,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
           const float alpha = first ? 0.0f : __builtin_amdgcn_exp2f(-move);
           const float beta = __builtin_amdgcn_ldexpf(alpha, fall);
           m_use[nr] += move;
-          m_limit[nr] = some ? 4.0f : m_limit[nr];
+          m_limit[nr] = some ? limit_of(0) : m_limit[nr];
           l_sum[nr] *= alpha;
 #pragma unroll
           for (int T = 0; T < 2; ++T) t[nr][T] -= move;
@@ -901,62 +902,53 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
           __builtin_amdgcn_sched_barrier(0);
         });
         // exponents of the rows' A before and after this step, and their range over the rows
-        constexpr float kNone = -1000.0f;
-        float was[NR], now[NR], lo = -kNone, hi = kNone;
+        constexpr int kNone = -1000;
+        int was[NR], now[NR];
+        float lo = -kNone, hi = kNone;
         bool without = false;  // a row that may come to see a scale, but has not
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
           seen[nr] = max_over_groups(seen[nr]);
           was[nr] = m_limit[nr] == kNothing || m_limit[nr] == kZeros || a_exp == kStart
                         ? kNone
-                        : (float)a_exp - e_of(m_limit[nr]);
-          now[nr] = seen[nr] > 0.0f
-                        ? fmaxf(was[nr], (float)__builtin_amdgcn_frexp_expf(seen[nr]))
-                        : was[nr];
-          lo = now[nr] != kNone ? fminf(lo, now[nr]) : lo;
-          hi = fmaxf(hi, now[nr]);
+                        : a_exp - e_of(m_limit[nr]);
+          const int e_seen = seen[nr] > 0.0f ? __builtin_amdgcn_frexp_expf(seen[nr]) : kNone;
+          now[nr] = e_seen > was[nr] ? e_seen : was[nr];
+          lo = now[nr] != kNone ? fminf(lo, (float)now[nr]) : lo;
+          hi = fmaxf(hi, (float)now[nr]);
           without = without || (now[nr] == kNone && row_hi[nr] > 0);
         }
-        lo = -row16_max(-lo);
-        hi = row16_max(hi);
+        const int low = __builtin_amdgcn_readfirstlane((int)-row16_max(-lo));
+        const int high = __builtin_amdgcn_readfirstlane((int)row16_max(hi));
         // e = a_exp - (exponent of A) is 0 for the rows of the least A, unless a row's is
         // more than 2^64 times that: then -64 for the greatest. It is 89 at most (the sum of
         // 2^31 weights up to 2^(4 + 89) is in fp32's range), so A is more than a row's own
         // scales ask for where another row's are 2^153 times as large.
-        ex = a_exp;
-        if (hi != kNone) ex = clamp_to((int)fmaxf(lo, hi - 64.0f), kLeast, kMost);
-        ex = __builtin_amdgcn_readfirstlane(ex);
+        if (high != kNone) ex = clamp_to(low > high - 64 ? low : high - 64, kLeast, kMost);
+        else ex = a_exp;
         // rows whose A are within the 8-fold of the least all take that one
-        even = __builtin_amdgcn_ballot_w64(without) == 0 &&
-               __builtin_amdgcn_readfirstlane((int)hi) <= ex + 3;
-        float least = -kNone;
-        bool open = false;
+        even = __builtin_amdgcn_ballot_w64(without) == 0 && high <= ex + 3;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
           const float mx = max_over_groups(top[nr]);
           const bool first = m_limit[nr] == kNothing;
           const bool some = mx != -__builtin_inff();
           const bool scaled = now[nr] != kNone;
-          const float e_was = e_of(m_limit[nr]);
-          const float e = scaled && !even ? fminf((float)ex - now[nr], 89.0f) : 0.0f;
-          const float move = !some ? 0.0f : (first ? mx : fmaxf(mx - e_was, 0.0f));
+          const int e = scaled && !even ? (ex - now[nr] < 89 ? ex - now[nr] : 89) : 0;
+          const float move = !some ? 0.0f : (first ? mx : fmaxf(mx, 0.0f));
           const float alpha = first ? 0.0f : __builtin_amdgcn_exp2f(-move);
-          const float beta = __builtin_amdgcn_ldexpf(alpha, (int)(was[nr] - ((float)ex - e)));
-          const float shift = move - (e - e_was);
-          m_use[nr] += shift;
-          m_limit[nr] = first && !some ? kNothing : (scaled ? 4.0f + e : kZeros);
-          l_sum[nr] *= __builtin_amdgcn_ldexpf(alpha, (int)(e - e_was));
-          least = scaled ? fminf(least, (float)ex - e) : least;
-          open = open || m_limit[nr] == kZeros;
+          const float beta = __builtin_amdgcn_ldexpf(alpha, was[nr] - (ex - e));
+          m_use[nr] += move;
+          l_sum[nr] *= __builtin_amdgcn_ldexpf(alpha, e - e_of(m_limit[nr]));
+          m_limit[nr] = first && !some ? kNothing : (scaled ? limit_of(e) : kZeros);
 #pragma unroll
-          for (int T = 0; T < 2; ++T) t[nr][T] -= shift;
+          for (int T = 0; T < 2; ++T) t[nr][T] = (t[nr][T] - move) + (float)e;
 #pragma unroll
           for (int j = 0; j < 2 * P; ++j) o[nr][j] *= beta;
         }
         a_exp = ex;
-        const int least_exp = __builtin_amdgcn_readfirstlane((int)-row16_max(-least));
-        a_limit = __builtin_amdgcn_ballot_w64(open) != 0 ? 0.0f
-                                                         : __builtin_amdgcn_ldexpf(8.0f, least_exp);
+        // else every step comes here: e is added to its scores
+        a_limit = even ? __builtin_amdgcn_ldexpf(8.0f, ex) : -1.0f;
       }
       a_inv = __builtin_amdgcn_ldexpf(1.0f, 8 - (a_exp > kLeast ? a_exp : kLeast));
     }
@@ -1060,10 +1052,9 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
                   // may be subnormal
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) {
-    const float e = e_of(m_limit[nr]);
-    l_row[nr] = __builtin_amdgcn_ldexpf(sum_over_groups(l_sum[nr]), -(int)e);
-    m_ref[nr] = m_limit[nr] == kNothing ? kNothing : m_use[nr] + e;
-    a_row[nr] = a_exp - (int)e - 8;
+    l_row[nr] = __builtin_amdgcn_ldexpf(sum_over_groups(l_sum[nr]), -e_of(m_limit[nr]));
+    m_ref[nr] = m_limit[nr] == kNothing ? kNothing : m_use[nr];
+    a_row[nr] = a_exp - e_of(m_limit[nr]) - 8;
   }
   KernelArgs &end_args = *kernel_args();
   const int tid = fresh((int)threadIdx.x);

@@ -129,6 +129,46 @@ def test_value_scales_that_grow_from_row_to_row(nf4, orc, case, split):  # noqa:
         check_rows(out, *want, largest_seen(call, a, heads, True, 0), dtype, "nf4", d, max(lens))
 
 
+@pytest.mark.parametrize("case", BLOCKS, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_large_value_scales_beside_scores_of_any_size(nf4, orc, case):  # noqa: F811
+    """Scores of 2^28, whose neighbours in fp32 are 32 apart, and value scales that grow
+    with the rows: every row is finite, and the value of its nearest key where the next one
+    is 1e-2 of the largest score away (keys' codes and fp32 sums: 2^-10 of it at most)."""
+    dtype, d, bs, heads, kvh, lens, rows = case
+    if dtype == "fp16":
+        dtype = "bf16"  # (fp16's range ends before such queries)
+    call, pages = ref.make_call(lens, rows, 16, 980)
+    book = ref.codebook(orc, "nf4")
+    nat = ref.random_cache(book, pages, kvh, 16, d, bs, "nf4", 981)
+    k64 = dense(book, *nat[0], bs)
+    q = (queries(call.total, heads, d, "fp32", 982) * 2.0 ** 28).to(DT[dtype])
+    codes, a = nat[1]
+    for _, b, p, pg, at in call.places():
+        if pg >= 0:
+            a[pg, :, at] *= 2.0 ** min(100, 20 * (p - lens[b] + rows[b]))
+    v64 = dense(book, codes, a, bs)
+    sure = torch.zeros(call.total, heads, dtype=torch.bool)
+    row = 0
+    for b, n in enumerate(call.rows):
+        k, _ = ref.sequence(call, k64, b, kvh)
+        for i in range(n):
+            qr = q[row].double().reshape(kvh, heads // kvh, d)
+            ks = k[:, :lens[b] - n + i + 1]
+            two = torch.einsum("hgd,htd->hgt", qr, ks).topk(2, -1).values
+            reach = torch.einsum("hgd,htd->hgt", qr.abs(), ks.abs()).amax(-1)
+            sure[row] = (two[..., 0] - two[..., 1] >= 1e-2 * reach).reshape(heads)
+            row += 1
+    assert sure.sum() >= sure.numel() // 2
+    want, spread, reach = ref.attention(call, q, k64, v64, ref.sqrt_scale(d), True, 0)
+    cache = device_cache(nf4, (nat[0], (codes, a)), bs, "nf4")
+    seen = largest_seen(call, a, heads, True, 0)
+    for max_len in (1, 1 << 17):
+        out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=max(rows), max_len=max_len)
+        assert torch.isfinite(out).all()
+        got = torch.where(sure[..., None].cuda(), out, want.to(out.dtype).cuda())
+        check_rows(got, want, spread, torch.zeros_like(reach), seen, dtype, "nf4", d, max(lens))
+
+
 @pytest.mark.parametrize("d,bs,heads,kvh,rows,window,lens", [
     (64, 32, 8, 2, 5, 600, list(range(700, 733))),  # waves that share a block of two tiles
     (128, 64, 4, 2, 3, 600, list(range(700, 733))),  # of one
