@@ -146,6 +146,11 @@ __device__ __forceinline__ int seen_begin(KernelArgs &a, int end) {
   return a.window > 0 && end > a.window ? end - a.window : 0;
 }
 
+// A row's end as far as the table goes: a length may pass it.
+__device__ __forceinline__ int within(KernelArgs &a, int end) {
+  return end < a.kv.capacity ? end : a.kv.capacity;
+}
+
 // A sequence of the call.
 struct Sequence {
   int first;  // its first row in the tensors
@@ -166,7 +171,7 @@ __device__ __forceinline__ Sequence sequence_of(KernelArgs &a, int seq) {
     end = clamp_to(b1, 0, a.kv.total_rows);
   }
   s.n = end > s.first ? end - s.first : 0;
-  s.len = clamp_to(len, 0, a.kv.capacity);
+  s.len = clamp_to(len, 0, kMaxPositions);
   return s;
 }
 
@@ -184,9 +189,9 @@ __device__ __forceinline__ Block block_of(KernelArgs &a, const Sequence &s, int 
     const int token0 = row0 == 0 ? 0 : row0 / a.group;
     const int token1 = row0 + rows >= b.pairs ? tokens - 1 : (row0 + rows - 1) / a.group;
     const int end0 = seen_end(a, b, token0), end1 = seen_end(a, b, token1);
-    b.hi = end1;
+    b.hi = within(a, end1);
     b.lo = seen_begin(a, end0);
-    b.all_hi = end0;
+    b.all_hi = within(a, end0);
     b.all_lo = seen_begin(a, end1);
     if (b.hi <= b.lo) b.lo = b.hi = 0;
     b.lo &= ~(kStep - 1);
@@ -622,8 +627,9 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
       const bool have = blk.row0 + 16 * nr + n < blk.pairs;
-      row_hi[nr] = have ? seen_end(args, blk, row_at(16 * nr + n).token) : 0;
-      row_lo[nr] = have ? seen_begin(args, row_hi[nr]) : 0;
+      const int end_of_row = have ? seen_end(args, blk, row_at(16 * nr + n).token) : 0;
+      row_hi[nr] = within(args, end_of_row);
+      row_lo[nr] = seen_begin(args, end_of_row);
     }
     if constexpr (MERGE) {
       static_assert(NR * P <= kWaves, "a fragment for each wave");

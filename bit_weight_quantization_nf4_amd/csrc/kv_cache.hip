@@ -69,8 +69,8 @@ __device__ __forceinline__ RowPlace place_of(const KvArgs &kv, int row) {
   RowPlace r{false, false, 0, 0};
   r.in_call = row >= begin && row < end;
   if (!r.in_call) return r;
-  const int pos = clamp_to(kv.lens[b], 0, kv.capacity) - (end - row);
-  if (pos < 0) return r;
+  const int pos = clamp_to(kv.lens[b], 0, kMaxPositions) - (end - row);
+  if (pos < 0 || pos >= kv.capacity) return r;
   const int col = pos / kv.page_size;
   r.page = kv.table[(int64_t)b * kv.table_stride + col];
   r.at = pos - col * kv.page_size;

@@ -21,7 +21,7 @@ struct KvArgs {
   int32_t capacity;  // positions that the table can hold
 };
 
-// Most positions of a sequence.
+// Most positions of a sequence: lengths are clamped to it.
 constexpr int32_t kMaxPositions = 0x7ff00000;
 
 struct KvShape {

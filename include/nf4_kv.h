@@ -35,10 +35,11 @@
  * lengths serves the write of a step and the attention after it.
  *
  * Device data out of range never becomes an access out of range: offsets are
- * clamped to [0, total_rows], lengths to the table's capacity, and a page index
+ * clamped to [0, total_rows], lengths to [0, 2^31 - 2^20], and a page index
  * outside [0, num_pages) (-1 behind a sequence's last page, say) means that its
  * positions are not there: not written, read as zeros, not attended to. The same
- * holds for negative positions. Rows behind the last offset are left as they
+ * holds for negative positions and for those past the table's last column, so a
+ * step on a sequence whose table is full leaves what is cached as it is. Rows behind the last offset are left as they
  * are in every output. The positions of one nf4_kv_write must be distinct
  * (sequences may share pages that a call does not write to).
  */

@@ -293,3 +293,66 @@ def test_strides_of_one_row_and_one_head_do_not_matter(nf4, orc):  # noqa: F811
     table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
     lens = torch.tensor([9], dtype=torch.int32, device="cuda")
     assert same(nf4.kv_attention(q, loose, table, lens), nf4.kv_attention(q, single, table, lens))
+
+
+@pytest.mark.parametrize("past", [1, 3, 20, 1 << 30])
+def test_lengths_past_the_table(nf4, orc, past):  # noqa: F811
+    """Positions that the table has no room for are not there, as if its rows went on with
+    pages of -1: what is cached is not overwritten, reads give zeros, rows see the
+    positions that there are. Bitwise the calls with such a longer table, and those of
+    lengths that end within it for the other sequence."""
+    heads, kvh, d, bs, page, cols = 8, 2, 64, 32, 16, 3
+    lens, rows = [cols * page + past, 21], [5, 5]
+    book = ref.codebook(orc, "nf4")
+    table = torch.tensor([[3, 1, 5], [0, 4, -1]], dtype=torch.int32)
+    pages = 6
+    nat = ref.random_cache(book, pages, kvh, page, d, bs, "nf4", 951)
+    off = torch.tensor([0, 5, 10], dtype=torch.int32)
+    x = [row_values((10, kvh, d), "bf16", 952 + i).cuda() for i in range(2)]
+    q = queries(10, heads, d, "bf16", 954).cuda()
+    lens_t = torch.tensor(lens, dtype=torch.int32).cuda()
+    where = (table.cuda(), lens_t, off.cuda())
+    cache = device_cache(nf4, nat, bs, "nf4")
+    kq, vq = nf4.kv_write(cache, *x, *where, values=True)
+    got = natural(cache)
+    # the rows of the first sequence that have a place, by the definition
+    call = ref.Call(torch.cat([table, torch.full((2, 2), -1, dtype=torch.int32)], 1),
+                    [min(lens[0], (cols + 2) * page), 21], rows, off, page)
+    kept = {i for i in range(5) if lens[0] - 5 + i < cols * page}
+    written = torch.zeros(pages, page, dtype=torch.bool)
+    for i in range(5):
+        if i in kept:
+            p = lens[0] - 5 + i
+            written[table[0, p // page], p % page] = True
+        p = 16 + i
+        written[table[1, p // page], p % page] = True
+    for which in range(2):
+        for new, old in zip(got[which], nat[which]):
+            assert torch.equal(new[~written[:, None].expand(new.shape[:3])],
+                               old[~written[:, None].expand(old.shape[:3])])
+    k, v = nf4.kv_read(cache, 10, *where)
+    for i in range(10):
+        for t, val in ((k, kq), (v, vq)):
+            if i >= 5 or i in kept:
+                assert same(t[i], val[i]), i
+            else:
+                assert torch.all(t[i] == 0), i
+    # attention: the longer table's where it can be written down, the definition besides
+    k64, v64 = (dense(book, *t, bs) for t in got)
+    for causal, window in ((True, 0), (False, 0), (True, 7), (False, 30)):
+        kw = dict(max_rows=5, causal=causal, window=window)
+        for max_len in (1, 1 << 17):
+            out = nf4.kv_attention(q, cache, *where, max_len=max_len, **kw)
+            if past < 1 << 20:
+                longer = (call.table.cuda(), *where[1:])
+                assert same(nf4.kv_attention(q, cache, *longer, max_len=max_len, **kw), out)
+                want = ref.attention(call, q.cpu(), k64, v64, ref.sqrt_scale(d), causal, window)
+                check_rows(out, *want, largest_seen(call, got[1][1], heads, causal, window),
+                           "bf16", "nf4", d, 48)
+            elif window:
+                assert torch.all(out[:5] == 0)
+            else:
+                full = torch.tensor([cols * page, 21], dtype=torch.int32).cuda()
+                again = nf4.kv_attention(q, cache, where[0], full, where[2], max_len=max_len,
+                                         max_rows=5, causal=False)
+                assert same(out[:5], again[:5])
