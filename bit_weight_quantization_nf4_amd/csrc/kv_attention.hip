@@ -99,19 +99,19 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(Attn
 // ------------------------------------------------------------------- host
 
 // Waves have rows of their own where that gives a workgroup for every CU: they then
-// merge nothing (1024 and 512 rows at 5000 and 2500 positions, 32 query heads of 8: 205
-// us, 251 merged; 4 sequences of 256 rows at 1000: 51, 64). With fewer the waves that
-// share a block finish sooner (512 rows at 4096: 87 merged, 105 apart; 32 rows at 2048:
-// 18, 24). Sequences of fewer rows than a workgroup's leave its waves without any (64 of
-// one row: 36 merged, 84).
-constexpr int kApartMinRows = 128, kApartMinItems = 256;
+// merge nothing (1024 and 512 rows at 5000 and 2500 positions, 32 query heads of 8: 213
+// us, 247 merged; 4 sequences of 256 rows at 1000: 54, 65). With fewer the waves that
+// share a block finish sooner (512 rows at 4096: 87 merged, 109 apart; 32 rows at 2048:
+// 17, 93). Sequences of fewer rows than a workgroup's leave its waves without any (64 of
+// one row at 4000: 63 merged, 165).
+constexpr int kApartMinRows = 128;
 
 // From how many positions on an item is split, and the fewest that a range has. The
 // second launch takes about as long as 1500 positions of a workgroup: 1536 positions,
 // one row, 15.0 us whole and 17.8 split, 2048 18.0 either way, 4096 29.6 and 18.0.
 // Ranges of 256, 512 and 1024 differ by less than 1 us. A range of waves with rows of
-// their own costs more to join (1024 rows at 2048 positions: 90.7 whole, 96.1 in two; at
-// 4096 158 either way).
+// their own costs more to join (1024 rows at 2048 positions: 94.7 whole, 99.0 in two; at
+// 4096 176.7 whole, 162.9 in two).
 constexpr int64_t kSplitFrom = 2048, kMinRange = 512;
 constexpr int64_t kSplitFromApart = 4096, kMinRangeApart = 2048;
 // What a range costs besides its positions, in positions.
@@ -125,7 +125,11 @@ Plan plan_of(const KvAttentionSizes &z) {
   const int64_t pairs = (int64_t)z.max_rows * (z.heads / z.kv_heads);
   const int64_t apart_blocks = ceil_div(pairs, 16 * max_tiles(z.head_dim) * kApartWaves);
   p.merge = pairs < kApartMinRows ||
-            (int64_t)z.batch * z.kv_heads * apart_blocks < kApartMinItems;
+            (int64_t)z.batch * z.kv_heads * apart_blocks < device_cu_count();
+  // More rows than a tile's: blocks of two tiles look a position's codes up once for both.
+  // (8 kv heads of 128 in bf16, 16 sequences at 6000 positions: 20 rows a kv head 43 us, in
+  // one-tile blocks 53; 48 rows 63, 70; 96 rows 118, 114. Short calls lose by the second
+  // tile's merge: one sequence at 1000, 20 rows 16.6, 15.9.)
   p.tiles = p.merge && pairs <= 16 ? 1 : max_tiles(z.head_dim);
   p.wg_rows = 16 * p.tiles * (p.merge ? 1 : kApartWaves);
   p.wg_blocks = (int)ceil_div(pairs, p.wg_rows);
