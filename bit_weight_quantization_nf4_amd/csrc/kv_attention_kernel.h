@@ -35,8 +35,10 @@
 // positions averages out (5e-3 of the result at 70000 positions). Keys of bf16
 // rows take c1: there such a mean shifts all scores alike. mu = 1.6776896 2^7 makes
 // the 2-norm of NF4's c1 errors 6.2e-5 of the values' (1.6e-4 at mu = 2^7; a search
-// over 2^20 factors); E2M1 values are exact (mu = 6 2^7). 16-bit queries are exact
-// in fp16 after a power of two of the row's own, so no row depends on another's size.
+// over 2^20 factors); E2M1 values are exact (mu = 6 2^7). 16-bit queries enter as fp16
+// after a power of two of the row's own, so no row depends on another's size: fp16 rows
+// exactly, elements of bf16 rows to 2^-39 of the row's largest at least (fp16's least step
+// is 2^-24, the largest is brought to 2^14 ..).
 // w: one fp16 for bf16 rows (2^-12), two for fp16 rows, whose output resolves 2^-11; so
 // do their keys (one part would cost 3e-4 of the result at scores of size 3). fp32 rows:
 // q, c' and w in two parts each, the three leading products. Accumulators and
@@ -53,9 +55,11 @@
 //     42 us, 3.6 TB/s. Half of the SIMDs' cycles issue (VALU 37 %, MFMA 12 %): a position
 //     costs a fixed number of lookups, exponentials and products per 16 rows, of which
 //     4 are used. The rest waits for HBM and the uneven ends.
-//   - many rows (1024 and 512, 32 heads, 5000 and 2500 positions, 94 GFLOP): 203 us, 464
-//     TFLOP/s of the definition's, 700 of those issued (V's two parts). VALU and MFMA
-//     instructions do not overlap well within a SIMD and take about its whole time.
+//   - many rows (1024 and 512, 32 heads, 5000 and 2500 positions, 94 GFLOP): 212 us, 444
+//     TFLOP/s of the definition's, 660 of those issued (V's two parts). A wave's step is
+//     some 370 VALU instructions (107 us of every SIMD: addresses and merging of codes,
+//     scales of scores and weights, softmax) and 48 MFMA (56 us); these do not overlap
+//     well within a SIMD. Each wave decodes the same codes for rows of its own.
 //   - short calls: 9 us, of which the arguments' way, the table and the merge of the
 //     waves are 6.
 #pragma once
@@ -339,8 +343,12 @@ struct Attn {
   // suffice (128 registers), else one of 8 waves or two of 4 (256)
   static constexpr int kWavesPerSimd = MERGE && NR == 1 && D <= 128 && DT != kFP32 ? 4 : 2;
   // with two waves on a SIMD, lookups are kept ahead of the products that they feed;
-  // with four the others fill the wait, and the registers are needed
-  static constexpr bool kAhead = kWavesPerSimd < 4 && !(kSplitQ && D > 128);
+  // with four the others fill the wait, and the registers are needed. So they are for wide
+  // heads in two parts, which would spill (fp16, heads of 256 in blocks of 64: 16 uneven
+  // sequences up to 8000 positions 70 us, 96 with lookups ahead; 227, 300 at 512 and 256
+  // rows of 3000 and 1500)
+  static constexpr bool kAhead =
+      kWavesPerSimd < 4 && !(kSplitQ && D > 128) && !(kSplitK && D > 192);
   // the merge of the waves' results handles this many rows and columns at once, so
   // that its buffer and the table leave room for a second workgroup where there is one.
   // It goes by whole 32-wide pieces: half of 96 columns would end inside one
