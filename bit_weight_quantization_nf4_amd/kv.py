@@ -274,7 +274,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
     rows of a sequence where row_offsets is given (0: that many as there are
     rows), ``max_len`` about the longest of kv_lens (0: what the table can hold);
     both only size the launch, but rows of a sequence past max_rows stay
-    unwritten. ``scale`` defaults to head_dim ** -0.5. Rows behind the last
+    unwritten, and a batch of many sequences without max_rows takes several times
+    as long. ``scale`` defaults to head_dim ** -0.5. Rows behind the last
     offset are left as they are: unspecified without ``out``."""
     _check_rows(q, cache, "kv_attention")
     total, heads, d = q.shape

@@ -134,8 +134,11 @@ int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_
  * A query that is not finite spoils its own row only, and a scale in the cache that
  * is not the rows that see its position. (Key scales of 2^96 and more overflow in up to
  * 32 neighbouring rows of which one has a query of 2^64 or more; else in none.)
+ * Sums e_p v_p are formed before they are divided: a value scale times 16 times the
+ * positions seen has to stay below 2^128.
  * max_rows: the most rows of any sequence (rows past it are left as they are; 0
- * stands for total_rows); ignored without row_offsets. max_len: about the longest
+ * stands for total_rows, which plans that many for every sequence and takes several
+ * times as long where there are many); ignored without row_offsets. max_len: about the longest
  * kv_lens, which sizes the split of the positions over the device (any value gives
  * a right result; 0 stands for the table's capacity). workspace: at least
  * nf4_kv_attention_workspace_bytes of these sizes (16-byte aligned; NF4_ERR_SCRATCH
