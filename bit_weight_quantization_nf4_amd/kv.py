@@ -257,12 +257,18 @@ def kv_read(cache: KVCache, rows: int, block_table: torch.Tensor, kv_lens: torch
     return k, v
 
 
+def _int32(n: int) -> int:
+    """A size as the C calls take it (ctypes would drop the upper bits): the largest one is
+    past every position."""
+    return n if 0 <= n < 0x7ff00000 else (0x7ff00000 if n > 0 else -1)
+
+
 def kv_attention_workspace_bytes(batch: int, max_rows: int, max_len: int, num_heads: int,
                                  num_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
                                  window: int = 0) -> int:
     """nf4_kv_attention_workspace_bytes on the current device."""
-    return _lib().nf4_kv_attention_workspace_bytes(batch, max_rows, max_len, num_heads,
-                                                   num_kv_heads, head_dim, _DT[dtype], window)
+    sizes = map(_int32, (batch, max_rows, max_len, num_heads, num_kv_heads, head_dim))
+    return _lib().nf4_kv_attention_workspace_bytes(*sizes, _DT[dtype], _int32(window))
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -300,8 +306,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
         max_rows = total
     if max_len <= 0:
         max_len = rows.table_cols * cache.page_size
-    # what does not fit 32 bits is past every position
-    max_rows, max_len, window = (min(n, 0x7ff00000) for n in (max_rows, max_len, window))
+    max_rows, max_len, window = _int32(max_rows), _int32(max_len), _int32(window)
     qr, qh = strides
     orow, ohead = out_strides
     kv_heads, dt = cache.num_kv_heads, _DT[q.dtype]

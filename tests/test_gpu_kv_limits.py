@@ -356,3 +356,12 @@ def test_lengths_past_the_table(nf4, orc, past):  # noqa: F811
                 again = nf4.kv_attention(q, cache, where[0], full, where[2], max_len=max_len,
                                          max_rows=5, causal=False)
                 assert same(out[:5], again[:5])
+
+
+def test_a_window_below_32_bits_is_refused(nf4):  # noqa: F811
+    cache = nf4.KVCache.empty(1, 16, 1, 64)
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for window in (-1, -(1 << 32)):
+        with pytest.raises(nf4.Nf4Error):
+            nf4.kv_attention(q, cache, one[None] - 1, one, window=window)

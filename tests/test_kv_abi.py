@@ -177,3 +177,17 @@ def test_binding_refuses_cpu_tensors(kv):
         kv.KVCache(p, a, p.clone(), torch.zeros(2, 2, 16, 1), 64, "nf4")
     with pytest.raises(ValueError):
         kv.KVCache(p.float(), a, p, a)
+
+
+def test_workspace_query_of_sizes_past_32_bits(kv):
+    """The query's sizes are C ints: larger ones are taken as the largest, not modulo 2^32,
+    and negative ones stay negative."""
+    q = kv.kv_attention_workspace_bytes
+    most = 0x7ff00000
+    assert q(1, 1, most, 8, 8, 128) > 0
+    for n in (1 << 32, (1 << 40) + 5, most + 1):
+        assert q(1, 1, n, 8, 8, 128) == q(1, 1, most, 8, 8, 128)
+        assert q(1, 1, 1 << 17, 8, 8, 128, window=n) == q(1, 1, 1 << 17, 8, 8, 128)
+    low = -(1 << 32)
+    assert q(1, 1, low + 9, 8, 8, 128) == -1 and q(1, 1, 100, 8, 8, 128, window=low) == -1
+    assert q((1 << 32) + 1, 1, 1, 8, 8, 128) == -1 and q(1, 1, 1, (1 << 32) + 8, 8, 128) == -1
