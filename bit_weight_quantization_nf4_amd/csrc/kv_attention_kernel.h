@@ -575,7 +575,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   int row_lo[NR], row_hi[NR];  // positions the row sees
   // a row's scores are its products times this. The products, below 2^31 times a key scale,
   // are kept in range by 2^-31 with the key scales, unless a query of the wave's reaches
-  // 2^64: large scales have no finite scores there.
+  // 2^90: small key scales have to be exact there, and large ones have no finite scores.
   float qscale[NR];
   float key_factor = 1.0f;
   uint4 *const q_shared = reinterpret_cast<uint4 *>(merge_buf);  // [first, second parts][fragment][lane]
@@ -614,7 +614,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     auto set_scales = [&](const int (&ex)[NR]) {
       bool large = false;
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) large = large || ex[nr] > 64;
+      for (int nr = 0; nr < NR; ++nr) large = large || ex[nr] > 90;
       const int down = __builtin_amdgcn_ballot_w64(large) != 0 ? 0 : 31;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) qscale[nr] = __builtin_amdgcn_ldexpf(args.f, ex[nr] - 15 + down);
@@ -730,6 +730,9 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   const int all_lo = pin(blk.all_lo), all_hi = pin(blk.all_hi);
   const int any_hi = pin(blk.hi);
   for (int s = 0; s < nsteps; ++s) {
+    // (steps begin at a multiple of 32 bytes: where the compiler happens to put them, many
+    // rows take up to 2 % longer)
+    asm volatile(".p2align 5");
     const int pos0 = begin + kStep * (tw + TW * step);
     if (s + 1 < nsteps) {  // the last one loads its own inputs again
       advance();

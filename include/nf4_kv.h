@@ -133,7 +133,7 @@ int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_
  *   2^-150 of the largest one that any row sees, if that is more.)
  * A query that is not finite spoils its own row only, and a scale in the cache that
  * is not the rows that see its position. (Key scales of 2^96 and more overflow in up to
- * 32 neighbouring rows of which one has a query of 2^64 or more; else in none.)
+ * 32 neighbouring rows of which one has a query of 2^89 or more; else in none.)
  * Sums e_p v_p are formed before they are divided: a value scale times 16 times the
  * positions seen has to stay below 2^128.
  * max_rows: the most rows of any sequence (rows past it are left as they are; 0

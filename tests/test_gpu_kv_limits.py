@@ -365,3 +365,24 @@ def test_a_window_below_32_bits_is_refused(nf4):  # noqa: F811
     for window in (-1, -(1 << 32)):
         with pytest.raises(nf4.Nf4Error):
             nf4.kv_attention(q, cache, one[None] - 1, one, window=window)
+
+
+def test_large_keys_beside_a_large_query(nf4, orc):  # noqa: F811
+    """Keys of 2^118 under queries of 2^-118, one of which is of 2^80: the others' scores
+    are ordinary."""
+    d, bs, heads, kvh = 128, 64, 4, 2
+    call, pages = ref.make_call([75, 40], [5, 3], 16, 990)
+    book = ref.codebook(orc, "nf4")
+    nat = ref.random_cache(book, pages, kvh, 16, d, bs, "nf4", 991)
+    codes, a = nat[0]
+    a = a * 2.0 ** 118
+    q = queries(call.total, heads, d, "fp32", 992) * 2.0 ** -118
+    q[1] = queries(1, heads, d, "fp32", 993)[0] * 2.0 ** 80
+    keep = [0, 2, 3, 4, 5, 6, 7]
+    cache = device_cache(nf4, ((codes, a), nat[1]), bs, "nf4")
+    want = ref.attention(call, q, dense(book, codes, a, bs), dense(book, *nat[1], bs),
+                         ref.sqrt_scale(d), True, 0)
+    seen = largest_seen(call, nat[1][1], heads, True, 0)
+    for max_len in (1, 1 << 17):
+        out = nf4.kv_attention(q.cuda(), cache, *gpu_call(call), max_rows=5, max_len=max_len)
+        check_rows(out, *want, seen, "fp32", "nf4", d, 75, keep)
