@@ -1,0 +1,446 @@
+"""Cases that measure the microscaled 4-bit operators and the masked forms of
+the attention to a 4-bit cache.
+
+The operators: ``mx_quantize`` and ``mx_dequantize`` (E2M1 elements, a power of
+two per 32 of them), ``mx_linear`` (activations quantized in the call, times a
+weight in that format), and ``kv_attention`` where a window leaves a few first
+positions visible (``sinks``) or the call's rows are a tree of drafted tokens
+(``tree``). With ``own`` the framework's calls run; without it the same results
+come from elementary torch operations in fp32, rounded once.
+
+A microscaled matrix of R rows of K elements is padded to Kp, a multiple of 128:
+codes uint8 [R, Kp/2], element 2i of a row in the high nibble of byte i, and
+scales uint8 [Kp/128, R, 4], exponents biased by 127, those of the blocks 4t ..
+4t + 3 of row r at [t, r]. Blocks of zeros, as the padding, have scale 1 (127). The cache's layout
+is that of perf/operators.py's text: byte 16 k + m of a head vector holds elements
+32 k + 2 m (high nibble) and 32 k + 2 m + 1; a key row stores its bytes ordered
+(m, k), the value rows of four consecutive positions r share a run ordered (m, r, k).
+"""
+import math
+import statistics
+
+import torch
+
+own = False
+
+_DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+_BYTES = {"bf16": 2, "fp16": 2, "fp32": 4}
+
+
+def _mx(name, op, dtype="bf16", rows=1, k=4096, n=0, bias=False):
+    return dict(name=name, op=op, dtype=dtype, rows=rows, k=k, n=n, bias=bias)
+
+
+def _attention(name, op, dtype="bf16", quant_type="nf4", blocksize=64, page=64, heads=32, kv_heads=8,
+               head_dim=128, batch=1, rows=1, kv_len=1, ragged=False, window=0, sinks=0):
+    """rows: the most rows of a sequence in the call, the last of its kv_len positions;
+    ragged: the sequences' lengths and rows spread below these."""
+    return dict(name=name, op=op, dtype=dtype, quant_type=quant_type, blocksize=blocksize, page=page,
+                heads=heads, kv_heads=kv_heads, head_dim=head_dim, batch=batch, rows=rows,
+                kv_len=kv_len, ragged=ragged, window=window, sinks=sinks)
+
+
+def listed():
+    return [
+        # the activations of a single stream's step: latency only
+        _mx("requantize, one token", "requantize"),
+        # a weight as it is loaded, and restored for a check
+        _mx("requantize, a weight", "requantize", rows=11008),
+        # a single stream's step through the up projection of the stack of bench.py
+        _mx("product, one token", "product", n=11008),
+        # a small serving batch through its down projection
+        _mx("product, 16 rows", "product", dtype="fp16", rows=16, k=11008, n=4096),
+        # a prompt through a wide projection: the matrix-bound end
+        _mx("product, prompt", "product", rows=2048, n=14336),
+        # an fp32 evaluation run of odd sizes, with a bias
+        _mx("product, odd sizes", "product", dtype="fp32", rows=333, k=1003, n=1531, bias=True),
+        # a short chat, a small window: latency
+        _attention("sinks, one short sequence", "sinks", page=16, kv_len=301, window=128, sinks=4),
+        # serving sessions of mixed length, most past their window
+        _attention("sinks, serving batch", "sinks", batch=32, kv_len=16000, ragged=True, window=4096,
+                   sinks=4),
+        # a long session's next chunk
+        _attention("sinks, prompt chunk", "sinks", dtype="fp16", batch=2, rows=512, kv_len=8000,
+                   ragged=True, window=2048, sinks=33),
+        # a small tree of drafts after a short prompt: latency
+        _attention("tree, one short sequence", "tree", page=16, rows=13, kv_len=301),
+        # serving with trees of up to 64 drafts
+        _attention("tree, serving batch", "tree", batch=16, rows=64, kv_len=6000, ragged=True),
+        # a tree over a long document, E2M1 codes, one kv head for all
+        _attention("tree, long document", "tree", quant_type="fp4", blocksize=32, page=256, heads=16,
+                   kv_heads=2, rows=26, kv_len=131071),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi))))))
+
+
+def draw(rng):
+    op = rng.choice(["requantize", "product", "product", "sinks", "tree"])
+    dtype = rng.choice(["bf16", "bf16", "fp16", "fp32"])
+    if op == "requantize":
+        k = _log_int(rng, 32, 16384)
+        if rng.random() < 0.6:  # else an odd one
+            k = -(-k // 32) * 32
+        c = _mx("", op, dtype, rows=_log_int(rng, 1, 45_000_000 // k), k=k)
+    elif op == "product":
+        k, n = _log_int(rng, 64, 14336), _log_int(rng, 64, 14336)
+        if rng.random() < 0.7:
+            k, n = -(-k // 64) * 64, -(-n // 16) * 16
+        m = _log_int(rng, 1, min(2048, max(1, 110_000_000_000 // (k * n))))
+        c = _mx("", op, dtype, rows=m, k=k, n=n, bias=rng.random() < 0.4)
+    else:
+        d = rng.choice([64, 96, 128, 128, 192, 256])
+        kv_heads = rng.choice([1, 2, 4, 8, 8, 16])
+        group = rng.choice([1, 2, 3, 4, 8, 16])
+        if op == "sinks":
+            rows = rng.choice([1, 1, _log_int(rng, 2, 16), _log_int(rng, 16, 400)])
+        else:
+            rows = _log_int(rng, 2, 128)
+        batch = _log_int(rng, 1, 32 if rows == 1 else 8)
+        most = min(100_000_000 // (batch * kv_heads * d), 70_000_000 // (batch * rows * kv_heads * group))
+        kv_len = rows + _log_int(rng, 1, max(2, min(131072, most))) - 1
+        window = _log_int(rng, 16, 4096) if op == "sinks" or rng.random() < 0.3 else 0
+        c = _attention("", op, dtype, quant_type=rng.choice(["nf4", "nf4", "fp4"]),
+                       blocksize=rng.choice([b for b in (32, 64, 128) if d % b == 0]),
+                       page=rng.choice([16, 48, 64, 256]), heads=kv_heads * group, kv_heads=kv_heads,
+                       head_dim=d, batch=batch, rows=rows, kv_len=kv_len, ragged=rng.random() < 0.7,
+                       window=window, sinks=_log_int(rng, 1, 200) if window else 0)
+    del c["name"]
+    return c
+
+
+def _lengths(case):
+    """Cached lengths and rows of each sequence (by the case alone, as work() needs them)."""
+    n, r, b = case["kv_len"], case["rows"], case["batch"]
+    if not case["ragged"]:
+        return [n] * b, [r] * b
+    part = [((5 * i + b - 1) % b + 1) / b for i in range(b)]  # 1, then lower shares in turn
+    lens = [max(1, round(n * p)) for p in part]
+    return lens, [max(1, min(le, round(r * p))) for le, p in zip(lens, part)]
+
+
+def work(case):
+    e = _BYTES[case["dtype"]]
+    if case["op"] == "requantize":  # x in; codes and scales out and in again; values out
+        n = case["rows"] * case["k"]
+        return {"bytes": n * (2 * e + 2 * 17 / 32), "flops": 6 * n}
+    if case["op"] == "product":
+        m, n, k = case["rows"], case["n"], case["k"]
+        return {"bytes": m * k * e + n * k * 17 / 32 + m * n * e + (n * e if case["bias"] else 0),
+                "flops": 2.0 * m * n * k}
+    lens, rows = _lengths(case)
+    d, kh, w, sinks = case["head_dim"], case["kv_heads"], case["window"], case["sinks"]
+    stored = 2 * kh * (d / 2 + 4 * d / case["blocksize"])  # K and V of one position
+    seen = pairs = 0
+    for le, n in zip(lens, rows):
+        base = le - n
+        if case["op"] == "tree":
+            # every row sees what is before the call (the rows' places in a window differ by
+            # their depth, which is taken as 1 here) and, at the least, itself
+            first = min(base, w) + min(sinks, max(0, base - w)) if w else base
+            seen += first + n
+            pairs += n * (first + 1)
+            continue
+        low = le
+        for i in range(n):
+            hi = base + i + 1
+            lo = max(0, hi - w)
+            low = min(low, lo)
+            pairs += hi - lo + min(lo, sinks)
+        seen += le - low + min(low, sinks)
+    return {"bytes": seen * stored + 2 * sum(rows) * case["heads"] * d * e,
+            "flops": 4.0 * d * case["heads"] * pairs}
+
+
+# ------------------------------------------------------------------ inputs
+
+
+def _codebook(quant_type):
+    """The 16 code values by nibble: NF4 quantiles of a normal truncated at
+    929/960 and scaled to [-1, 1]; FP4 the E2M1 values over 6."""
+    if quant_type == "fp4":
+        mags = [0, 0.5, 1, 1.5, 2, 3, 4, 6]
+        return [m / 6 for m in mags] + [-m / 6 for m in mags]
+    inv = statistics.NormalDist().inv_cdf
+    top = 929 / 960
+    q = [inv(0.5 + (top - 0.5) * j / 7) for j in range(8)]
+    p = [inv(0.5 + (top - 0.5) * j / 8) for j in range(9)]
+    return [-v / inv(top) for v in reversed(q[1:])] + [0.0] + [v / inv(top) for v in p[1:]]
+
+
+def prepare(case, seed):
+    dev = "cuda" if torch.cuda.is_available() else "cpu"
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    dt = _DTYPES[case["dtype"]]
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device=dev)
+
+    s = dict(case, dt=dt)
+    if case["op"] in ("requantize", "product"):
+        k = case["k"]
+        # rows of unequal size, a few channels much larger than the others
+        channel = torch.exp(0.3 * normal(k)) * (1 + 19 * (torch.rand(k, generator=g, device=dev) < 0.01))
+        s["x"] = (normal(case["rows"], k) * channel * torch.exp(0.3 * normal(case["rows"], 1))).to(dt)
+        if case["op"] == "product":
+            w = normal(case["n"], k) * 0.02 * (0.5 + torch.arange(k, device=dev) % 7 / 4)
+            nibble, scale = _mx_encode(w)
+            s["codes"] = nibble[:, 0::2] << 4 | nibble[:, 1::2]
+            s["scales"] = scale.view(case["n"], -1, 4).transpose(0, 1).contiguous()
+            s["bias"] = normal(case["n"]).to(dt) if case["bias"] else None
+        return s
+
+    lens, rows = _lengths(case)
+    d, kh, ps, b = case["head_dim"], case["kv_heads"], case["page"], case["batch"]
+    total = sum(rows)
+    # pages in an order of their own, a few of them unused; -1 behind a sequence's last
+    need = [-(-le // ps) for le in lens]
+    pages = sum(need) + 3
+    order = torch.randperm(pages, generator=g, device=dev).to(torch.int32)
+    table = torch.full((b, max(need) + 1), -1, dtype=torch.int32, device=dev)
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = order[at:at + n]
+        at += n
+    off = [0]
+    for n in rows:
+        off.append(off[-1] + n)
+    s.update(table=table, total=total, book=torch.tensor(_codebook(case["quant_type"]), device=dev),
+             kv_lens=torch.tensor(lens, dtype=torch.int32, device=dev),
+             offsets=torch.tensor(off, dtype=torch.int32, device=dev))
+    # the cache: normal head vectors with channels and positions of unequal size, as codes
+    by_value, nibble = torch.sort(s["book"])
+    mids, nibble = (by_value[1:] + by_value[:-1]) / 2, nibble.to(torch.uint8)
+    for name in ("k", "v"):
+        s[name + "_packed"] = torch.empty(pages, kh, ps, d // 2, dtype=torch.uint8, device=dev)
+        s[name + "_absmax"] = torch.empty(pages, kh, ps, d // case["blocksize"], device=dev)
+        for lo in range(0, pages, 512):
+            hi = min(pages, lo + 512)
+            x = normal(hi - lo, kh, ps, d) * (0.5 + torch.arange(d, device=dev) % 7 / 4)
+            x = (x * torch.exp(0.5 * normal(hi - lo, kh, ps, 1))).unflatten(-1, (-1, case["blocksize"]))
+            a = x.abs().amax(-1)
+            c = nibble[torch.bucketize(x / a.unsqueeze(-1), mids)].flatten(-2)
+            run = (c[..., 0::2] << 4 | c[..., 1::2]).unflatten(-1, (d // 32, 16))
+            if name == "v":  # (position / 4, m, position % 4, k)
+                run = run.unflatten(2, (ps // 4, 4)).permute(0, 1, 2, 5, 3, 4)
+            else:
+                run = run.mT
+            s[name + "_packed"][lo:hi] = run.reshape(hi - lo, kh, ps, d // 2)
+            s[name + "_absmax"][lo:hi] = a
+    s["q"] = (1.5 * normal(total, case["heads"], d)).to(dt)
+    s["tree"] = None
+    if case["op"] == "tree":
+        # row 0 is the root; a later one follows the row before it or any earlier one
+        host = torch.Generator().manual_seed(seed)
+        n = case["rows"]
+        u = torch.rand(2, b, n, generator=host)
+        j = torch.arange(n)
+        parent = torch.where(u[0] < 0.4, j - 1, (u[1] * j).long().clamp(max=n - 1))
+        seen = torch.zeros(b, n, -(-n // 32) * 32, dtype=torch.int64)
+        for i in range(n):
+            if i:
+                seen[:, i] = seen[torch.arange(b), parent[:, i]]
+            seen[:, i, i] = 1
+        words = (seen.view(b, n, -1, 32) << torch.arange(32)).sum(-1)
+        words = torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
+        s["tree"] = torch.cat([words[i, :r] for i, r in enumerate(rows)]).to(dev)
+        s["parent"] = parent
+    return s
+
+
+# ------------------------------------------------------------- plain forms
+
+
+def _mx_encode(x):
+    """(nibbles [R, Kp], biased exponents [R, Kp/32]) of x [R, K]: per block of 32 the
+    power of two s = floor(log2 max|x|) - 2 from -127 to 125, and x / s rounded to the
+    nearest of 0, 1/2, 1, 3/2, 2, 3, 4, 6, ties to the even code. Blocks of zeros, the
+    padding's among them, have s = 1."""
+    x = torch.nn.functional.pad(x.float(), (0, -x.shape[1] % 128)).unflatten(-1, (-1, 32))
+    top = x.abs().amax(-1)
+    e = (torch.frexp(top).exponent - 3).clamp(-127, 125).where(top > 0, 0)
+    m = torch.ldexp(x.abs(), -e.unsqueeze(-1))
+    step = torch.where(m < 2, 0.5, torch.where(m < 4, 1.0, 2.0))
+    m = (torch.round(m / step) * step).clamp(max=6.0)
+    rank = torch.where(m < 2, 2 * m, torch.where(m < 4, m + 2, m / 2 + 4))
+    nibble = rank.to(torch.uint8) | ((x < 0) & (m > 0)).to(torch.uint8) << 3
+    return nibble.flatten(-2), (e + 127).to(torch.uint8)
+
+
+def _mx_values(nibble, scale, k):
+    """What codes stand for, in fp32: [R, K]."""
+    book = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6], device=nibble.device)
+    v = book[nibble.int()].unflatten(-1, (-1, 32))
+    return torch.ldexp(v, scale.int().unsqueeze(-1) - 127).flatten(-2)[:, :k]
+
+
+def _plain_requantize(s):
+    nibble, scale = _mx_encode(s["x"])
+    scales = scale.view(s["rows"], -1, 4).transpose(0, 1).contiguous()
+    return [_mx_values(nibble, scale, s["k"]).to(s["dt"]), scales]
+
+
+def _plain_product(s):
+    k = s["k"]
+    x = _mx_values(*_mx_encode(s["x"]), k)
+    nibble = torch.stack((s["codes"] >> 4, s["codes"] & 15), -1).flatten(-2)
+    w = _mx_values(nibble, s["scales"].transpose(0, 1).reshape(s["n"], -1), k)
+    y = torch.matmul(x, w.T)
+    return (y if s["bias"] is None else y + s["bias"].float()).to(s["dt"])
+
+
+def _plain_attention(s):
+    b, kh, d, ps = s["batch"], s["kv_heads"], s["head_dim"], s["page"]
+    group, n = s["heads"] // kh, s["rows"]
+    table = s["table"].clamp(min=0).long()
+    t = table.shape[1] * ps
+    # the sequences' keys and values side by side: [B, kv heads, T, D]
+    k = s["k_packed"][table].unflatten(-1, (16, d // 32)).mT.flatten(-2)
+    v = s["v_packed"][table].view(b, -1, kh, ps // 4, 16, 4, d // 32).permute(
+        0, 1, 2, 3, 5, 6, 4).reshape(b, -1, kh, ps, d // 2)
+    wide = []
+    for x, a in ((k, s["k_absmax"]), (v, s["v_absmax"])):
+        x = s["book"][torch.stack((x >> 4, x & 15), -1).flatten(-2).int()]
+        x = (x.unflatten(-1, (-1, s["blocksize"])) * a[table].unsqueeze(-1)).flatten(-2)
+        wide.append(x.transpose(1, 2).reshape(b, kh, t, d))
+    k, v = wide
+    # queries padded to the longest sequence's: [B, kv heads, group * n, D]
+    i = torch.arange(n, device=table.device)
+    j = torch.arange(t, device=table.device)
+    off = s["offsets"]
+    base = (s["kv_lens"] - off[1:] + off[:-1])[:, None, None]
+    at = (off[:-1, None] + i).clamp(max=s["total"] - 1)
+    q = s["q"][at].float().view(b, n, kh, group, d).permute(0, 2, 3, 1, 4).reshape(b, kh, group * n, d)
+    score = torch.matmul(q, k.mT).view(b, kh, group, n, t) / math.sqrt(d)
+    if s["tree"] is None:
+        end = base + i[:, None] + 1  # the row's place in the sequence, plus 1
+        seen = j < end
+    else:
+        bits = (s["tree"][at].unsqueeze(-1) >> torch.arange(32, device=table.device) & 1).flatten(-2)
+        end = base + bits.sum(-1, keepdim=True)
+        seen = j < base
+    if s["window"]:
+        seen = seen & ((j >= end - s["window"]) | (j < s["sinks"]))
+    if s["tree"] is not None:
+        draft = j - base
+        bit = torch.gather(bits, 2, draft.clamp(0, bits.shape[2] - 1).expand(b, n, t))
+        seen = seen | ((draft >= 0) & (draft < bits.shape[2]) & (bit == 1))
+    score = score.masked_fill(~seen[:, None, None], -math.inf)
+    top = score.amax(-1, keepdim=True)
+    p = torch.exp(score - top.masked_fill(top == -math.inf, 0.0))
+    total = p.sum(-1, keepdim=True)
+    o = torch.matmul(p.view(b, kh, group * n, t), v).view(b, kh, group, n, d)
+    o = torch.where(total > 0, o / total, 0.0).permute(0, 3, 1, 2, 4).reshape(b, n, kh * group, d)
+    row = torch.arange(s["total"], device=table.device)
+    seq = torch.searchsorted(off, row.to(torch.int32), right=True) - 1
+    return o[seq, row - off[seq]].to(s["dt"])
+
+
+# -------------------------------------------------------------------- calls
+
+
+def run(s):
+    if own:
+        import bit_weight_quantization_nf4_amd as nf4
+
+        if s["op"] == "requantize":
+            t = nf4.mx_quantize(s["x"])
+            return [nf4.mx_dequantize(t, s["dt"]), t.scales]
+        if s["op"] == "product":
+            return nf4.mx_linear(s["x"], nf4.MXTensor(s["codes"], s["scales"], (s["n"], s["k"])), s["bias"])
+        cache = nf4.KVCache(s["k_packed"], s["k_absmax"], s["v_packed"], s["v_absmax"],
+                            s["blocksize"], s["quant_type"])
+        return nf4.kv_attention(s["q"], cache, s["table"], s["kv_lens"], s["offsets"],
+                                max_rows=s["rows"], max_len=s["kv_len"], window=s["window"],
+                                sinks=s["sinks"], tree=s["tree"])
+    return {"requantize": _plain_requantize, "product": _plain_product}.get(
+        s["op"], _plain_attention)(s)
+
+
+# ------------------------------------------------------------ in 64 bits
+
+
+def _exact_mx(x):
+    """The values that microscaled x stands for, and the biased exponents, by search:
+    the nearest magnitude by distance, of two equally near ones the even code."""
+    r, k = x.shape
+    x = torch.nn.functional.pad(x.double(), (0, -k % 32)).view(r, -1, 32)
+    top = x.abs().max(-1).values
+    power = torch.full_like(top, -127.0)
+    for e in range(-126, 126):  # the largest power with 4 * 2^e <= max|x|
+        power = torch.where(top >= 4 * 2.0 ** e, float(e), power)
+    power = torch.where(top > 0, power, 0.0)
+    unit = torch.pow(2.0, power).unsqueeze(-1)
+    near, best = torch.zeros_like(x), (x / unit).abs()
+    for odd, mag in enumerate((0.5, 1, 1.5, 2, 3, 4, 6)):
+        far = ((x / unit).abs() - mag).abs()
+        closer = far < best if odd % 2 == 0 else far <= best
+        near, best = torch.where(closer, float(mag), near), torch.where(closer, far, best)
+    scale = torch.nn.functional.pad((power + 127).to(torch.uint8), (0, -power.shape[1] % 4), value=127)
+    return (near * unit * x.sign()).view(r, -1)[:, :k], scale.view(r, -1, 4).transpose(0, 1).contiguous()
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "requantize":
+        return list(_exact_mx(s["x"]))
+    if case["op"] == "product":
+        n, k = case["n"], case["k"]
+        byte = s["codes"].long()[:, :, None].expand(-1, -1, 2)
+        code = torch.where(torch.arange(2, device=byte.device) == 0, byte // 16, byte % 16).reshape(n, -1)
+        mag = code % 8
+        v = torch.where(mag < 2, mag * 0.5, (1 + (mag % 2) * 0.5) * torch.pow(2.0, (mag // 2 - 1).double()))
+        v = torch.where(code >= 8, -v, v)
+        block = torch.arange(code.shape[1], device=byte.device) // 32
+        e = s["scales"].permute(1, 0, 2).reshape(n, -1)[:, block].double() - 127
+        y = _exact_mx(s["x"])[0] @ (v * torch.pow(2.0, e))[:, :k].T
+        return y if s["bias"] is None else y + s["bias"].double()
+    lens, rows = _lengths(case)
+    ps, kh, d = case["page"], case["kv_heads"], case["head_dim"]
+    group, dev = case["heads"] // kh, s["table"].device
+    # the place of every element of a head of a page, by its index
+    e = torch.arange(d, device=dev)
+    piece, m = e // 32, e % 32 // 2
+    t = torch.arange(ps, device=dev)[:, None]
+    place = {"k": t * (d // 2) + m * (d // 32) + piece,
+             "v": t // 4 * (2 * d) + m * (d // 8) + t % 4 * (d // 32) + piece}
+    first, outs = 0, []
+    for b, (le, n) in enumerate(zip(lens, rows)):
+        pages = s["table"][b, :-(-le // ps)].long()
+        wide = {}
+        for name in ("k", "v"):
+            raw = s[name + "_packed"][pages].view(len(pages), kh, -1)[:, :, place[name]]
+            code = torch.where(e % 2 == 0, raw >> 4, raw & 15).long()
+            a = s[name + "_absmax"][pages].double().repeat_interleave(case["blocksize"], -1)
+            wide[name] = (s["book"].double()[code] * a).transpose(0, 1).reshape(kh, -1, d)[:, :le]
+        hidden = torch.zeros(n, le, dtype=torch.bool)
+        for i in range(n):
+            if case["op"] == "tree":
+                line = [i]  # the row and its ancestors, up to the root
+                while line[-1]:
+                    line.append(int(s["parent"][b, line[-1]]))
+                place_of_row = le - n + len(line) - 1
+                hidden[i, le - n:] = True
+                hidden[i, [le - n + a for a in line]] = False
+                last = le - n
+            else:
+                place_of_row = le - n + i
+                hidden[i, place_of_row + 1:] = True
+                last = le
+            if case["window"]:  # cached positions too far back, but for the first ones
+                far = min(max(0, place_of_row - case["window"] + 1), last)
+                hidden[i, min(case["sinks"], far):far] = True
+        hidden = hidden.to(dev)
+        q = s["q"][first:first + n].double()
+        first += n
+        o = torch.empty(n, kh * group, d, dtype=torch.float64, device=dev)
+        for h in range(kh * group):
+            z = (q[:, h] @ wide["k"][h // group].T) * d ** -0.5
+            z[hidden] = -math.inf
+            # every row of these cases sees at least itself
+            o[:, h] = torch.softmax(z, -1) @ wide["v"][h // group]
+        outs.append(o)
+    return torch.cat(outs)
