@@ -43,31 +43,31 @@ def _attention(name, op, dtype="bf16", quant_type="nf4", blocksize=64, page=64, 
 def listed():
     return [
         # the activations of a single stream's step: latency only
-        _mx("requantize, one token", "requantize"),
+        _mx("requantize: one token", "requantize"),
         # a weight as it is loaded, and restored for a check
-        _mx("requantize, a weight", "requantize", rows=11008),
+        _mx("requantize: a weight", "requantize", rows=11008),
         # a single stream's step through the up projection of the stack of bench.py
-        _mx("product, one token", "product", n=11008),
+        _mx("product: one token", "product", n=11008),
         # a small serving batch through its down projection
-        _mx("product, 16 rows", "product", dtype="fp16", rows=16, k=11008, n=4096),
+        _mx("product: 16 rows", "product", dtype="fp16", rows=16, k=11008, n=4096),
         # a prompt through a wide projection: the matrix-bound end
-        _mx("product, prompt", "product", rows=2048, n=14336),
+        _mx("product: prompt", "product", rows=2048, n=14336),
         # an fp32 evaluation run of odd sizes, with a bias
-        _mx("product, odd sizes", "product", dtype="fp32", rows=333, k=1003, n=1531, bias=True),
+        _mx("product: odd sizes", "product", dtype="fp32", rows=333, k=1003, n=1531, bias=True),
         # a short chat, a small window: latency
-        _attention("sinks, one short sequence", "sinks", page=16, kv_len=301, window=128, sinks=4),
+        _attention("sinks: one short sequence", "sinks", page=16, kv_len=301, window=128, sinks=4),
         # serving sessions of mixed length, most past their window
-        _attention("sinks, serving batch", "sinks", batch=32, kv_len=16000, ragged=True, window=4096,
+        _attention("sinks: serving batch", "sinks", batch=32, kv_len=16000, ragged=True, window=4096,
                    sinks=4),
         # a long session's next chunk
-        _attention("sinks, prompt chunk", "sinks", dtype="fp16", batch=2, rows=512, kv_len=8000,
+        _attention("sinks: prompt chunk", "sinks", dtype="fp16", batch=2, rows=512, kv_len=8000,
                    ragged=True, window=2048, sinks=33),
         # a small tree of drafts after a short prompt: latency
-        _attention("tree, one short sequence", "tree", page=16, rows=13, kv_len=301),
+        _attention("tree: one short sequence", "tree", page=16, rows=13, kv_len=301),
         # serving with trees of up to 64 drafts
-        _attention("tree, serving batch", "tree", batch=16, rows=64, kv_len=6000, ragged=True),
+        _attention("tree: serving batch", "tree", batch=16, rows=64, kv_len=6000, ragged=True),
         # a tree over a long document, E2M1 codes, one kv head for all
-        _attention("tree, long document", "tree", quant_type="fp4", blocksize=32, page=256, heads=16,
+        _attention("tree: long document", "tree", quant_type="fp4", blocksize=32, page=256, heads=16,
                    kv_heads=2, rows=26, kv_len=131071),
     ]
 
