@@ -519,8 +519,11 @@ def linear(x: torch.Tensor, qs: QuantState, bias: torch.Tensor | None = None,
 
 from .kv import (  # noqa: E402  (needs the helpers above)
     KVCache, kv_attention, kv_attention_workspace_bytes, kv_read, kv_write)
+from .mx import (  # noqa: E402
+    MXTensor, mx_dequantize, mx_linear, mx_quantize, mx_workspace_bytes)
 
 __all__ = [
+    "MXTensor", "mx_quantize", "mx_dequantize", "mx_linear", "mx_workspace_bytes",
     "KVCache", "kv_write", "kv_read", "kv_attention", "kv_attention_workspace_bytes",
     "QuantState", "QWeightDesc", "Nf4Error", "lib", "exported_names", "codebook", "packed_bytes",
     "num_blocks", "quantize", "quantize_grouped", "double_quant", "dequantize",

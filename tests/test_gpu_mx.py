@@ -1,0 +1,289 @@
+"""Microscaled 4-bit matrices on the GPU against 64 bits: quantisation bit for bit,
+restoring, products from one row to many.
+
+Tolerance of a product. The operands' values are exact; a block of 32 products of E2M1 values
+is a sum of multiples of 1/4 below 2^11 and exact in fp32, so a 128-wide step adds four exact
+terms to the sum. Counted as 4 additions of relative error 2^-23 (truncation) of the sum of the
+absolute products at most, with 16 more where waves' sums are joined and the bias added:
+(4 steps + 20) 2^-23 sum |x w|, and half a step of the output's type."""
+import pytest
+import torch
+
+import mx_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+@pytest.fixture(scope="module")
+def nf4():
+    import bit_weight_quantization_nf4_amd as m
+
+    assert torch.cuda.is_available(), "no GPU"
+    m.lib()
+    return m
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rows_of(rows, cols, dtype, seed, spread=1.0):
+    g = gen(seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(spread * torch.randn(rows, 1, generator=g))
+    return (x * torch.exp(spread * torch.randn(cols, generator=g))).to(dtype)
+
+
+def check_quantized(nf4, x_host, x_dev):
+    t = nf4.mx_quantize(x_dev)
+    codes, scales = ref.quantize(x_host)
+    b, s = ref.store(codes, scales)
+    assert torch.equal(t.scales.cpu(), s), "scales differ"
+    assert torch.equal(t.codes.cpu(), b), "codes differ"
+    return t, codes, scales
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 31), (3, 33), (5, 128), (33, 130), (31, 512),
+                                       (64, 640), (70, 1003), (2, 4096), (129, 2050)])
+def test_quantize_and_restore(nf4, rows, cols, dtype):
+    x = rows_of(rows, cols, dtype, rows * 7 + cols)
+    t, codes, scales = check_quantized(nf4, x, x.cuda())
+    v = ref.values(codes, scales, cols)
+    for out in DTYPES:
+        assert torch.equal(nf4.mx_dequantize(t, out).cpu(), v.to(out))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("order", ["near", "mixed"])
+def test_quantize_every_pattern(nf4, dtype, order):
+    """All 65536 patterns, in blocks of neighbouring ones and mixed: ties, subnormals, zeros of
+    both signs, infinities and NaN."""
+    p = torch.arange(65536)
+    if order == "mixed":  # finite ones only, so that no block is lost to a NaN
+        p = p[torch.isfinite(p.to(torch.int16).view(dtype).float())]
+        p = p[torch.randperm(len(p), generator=gen(3))][:len(p) // 32 * 32]
+    x = torch.where(p >= 32768, p - 65536, p).to(torch.int16).view(dtype).view(-1, 32)
+    t, codes, scales = check_quantized(nf4, x, x.cuda())
+    v = ref.values(codes, scales, 32)
+    for out in (torch.bfloat16, torch.float32):
+        assert torch.equal(nf4.mx_dequantize(t, out).cpu().nan_to_num(7.0), v.to(out).nan_to_num(7.0))
+
+
+def test_quantize_fp32_patterns(nf4):
+    """Exponents over all of fp32, neighbours of the ties, and what is not finite."""
+    g = gen(4)
+    e = torch.randint(0, 255, (3000, 1), generator=g)
+    lower = (e - torch.randint(0, 6, (3000, 128), generator=g)).clamp(min=0)
+    m = torch.randint(0, 1 << 23, (3000, 128), generator=g)
+    tie = torch.tensor([0, 1 << 22, 1 << 21, 3 << 21])[torch.randint(0, 4, (3000, 128), generator=g)]
+    near = (tie + torch.randint(-1, 2, (3000, 128), generator=g)).clamp(0, (1 << 23) - 1)
+    m = torch.where(torch.rand(3000, 128, generator=g) < 0.5, m, near)
+    bits = lower << 23 | m
+    bits = torch.where(torch.rand(3000, 128, generator=g) < 0.5, bits, bits - (1 << 31))
+    x = bits.to(torch.int32).view(torch.float32)
+    x[7, 3], x[8, 40], x[9, 127] = torch.inf, -torch.inf, torch.nan
+    x[10], x[11, 32:64] = 0.0, -0.0
+    t, codes, scales = check_quantized(nf4, x, x.cuda())
+    v = ref.values(codes, scales, 128).float()  # 4 2^126 and larger are past fp32
+    assert torch.equal(nf4.mx_dequantize(t, torch.float32).cpu().nan_to_num(7.0), v.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_quantize_strided_views_and_outputs(nf4, dtype):
+    """Rows at any distance and alignment, leading dimensions, outputs within a larger one."""
+    big = rows_of(40, 700, dtype, 11)
+    dev = big.cuda()
+    for view in (lambda t: t[:, 1:334], lambda t: t[3:21:2, :512], lambda t: t[:, 16:656],
+                 lambda t: t[5], lambda t: t.view(4, 10, 700)[..., 5:100], lambda t: t.T,
+                 lambda t: t[:1, 3:67]):
+        x = view(big)
+        check_quantized(nf4, x.reshape(-1, x.shape[-1]), view(dev))
+    t = nf4.mx_quantize(dev[:, :333])
+    room = torch.full((42, 400), 9.0, dtype=dtype, device="cuda")
+    nf4.mx_dequantize(t, out=room[1:41, 7:340])
+    assert torch.equal(room[1:41, 7:340], nf4.mx_dequantize(t, dtype))
+    room[1:41, 7:340] = 9.0
+    assert bool((room == 9.0).all())
+    again = nf4.MXTensor.empty(40, 333)
+    assert nf4.mx_quantize(dev[:, :333], out=again) is again
+    assert torch.equal(again.codes, t.codes) and torch.equal(again.scales, t.scales)
+
+
+def test_restore_every_scale_and_code(nf4):
+    codes = torch.arange(16).repeat(256, 8)
+    scales = torch.arange(256)[:, None].repeat(1, 4)
+    b, s = ref.store(codes, scales)
+    t = nf4.MXTensor(b.cuda(), s.cuda(), (256, 128))
+    v = ref.values(codes, scales, 128)
+    for dtype in DTYPES:
+        got, want = nf4.mx_dequantize(t, dtype).cpu(), v.to(dtype)
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got.nan_to_num(7.0, 8.0, 9.0), want.nan_to_num(7.0, 8.0, 9.0))
+
+
+# ------------------------------------------------------------------- products
+
+
+def weight_of(nf4, n, k, seed):
+    w = rows_of(n, k, torch.float32, seed, 0.5)
+    return nf4.mx_quantize(w.cuda())
+
+
+def dense(t):
+    codes, scales = ref.load(t.codes.cpu(), t.scales.cpu())
+    return ref.values(codes, scales, t.shape[1])
+
+
+def check_product(y, x64, w64, bias, k, note=""):
+    want = x64 @ w64.T
+    size = x64.abs() @ w64.abs().T
+    if bias is not None:
+        want = want + bias.double()
+        size = size + bias.double().abs()
+    steps = ref.padded(k) // 128
+    eps = torch.finfo(y.dtype).eps / 2
+    bound = (4 * steps + 20) * 2.0 ** -23 * size * (1 + eps) + eps * want.abs() + \
+        torch.finfo(y.dtype).smallest_normal * eps
+    off = (y.cpu().double() - want).abs()
+    # a partial sum may be as large as the sum of the absolute products: where that passes fp32's
+    # largest number, 2^128 (1 - 2^-24), the result may be an infinity, or NaN from two of them
+    fits = size < 2.0 ** 127
+    assert bool((off <= bound)[fits].all()), (note, float((off - bound)[fits].max()))
+    return fits
+
+
+SHAPES = [(1, 1, 1), (1, 16, 128), (1, 11, 1003), (2, 33, 256), (1, 300, 4096), (3, 17, 4224),
+          (16, 65, 384), (5, 1000, 11008), (17, 40, 640), (32, 31, 129), (33, 100, 1024),
+          (64, 130, 2048), (65, 1, 128), (65, 129, 130), (128, 128, 512), (200, 333, 1003),
+          (257, 255, 384), (513, 640, 256), (300, 1, 4096), (1000, 520, 896)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_product(nf4, m, n, k, dtype):
+    w = weight_of(nf4, n, k, n + k)
+    x = rows_of(m, k, dtype, m + k, 0.5)
+    q = nf4.mx_quantize(x.cuda())
+    x64, w64 = dense(q), dense(w)
+    y = nf4.mx_linear(x.cuda(), w)
+    assert y.dtype == dtype and y.shape == (m, n)
+    check_product(y, x64, w64, None, k, "raw x")
+    # quantizing x in the call or before is the same
+    assert torch.equal(nf4.mx_linear(q, w, out_dtype=dtype), y)
+    g = gen(9)
+    bias = torch.randn(n, generator=g)
+    for out in DTYPES:
+        b = bias.to(out)
+        y = nf4.mx_linear(q, w, b.cuda(), out_dtype=out)
+        check_product(y, x64, w64, b, k, out)
+        assert torch.equal(nf4.mx_linear(x.cuda(), w, b.cuda(), out_dtype=out), y)
+
+
+@pytest.mark.parametrize("m", [1, 7, 40, 130])
+def test_product_strides(nf4, m):
+    """Strided x and outputs, of any alignment; what lies beside an output stays."""
+    n, k = 45, 333
+    w = weight_of(nf4, n, k, 1)
+    x = rows_of(m, k + 20, torch.bfloat16, 2).cuda()
+    for at in (0, 3, 8):
+        want = nf4.mx_linear(x[:, at:at + k].contiguous(), w)
+        room = torch.full((m + 2, n + 9), 5.0, dtype=torch.bfloat16, device="cuda")
+        got = nf4.mx_linear(x[:, at:at + k], w, out=room[1:m + 1, 3:3 + n])
+        assert torch.equal(got, want)
+        room[1:m + 1, 3:3 + n] = 5.0
+        assert bool((room == 5.0).all())
+    x3 = x[:, :k].contiguous().view(1, m, k)
+    assert torch.equal(nf4.mx_linear(x3, w), nf4.mx_linear(x3[0], w))
+
+
+@pytest.mark.parametrize("m", [1, 20, 150])
+def test_blocks_that_are_not_finite_spoil_their_row_or_column_only(nf4, m):
+    n, k = 70, 512
+    wd = rows_of(n, k, torch.float32, 1)
+    x = rows_of(m, k, torch.float32, 2)
+    clean = nf4.mx_linear(x.cuda(), nf4.mx_quantize(wd.cuda()))
+    wd[13, 100], wd[69, 511] = torch.nan, torch.inf
+    x[m // 2, 17] = -torch.inf
+    y = nf4.mx_linear(x.cuda(), nf4.mx_quantize(wd.cuda()))
+    lost = torch.zeros(m, n, dtype=torch.bool)
+    lost[m // 2], lost[:, 13], lost[:, 69] = True, True, True
+    assert torch.equal(y.isnan().cpu(), lost)
+    assert torch.equal(y.cpu()[~lost], clean.cpu()[~lost])
+
+
+def test_large_and_small_scales(nf4):
+    """Scales whose product passes fp32's range or falls below it, rows of unequal size."""
+    n, k = 32, 256
+    for m in (3, 80):
+        for ex, ew in ((100, -100), (-100, 100), (60, 60), (-60, -60), (0, 0)):
+            x = (rows_of(m, k, torch.float32, 5) * 2.0 ** ex).cuda()
+            w = nf4.mx_quantize((rows_of(n, k, torch.float32, 6) * 2.0 ** ew).cuda())
+            q = nf4.mx_quantize(x)
+            fits = check_product(nf4.mx_linear(x, w), dense(q), dense(w), None, k, (ex, ew))
+            assert bool(fits.all()) or (ex, ew) == (60, 60)
+            assert bool(fits.any())
+
+
+def test_products_of_zero_sizes(nf4):
+    w = weight_of(nf4, 8, 64, 1)
+    assert nf4.mx_linear(torch.empty(0, 64, device="cuda"), w).shape == (0, 8)
+    none = nf4.MXTensor.empty(0, 64)
+    assert nf4.mx_linear(torch.ones(3, 64, device="cuda"), none).shape == (3, 0)
+    assert nf4.mx_quantize(torch.empty(0, 64, device="cuda")).shape == (0, 64)
+    assert nf4.mx_dequantize(none).shape == (0, 64)
+
+
+def test_binding_refusals(nf4):
+    w = weight_of(nf4, 8, 64, 1)
+    x = torch.ones(3, 64, device="cuda")
+    with pytest.raises(ValueError):
+        nf4.mx_linear(x[:, :63], w)
+    with pytest.raises(TypeError):
+        nf4.mx_linear(x.double(), w)
+    with pytest.raises(ValueError):
+        nf4.mx_linear(x, w, torch.ones(8, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        nf4.mx_linear(x, w, torch.ones(7, device="cuda"))
+    with pytest.raises(ValueError):
+        nf4.mx_linear(x, w, out=torch.empty(3, 9, device="cuda"))
+    with pytest.raises(ValueError):
+        nf4.mx_linear(x, w, out=torch.empty(8, 3, device="cuda").T)
+    with pytest.raises(TypeError):
+        nf4.mx_linear(x, w, out_dtype=torch.int32)
+    with pytest.raises(ValueError):
+        nf4.MXTensor(w.codes[:, ::2], w.scales, (8, 64))
+    with pytest.raises(ValueError):
+        nf4.mx_quantize(x, out=w)
+    with pytest.raises(TypeError):
+        nf4.mx_dequantize(w, torch.int8)
+
+
+@pytest.mark.parametrize("m", [1, 24, 300])
+def test_streams_and_graphs(nf4, m):
+    """A side stream, and a captured call replayed on other inputs beside eager work."""
+    n, k = 96, 1024
+    w = weight_of(nf4, n, k, 3)
+    xs = [rows_of(m, k, torch.bfloat16, s).cuda() for s in (1, 2, 3)]
+    want = [nf4.mx_linear(x, w) for x in xs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = nf4.mx_linear(xs[1], w)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want[1])
+    held = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t = nf4.mx_quantize(held)
+        out = nf4.mx_linear(held, w)
+        same = nf4.mx_linear(t, w)
+        back = nf4.mx_dequantize(t)
+    for x, y in zip(xs * 2, want * 2):
+        held.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = nf4.mx_quantize(x)
+        assert torch.equal(out, y) and torch.equal(same, y)
+        assert torch.equal(back, nf4.mx_dequantize(eager))
