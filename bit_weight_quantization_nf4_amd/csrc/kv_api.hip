@@ -1,5 +1,5 @@
-// kv_api.hip -- the extern "C" boundary of the 4-bit key/value cache (declared
-// in include/nf4_kv.h): argument validation and dispatch to the launchers.
+// kv_api.hip -- the extern "C" boundary of the 4-bit key/value cache (declared in
+// include/nf4_kv.h and nf4_kv_mask.h): argument validation and dispatch to the launchers.
 // Every check runs before the first launch, so a rejected call writes nothing.
 #include <math.h>
 
@@ -117,6 +117,50 @@ nf4_status check_rows(const void *p, int64_t row_stride, int64_t head_stride, in
   return NF4_OK;
 }
 
+int64_t attention_bytes(const KvAttentionSizes &z) {
+  if (z.batch < 0 || z.max_rows < 0 || z.max_len < 0 || z.heads <= 0 || z.kv_heads <= 0 ||
+      z.heads % z.kv_heads != 0 || !valid_head_dim(z.head_dim) || !valid_dtype(z.dtype) ||
+      z.window < 0)
+    return -1;
+  if (z.batch == 0 || z.max_rows == 0) return 0;
+  return kv_attention_fits(z) ? kv_attention_bytes(z) : -1;
+}
+
+nf4_status attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, const KvAttentionCall &c,
+                     int32_t num_heads, int32_t dtype, int32_t window, int32_t sinks,
+                     int32_t max_rows, int32_t max_len, int64_t workspace_bytes, void *stream) {
+  KvArgs kv;
+  KvShape sh;
+  bool any = false;
+  nf4_status st = check_call(cache, rows, dtype, &kv, &sh, &any);
+  if (st != NF4_OK) return st;
+  if (num_heads <= 0 || num_heads % kv.kv_heads != 0) return NF4_ERR_INVALID_ARGUMENT;
+  if (window < 0 || max_rows < 0 || max_len < 0 || workspace_bytes < 0 || !isfinite(c.scale))
+    return NF4_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes > 0 && c.workspace == nullptr) return NF4_ERR_INVALID_ARGUMENT;
+  st = check_rows(c.q, c.q_row, c.q_head, num_heads, sh.head_dim, dtype, kv, any);
+  if (st != NF4_OK) return st;
+  st = check_rows(c.out, c.out_row, c.out_head, num_heads, sh.head_dim, dtype, kv, any);
+  if (st != NF4_OK) return st;
+  if (!aligned(c.workspace, 16) || !aligned(c.tree, 4)) return NF4_ERR_MISALIGNED;
+  if (!any) return NF4_OK;
+  const KvAttentionSizes z{
+      kv.batch, kv.offsets == nullptr ? kv.uniform : (max_rows > 0 ? max_rows : kv.total_rows),
+      max_len > 0 ? max_len : kv.capacity, num_heads, kv.kv_heads, sh.head_dim, dtype, window,
+      sinks};
+  if (!kv_attention_fits(z)) return NF4_ERR_UNSUPPORTED;
+  st = nf4_device_check();
+  if (st != NF4_OK) return st;
+  const int64_t need = kv_attention_bytes(z);
+  if (workspace_bytes < need) return NF4_ERR_SCRATCH;
+  if (log_on())
+    log_msg("kv_attention%s rows=%d batch=%d heads=%d/%d head_dim=%d bs=%d dtype=%d max_rows=%d "
+            "max_len=%d: kv_attention_kernel%s", c.masked ? "_masked" : "", kv.total_rows, kv.batch,
+            num_heads, kv.kv_heads, sh.head_dim, sh.blocksize, dtype, z.max_rows, z.max_len,
+            need > 0 ? ", positions split, joined by kv_attention_join_kernel" : "");
+  return from_hip(launch_kv_attention(kv, sh, z, c, reinterpret_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -170,13 +214,17 @@ nf4_status nf4_kv_read(const nf4_kv_cache *cache, const nf4_kv_rows *rows, int32
 int64_t nf4_kv_attention_workspace_bytes(int32_t batch, int32_t max_rows, int32_t max_len,
                                          int32_t num_heads, int32_t num_kv_heads,
                                          int32_t head_dim, int32_t dtype, int32_t window) {
-  if (batch < 0 || max_rows < 0 || max_len < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-      num_heads % num_kv_heads != 0 || !valid_head_dim(head_dim) || !valid_dtype(dtype) ||
-      window < 0)
-    return -1;
-  if (batch == 0 || max_rows == 0) return 0;
-  const KvAttentionSizes z{batch, max_rows, max_len, num_heads, num_kv_heads, head_dim, dtype, window};
-  return kv_attention_fits(z) ? kv_attention_bytes(z) : -1;
+  return attention_bytes(
+      {batch, max_rows, max_len, num_heads, num_kv_heads, head_dim, dtype, window});
+}
+
+int64_t nf4_kv_attention_masked_workspace_bytes(int32_t batch, int32_t max_rows, int32_t max_len,
+                                                int32_t num_heads, int32_t num_kv_heads,
+                                                int32_t head_dim, int32_t dtype, int32_t window,
+                                                int32_t sinks) {
+  if (sinks < 0) return -1;
+  return attention_bytes(
+      {batch, max_rows, max_len, num_heads, num_kv_heads, head_dim, dtype, window, sinks});
 }
 
 nf4_status nf4_kv_attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, const void *q,
@@ -185,21 +233,6 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, 
                             int32_t max_rows, int32_t max_len, void *out, int64_t out_row_stride,
                             int64_t out_head_stride, void *workspace, int64_t workspace_bytes,
                             void *stream) {
-  KvArgs kv;
-  KvShape sh;
-  bool any = false;
-  nf4_status st = check_call(cache, rows, dtype, &kv, &sh, &any);
-  if (st != NF4_OK) return st;
-  if (num_heads <= 0 || num_heads % kv.kv_heads != 0) return NF4_ERR_INVALID_ARGUMENT;
-  if (window < 0 || max_rows < 0 || max_len < 0 || workspace_bytes < 0 || !isfinite(scale))
-    return NF4_ERR_INVALID_ARGUMENT;
-  if (workspace_bytes > 0 && workspace == nullptr) return NF4_ERR_INVALID_ARGUMENT;
-  st = check_rows(q, q_row_stride, q_head_stride, num_heads, sh.head_dim, dtype, kv, any);
-  if (st != NF4_OK) return st;
-  st = check_rows(out, out_row_stride, out_head_stride, num_heads, sh.head_dim, dtype, kv, any);
-  if (st != NF4_OK) return st;
-  if (!aligned(workspace, 16)) return NF4_ERR_MISALIGNED;
-  if (!any) return NF4_OK;
   KvAttentionCall c;
   c.q = q;
   c.out = out;
@@ -210,20 +243,38 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, 
   c.scale = scale;
   c.causal = causal != 0;
   c.workspace = workspace;
-  const KvAttentionSizes z{
-      kv.batch, kv.offsets == nullptr ? kv.uniform : (max_rows > 0 ? max_rows : kv.total_rows),
-      max_len > 0 ? max_len : kv.capacity, num_heads, kv.kv_heads, sh.head_dim, dtype, window};
-  if (!kv_attention_fits(z)) return NF4_ERR_UNSUPPORTED;
-  st = nf4_device_check();
-  if (st != NF4_OK) return st;
-  const int64_t need = kv_attention_bytes(z);
-  if (workspace_bytes < need) return NF4_ERR_SCRATCH;
-  if (log_on())
-    log_msg("kv_attention rows=%d batch=%d heads=%d/%d head_dim=%d bs=%d dtype=%d max_rows=%d "
-            "max_len=%d: kv_attention_kernel%s", kv.total_rows, kv.batch, num_heads, kv.kv_heads,
-            sh.head_dim, sh.blocksize, dtype, z.max_rows, z.max_len,
-            need > 0 ? ", positions split, joined by kv_attention_join_kernel" : "");
-  return from_hip(launch_kv_attention(kv, sh, z, c, reinterpret_cast<hipStream_t>(stream)));
+  return attention(cache, rows, c, num_heads, dtype, window, 0, max_rows, max_len, workspace_bytes,
+                   stream);
+}
+
+nf4_status nf4_kv_attention_masked(const nf4_kv_cache *cache, const nf4_kv_rows *rows,
+                                   const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                                   int32_t num_heads, int32_t dtype, float scale, int32_t window,
+                                   int32_t sinks, const uint32_t *tree, int64_t tree_stride,
+                                   int32_t tree_words, int32_t max_rows, int32_t max_len, void *out,
+                                   int64_t out_row_stride, int64_t out_head_stride,
+                                   void *workspace, int64_t workspace_bytes, void *stream) {
+  if (sinks < 0) return NF4_ERR_INVALID_ARGUMENT;
+  if (tree != nullptr && (tree_words < 0 || tree_stride < tree_words ||
+                          (rows != nullptr && rows->total_rows > 0 &&
+                           tree_stride > (INT64_MAX >> 3) / rows->total_rows)))
+    return NF4_ERR_INVALID_ARGUMENT;
+  KvAttentionCall c;
+  c.q = q;
+  c.out = out;
+  c.q_row = q_row_stride;
+  c.q_head = q_head_stride;
+  c.out_row = out_row_stride;
+  c.out_head = out_head_stride;
+  c.scale = scale;
+  c.causal = 1;
+  c.workspace = workspace;
+  c.masked = true;
+  c.tree = tree;
+  c.tree_stride = tree_stride;
+  c.tree_words = tree_words;
+  return attention(cache, rows, c, num_heads, dtype, window, sinks, max_rows, max_len,
+                   workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -14,24 +14,24 @@ namespace {
 // become zeros.
 constexpr int kJoinWaves = 4;
 
-template <int D, int DT, bool ROWS_APART>
-__global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(AttnArgs, int align) {
+template <int D, int DT, bool ROWS_APART, bool MASK>
+__global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(ArgsOf<MASK>, int align) {
   constexpr int C = (D + 127) / 128;  // element pairs of a lane, at 2 lane + 128 c
   constexpr int SW = ROWS_APART ? 1 : kJoinWaves;  // waves of a row
   __shared__ float acc[SW][D];
   __shared__ float sums[SW];
-  fetch_args();
-  KernelArgs &args = *kernel_args();
+  fetch_args<MASK>();
+  KernelArgsOf<MASK> &args = *kernel_args<MASK>();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sw = ROWS_APART ? 0 : wave;
   const int pair = ROWS_APART ? (int)blockIdx.x * kJoinWaves + wave : (int)blockIdx.x;
   const int h = (int)blockIdx.y, seq = (int)blockIdx.z;
   const int wb = args.wg_blocks == 1 ? 0 : pair / args.wg_rows, row = pair - wb * args.wg_rows;
-  const Block blk = block_of(args, sequence_of(args, seq), wb * args.wg_rows, args.wg_rows);
+  const Block blk = block_of<MASK>(args, sequence_of(args, seq), wb * args.wg_rows, args.wg_rows);
   if (pair >= blk.pairs) return;
   const int range = range_of(blk, args.splits, align);
-  const int pieces = range > 0 ? (blk.hi - blk.lo - 1) / range + 1 : 0;  // (no sum past 2^31)
+  const int pieces = range > 0 ? (span_of(blk) - 1) / range + 1 : 0;  // (no sum past 2^31)
   const int64_t base = item_of(args, seq, h, wb) * args.splits * args.part_rows + row;
   auto part_row = [&](int i) { return base + (int64_t)i * args.part_rows; };
 
@@ -138,7 +138,8 @@ Plan plan_of(const KvAttentionSizes &z) {
   // positions that a row sees at most, in units of the time that one takes at 16 bits
   // and head_dim 128
   int64_t span = z.max_len;
-  if (z.window > 0 && span > (int64_t)z.window + z.max_rows) span = (int64_t)z.window + z.max_rows;
+  const int64_t reach = (int64_t)z.window + z.sinks + z.max_rows;
+  if (z.window > 0 && span > reach) span = reach;
   const int64_t weight = z.head_dim * (z.dtype == kFP32 ? 3 : 1);
   int64_t s = 1;
   if (span * weight >= (p.merge ? kSplitFrom : kSplitFromApart) * 128) {
@@ -183,33 +184,40 @@ uint32_t f16_bits(double v, double *rest) {
   return b;
 }
 
-template <int D, int DT>
-hipError_t launch_join(const AttnArgs &a, const Plan &p, hipStream_t stream) {
+template <int D, int DT, bool MASK>
+hipError_t launch_join(const ArgsOf<MASK> &a, const Plan &p, hipStream_t stream) {
   const int rows = a.max_rows * a.group;
   dim3 grid((unsigned)rows, (unsigned)a.kv.kv_heads, (unsigned)a.kv.batch);
   if (p.merge) {
-    hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, false>), grid, dim3(64 * kJoinWaves), 0,
+    hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, false, MASK>), grid, dim3(64 * kJoinWaves), 0,
                        stream, a, p.align);
   } else {
     grid.x = (unsigned)ceil_div(rows, kJoinWaves);
-    hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, true>), grid, dim3(64 * kJoinWaves), 0,
+    hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, true, MASK>), grid, dim3(64 * kJoinWaves), 0,
                        stream, a, p.align);
   }
   return hipGetLastError();
 }
 
-template <int DT>
-hipError_t launch_dt(const AttnArgs &a, const Plan &p, const KvShape &sh, hipStream_t stream) {
-  const hipError_t e = launch_shape<DT>(a, p, sh.head_dim, sh.blocksize, stream);
+template <int DT, bool MASK>
+hipError_t launch_dt(const ArgsOf<MASK> &a, const Plan &p, const KvShape &sh, hipStream_t stream) {
+  const hipError_t e = launch_shape<DT, MASK>(a, p, sh.head_dim, sh.blocksize, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   switch (sh.head_dim) {
-    case 64: return launch_join<64, DT>(a, p, stream);
-    case 96: return launch_join<96, DT>(a, p, stream);
-    case 128: return launch_join<128, DT>(a, p, stream);
-    case 192: return launch_join<192, DT>(a, p, stream);
-    case 256: return launch_join<256, DT>(a, p, stream);
+    case 64: return launch_join<64, DT, MASK>(a, p, stream);
+    case 96: return launch_join<96, DT, MASK>(a, p, stream);
+    case 128: return launch_join<128, DT, MASK>(a, p, stream);
+    case 192: return launch_join<192, DT, MASK>(a, p, stream);
+    case 256: return launch_join<256, DT, MASK>(a, p, stream);
   }
   return hipErrorNotSupported;
+}
+
+template <bool MASK>
+hipError_t launch_type(const ArgsOf<MASK> &a, const Plan &p, const KvShape &sh, hipStream_t stream) {
+  if (sh.dtype == kFP32) return launch_dt<kFP32, MASK>(a, p, sh, stream);
+  if (sh.dtype == kFP16) return launch_dt<kFP16, MASK>(a, p, sh, stream);
+  return launch_dt<kBF16, MASK>(a, p, sh, stream);
 }
 
 }  // namespace
@@ -232,7 +240,7 @@ bool kv_attention_fits(const KvAttentionSizes &z) {
 hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAttentionSizes &z,
                                const KvAttentionCall &c, hipStream_t stream) {
   const Plan p = plan_of(z);
-  AttnArgs a;
+  MaskedArgs a;
   a.kv = kv;
   a.q = c.q;
   a.out = c.out;
@@ -259,9 +267,12 @@ hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAtte
     const uint32_t c1 = f16_bits((double)t.value[i] * mu, &rest);
     a.codes[i] = c1 | f16_bits(rest, nullptr) << 16;
   }
-  if (sh.dtype == kFP32) return launch_dt<kFP32>(a, p, sh, stream);
-  if (sh.dtype == kFP16) return launch_dt<kFP16>(a, p, sh, stream);
-  return launch_dt<kBF16>(a, p, sh, stream);
+  if (!c.masked) return launch_type<false>(a, p, sh, stream);
+  a.sinks = z.window > 0 ? z.sinks : 0;
+  a.tree = c.tree;
+  a.tree_stride = c.tree_stride;
+  a.tree_words = c.tree_words;
+  return launch_type<true>(a, p, sh, stream);
 }
 
 }  // namespace nf4

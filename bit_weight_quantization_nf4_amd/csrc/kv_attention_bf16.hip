@@ -4,7 +4,7 @@
 namespace nf4 {
 namespace kvattn {
 
-template hipError_t launch_shape<kBF16>(const AttnArgs &, const Plan &, int, int, hipStream_t);
+NF4_KV_SHAPES(kBF16, false)
 
 }  // namespace kvattn
 }  // namespace nf4

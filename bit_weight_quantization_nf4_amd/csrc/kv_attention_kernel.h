@@ -97,22 +97,37 @@ struct AttnArgs {
   uint32_t codes[16];  // by nibble: c1 in the low half, c2 in the high one (fp16)
 };
 
+// What the masked form (nf4_kv_mask.h) takes besides: first positions that stay visible
+// behind a window, and a tree of the call's rows.
+struct MaskedArgs : AttnArgs {
+  int32_t sinks;        // 0 without a window
+  int32_t tree_words;   // 32-bit words of a row's mask
+  const uint32_t *tree; // null: rows see what is before them
+  int64_t tree_stride;  // words between rows
+};
+
 // The kernels read their arguments through this type, from the argument segment
 // and through a pointer that is renewed where a kernel's phases meet: held in
 // scalar registers from end to end they would not leave enough of these.
-typedef const __attribute__((address_space(4))) AttnArgs KernelArgs;
+template <bool MASK>
+using ArgsOf = std::conditional_t<MASK, MaskedArgs, AttnArgs>;
+template <bool MASK>
+using KernelArgsOf = const __attribute__((address_space(4))) ArgsOf<MASK>;
+typedef KernelArgsOf<false> KernelArgs;
 
-__device__ __forceinline__ KernelArgs *kernel_args() {
-  auto *p = (KernelArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+template <bool MASK = false>
+__device__ __forceinline__ KernelArgsOf<MASK> *kernel_args() {
+  auto *p = (KernelArgsOf<MASK> *)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(p));
   return p;
 }
 
 // Has every 64-byte line of the arguments on its way to the scalar cache at once:
 // they lie in host memory, and a line takes about a microsecond.
+template <bool MASK = false>
 __device__ __forceinline__ void fetch_args() {
-  const auto *p = (const __attribute__((address_space(4))) uint32_t *)kernel_args();
-  constexpr int kLines = (sizeof(AttnArgs) + 63) / 64;
+  const auto *p = (const __attribute__((address_space(4))) uint32_t *)kernel_args<MASK>();
+  constexpr int kLines = (sizeof(ArgsOf<MASK>) + 63) / 64;
   uint32_t v[kLines];
 #pragma unroll
   for (int i = 0; i < kLines; ++i) v[i] = p[16 * i];
@@ -129,11 +144,15 @@ struct Block {
   int pairs;     // such pairs of the sequence (up to max_rows tokens)
   int lo, hi;    // positions [lo, hi) that any row of the block sees
   int all_lo, all_hi;  // positions that every row sees
+  int sink_hi;   // masked form: so do [0, sink_hi), whole steps that end before lo (0: none)
 };
+
+// Positions that a block goes through.
+__device__ __forceinline__ int span_of(const Block &b) { return b.sink_hi + (b.hi - b.lo); }
 
 // Positions of a range: equal multiples of `align`.
 __device__ __forceinline__ int range_of(const Block &b, int splits, int align) {
-  const int total = b.hi - b.lo;
+  const int total = span_of(b);
   const int range = splits == 1 ? total : (total + splits - 1) / splits;
   return (range + align - 1) / align * align;
 }
@@ -179,7 +198,12 @@ __device__ __forceinline__ Sequence sequence_of(KernelArgs &a, int seq) {
   return s;
 }
 
-__device__ __forceinline__ Block block_of(KernelArgs &a, const Sequence &s, int row0, int rows) {
+// Rows of a tree see positions before the call's by their depth, which is not known here: at
+// most as many as the sequence has rows.
+template <bool MASK = false>
+__device__ __forceinline__ Block block_of(KernelArgsOf<MASK> &args, const Sequence &s, int row0,
+                                          int rows) {
+  KernelArgs &a = args;
   Block b;
   b.n = s.n;
   b.first = s.first;
@@ -187,20 +211,53 @@ __device__ __forceinline__ Block block_of(KernelArgs &a, const Sequence &s, int 
   const int tokens = b.n < a.max_rows ? b.n : a.max_rows;
   b.pairs = tokens * a.group;
   b.row0 = row0;
-  b.lo = b.hi = b.all_lo = b.all_hi = 0;
+  b.lo = b.hi = b.all_lo = b.all_hi = b.sink_hi = 0;
   if (b.row0 < b.pairs) {
     // divisions only where a sequence has several blocks
     const int token0 = row0 == 0 ? 0 : row0 / a.group;
     const int token1 = row0 + rows >= b.pairs ? tokens - 1 : (row0 + rows - 1) / a.group;
-    const int end0 = seen_end(a, b, token0), end1 = seen_end(a, b, token1);
+    int end0 = seen_end(a, b, token0), end1 = seen_end(a, b, token1);
+    if constexpr (MASK) {
+      if (args.tree != nullptr) {
+        end0 = b.len - b.n;
+        end1 = b.len;
+      }
+    }
     b.hi = within(a, end1);
     b.lo = seen_begin(a, end0);
     b.all_hi = within(a, end0);
     b.all_lo = seen_begin(a, end1);
     if (b.hi <= b.lo) b.lo = b.hi = 0;
     b.lo &= ~(kStep - 1);
+    if constexpr (MASK) {
+      const int sinks = args.sinks < b.hi ? args.sinks : b.hi;
+      const int whole = (sinks + kStep - 1) & ~(kStep - 1);
+      if (whole < b.lo) b.sink_hi = whole;
+      else if (sinks > 0) b.lo = 0;
+    }
   }
   return b;
+}
+
+// Rows of a tree that row `token` of a block's sequence sees (of those the sequence has).
+__device__ __forceinline__ int rows_seen(KernelArgsOf<true> &a, const Block &b, int token) {
+  const uint32_t *row = a.tree + (int64_t)(b.first + token) * a.tree_stride;
+  int count = 0;
+  for (int w = 0; w < a.tree_words && 32 * w < b.n; ++w) {
+    const int left = b.n - 32 * w;
+    count += __popc(left < 32 ? row[w] & ((1u << left) - 1) : row[w]);
+  }
+  return count;
+}
+
+// Bits `first` ... `first` + 31 of that row's mask, zeros where it has none.
+__device__ __forceinline__ uint32_t tree_bits(KernelArgsOf<true> &a, const Block &b, int token,
+                                              int first) {
+  const uint32_t *row = a.tree + (int64_t)(b.first + token) * a.tree_stride;
+  const int w = first >> 5, sh = first & 31;
+  const uint32_t lo = w >= 0 && w < a.tree_words ? row[w] : 0;
+  const uint32_t hi = w + 1 >= 0 && w + 1 < a.tree_words ? row[w + 1] : 0;
+  return sh == 0 ? lo : lo >> sh | hi << (32 - sh);
 }
 
 // Byte SRC of w as the second byte of a table address, lane_off as its first.
@@ -367,10 +424,10 @@ struct StepIn {
   float ks[(8 * (D / BS) + 15) / 16], vs[(8 * (D / BS) + 15) / 16];
 };
 
-template <int D, int BS, int DT, int NR, bool MERGE>
+template <int D, int BS, int DT, int NR, bool MERGE, bool MASK>
 __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute__((
     amdgpu_waves_per_eu(Attn<D, BS, DT, NR, MERGE>::kWavesPerSimd))) void kv_attention_kernel(
-    AttnArgs) {
+    ArgsOf<MASK>) {
   using A = Attn<D, BS, DT, NR, MERGE>;
   constexpr int P = A::P, NB = A::NB, PB = A::PB, NS = A::NS;
   constexpr int kWaves = A::kWaves, kThreads = A::kThreads;
@@ -387,7 +444,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
                         (sizeof(lds) + sizeof(merge_buf) + sizeof(wave_m) + sizeof(wave_l) +
                          sizeof(total_l) + sizeof(wave_top)) <= 160 * 1024, "LDS");
 
-  fetch_args();
+  fetch_args<MASK>();
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int tw = MERGE ? wave : 0;
   const uint32_t my_code = kernel_args()->codes[threadIdx.x & 15];
@@ -410,7 +467,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   const int lane = (int)threadIdx.x & 63;
   const int n = lane & 15, g = lane >> 4;
   const uint32_t lane_off = 4u * (lane & 31);
-  KernelArgs &args = *kernel_args();
+  KernelArgsOf<MASK> &args = *kernel_args<MASK>();
   const auto &kv = args.kv;
   const int h = (int)blockIdx.y, seq = (int)blockIdx.z;
   int wb = (int)blockIdx.x, split = 0;
@@ -421,25 +478,45 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   // blocks of later rows see more positions: they come first
   wb = args.wg_blocks - 1 - wb;
   const Sequence of = sequence_of(args, seq);
-  const Block item = block_of(args, of, wb * args.wg_rows, args.wg_rows);
+  const Block item = block_of<MASK>(args, of, wb * args.wg_rows, args.wg_rows);
   const int range = range_of(item, args.splits, kStep * TW);
-  int begin = item.lo + split * range;
-  int end = range < item.hi - begin ? begin + range : item.hi;
-  // a workgroup without rows, or with a range past the positions, leaves nothing
-  // behind; with one range the rows that see nothing are still written
-  if (item.row0 >= item.pairs || (begin >= item.hi && args.splits > 1)) return;
+  int begin, end;
+  // masked form: the range's first steps, before `begin`'s, that are of the first positions
+  int sink_begin = 0, sink_steps = 0;
+  if constexpr (MASK) {
+    const int from = split * range, total = span_of(item);
+    if (item.row0 >= item.pairs || (from >= total && args.splits > 1)) return;
+    const int to = range < total - from ? from + range : total;
+    if (from < item.sink_hi) {
+      sink_begin = from;
+      sink_steps = ((to < item.sink_hi ? to : item.sink_hi) - from) / kStep;
+    }
+    const int back = item.lo - item.sink_hi;
+    begin = (from > item.sink_hi ? from : item.sink_hi) + back;
+    end = (to > item.sink_hi ? to : item.sink_hi) + back;
+  } else {
+    begin = item.lo + split * range;
+    end = range < item.hi - begin ? begin + range : item.hi;
+    // a workgroup without rows, or with a range past the positions, leaves nothing
+    // behind; with one range the rows that see nothing are still written
+    if (item.row0 >= item.pairs || (begin >= item.hi && args.splits > 1)) return;
+  }
   const bool whole_item = args.splits == 1;
   const int64_t part_row0 = (item_of(args, seq, h, wb) * args.splits + split) * args.part_rows;
   // a wave's own rows may see less, and there may be none
-  const Block blk = MERGE ? item : block_of(args, of, item.row0 + wave * A::kRows, A::kRows);
+  const Block blk = MERGE ? item : block_of<MASK>(args, of, item.row0 + wave * A::kRows, A::kRows);
   const bool have_rows = blk.row0 < blk.pairs;
   if (!MERGE) {
-    begin = begin > blk.lo ? begin : blk.lo;
+    // (where the block goes from position 0 on for the first ones' sake, its waves do)
+    bool later = true;
+    if constexpr (MASK) later = item.sink_hi > 0 || args.sinks == 0;
+    if (later) begin = begin > blk.lo ? begin : blk.lo;
     end = end < blk.hi ? end : blk.hi;
+    if (MASK && blk.hi == 0) sink_steps = 0;
   }
 
   // ---- where its steps lie, and the first one's inputs on their way
-  const int steps_all = end > begin ? (end - begin + kStep - 1) / kStep : 0;
+  const int steps_all = (end > begin ? (end - begin + kStep - 1) / kStep : 0) + sink_steps;
   const int nsteps = steps_all > tw ? (steps_all - tw + TW - 1) / TW : 0;
   // scalars of the loop, kept in registers
   const int64_t head_packed = (int64_t)h * kv.page_size * (16 * P);
@@ -456,17 +533,38 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   const int tiles_per_page = pin(kv.page_size / 16);
   // both tiles of a step in one page, which holds an even number of them
   const bool paired = (tiles_per_page & 1) == 0;
-  const int tile0 = (begin >> 4) + 2 * tw;
+  // the range's step i is at begin + 32 i, but for the masked form's first ones
+  if constexpr (MASK) begin -= kStep * sink_steps;
+  const int jump = MASK ? begin - sink_begin : 0;
+  auto position_of_step = [&](int i) {
+    return begin + kStep * i - (MASK && i < sink_steps ? jump : 0);
+  };
+  const int tile0 = MASK ? position_of_step(tw) >> 4 : (begin >> 4) + 2 * tw;
   const int first_col = nsteps > 0 ? tile0 / tiles_per_page : 0;
   int col = first_col, in_page = tile0 - first_col * tiles_per_page;
   const int step_cols = pin(2 * TW / tiles_per_page);
   const int step_in_page = pin(2 * TW - step_cols * tiles_per_page);
+  // (the masked form's: from the first positions' tiles to the others, at step `at`)
+  const int jump_cols = MASK ? pin((jump >> 4) / tiles_per_page) : 0;
+  const int jump_in_page = MASK ? pin((jump >> 4) - jump_cols * tiles_per_page) : 0;
+  int at = tw;
   auto advance = [&] {
     col += step_cols;
     in_page += step_in_page;
     if (in_page >= tiles_per_page) {
       in_page -= tiles_per_page;
       ++col;
+    }
+    if constexpr (MASK) {
+      if (at < sink_steps && at + TW >= sink_steps) {
+        col += jump_cols;
+        in_page += jump_in_page;
+        if (in_page >= tiles_per_page) {
+          in_page -= tiles_per_page;
+          ++col;
+        }
+      }
+      at += TW;
     }
   };
   // pages (and tiles within them) of a step's two 16-position tiles
@@ -515,7 +613,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   // where a window leaves no position of the wave's first step to all rows, that step comes
   // last: their common A is then known (52 rows of 16 sequences in a window of 1024: 14.2
   // us, 15.2 in order)
-  int step = nsteps > 1 && blk.all_lo >= begin + kStep * (tw + 1) ? 1 : 0;
+  int step = nsteps > 1 && sink_steps == 0 && blk.all_lo >= begin + kStep * (tw + 1) ? 1 : 0;
   if (step > 0) advance();
   StepIn<D, BS> in;
   // the scales that the lane holds: values 16 u + n of the DPP row's 8 positions
@@ -638,6 +736,18 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
       const int end_of_row = have ? seen_end(args, blk, row_at(16 * nr + n).token) : 0;
       row_hi[nr] = within(args, end_of_row);
       row_lo[nr] = seen_begin(args, end_of_row);
+      if constexpr (MASK) {
+        if (args.tree != nullptr) {
+          row_hi[nr] = have ? within(args, blk.len) : 0;
+          // its place in a window: the rows that it sees come behind the positions before the
+          // call's, which alone the window hides
+          if (have && args.window > 0) {
+            const int before = blk.len - blk.n;
+            const int lo = seen_begin(args, before + rows_seen(args, blk, row_at(16 * nr + n).token));
+            row_lo[nr] = lo < before ? lo : (before > 0 ? before : 0);
+          }
+        }
+      }
     }
     if constexpr (MERGE) {
       static_assert(NR * P <= kWaves, "a fragment for each wave");
@@ -729,23 +839,33 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
 
   const int all_lo = pin(blk.all_lo), all_hi = pin(blk.all_hi);
   const int any_hi = pin(blk.hi);
+  // masked form: positions before this one are seen by all rows too, those from `base` on by the
+  // tree
+  int all_sinks = 0, sinks = 0, base = 0x7fffffff;
+  if constexpr (MASK) {
+    sinks = pin(args.sinks);
+    all_sinks = pin(sinks < all_hi ? sinks : all_hi);
+    base = pin(args.tree != nullptr ? blk.len - blk.n : 0x7fffffff);
+  }
   for (int s = 0; s < nsteps; ++s) {
     // (steps begin at a multiple of 32 bytes: where the compiler happens to put them, many
     // rows take up to 2 % longer)
     asm volatile(".p2align 5");
-    const int pos0 = begin + kStep * (tw + TW * step);
+    const int pos0 = position_of_step(tw + TW * step);
     if (s + 1 < nsteps) {  // the last one loads its own inputs again
       advance();
       if (++step == nsteps) {
         step = 0;
         col = first_col;
         in_page = tile0 - first_col * tiles_per_page;
+        at = tw;
       }
     }
     const Where next_at = locate();
     const bool ok[2] = {ok0, ok1};
     // every row sees the whole step (uniform)
-    const bool whole = ok0 && ok1 && pos0 >= all_lo && pos0 + kStep <= all_hi;
+    bool whole = ok0 && ok1 && pos0 >= all_lo && pos0 + kStep <= all_hi;
+    if constexpr (MASK) whole = whole || (ok0 && ok1 && pos0 + kStep <= all_sinks);
 
     // ---- S^T = K Q^T, combined over blocks into log2 units past m_use
     f32x4 t[NR][2];
@@ -835,9 +955,28 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int p = pos0 + 16 * T + 4 * g + r;
-            const bool see = ok[T] && p >= row_lo[nr] && p < row_hi[nr];
+            bool see = ok[T] && p >= row_lo[nr] && p < row_hi[nr];
+            if constexpr (MASK) see = ok[T] && (p >= row_lo[nr] || p < sinks) && p < row_hi[nr];
             t[nr][T][r] = see ? t[nr][T][r] : -__builtin_inff();
           }
+      if constexpr (MASK) {
+        if (pos0 + kStep > base) {  // some of the positions are the call's rows
+          KernelArgsOf<MASK> &targs = *kernel_args<MASK>();
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            const int i = blk.row0 + 16 * nr + n < blk.pairs ? 16 * nr + n : 0;
+            const uint32_t bits = tree_bits(targs, blk, row_at(i).token, pos0 - base);
+#pragma unroll
+            for (int T = 0; T < 2; ++T)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int j = 16 * T + 4 * g + r;
+                const bool hidden = pos0 + j >= base && (bits >> j & 1) == 0;
+                t[nr][T][r] = hidden ? -__builtin_inff() : t[nr][T][r];
+              }
+          }
+        }
+      }
       // scales of positions that no row sees may be anything
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
@@ -873,7 +1012,8 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
         for (int u = 0; u < NS; ++u) {
           any = max2(any, size(u));
           const int p = pos0 + position_of(u);
-          av = max2(av, whole || (p >= all_lo && p < all_hi) ? size(u) : 0.0f);
+          const bool all = whole || (p >= all_lo && p < all_hi) || (MASK && p < all_sinks);
+          av = max2(av, all ? size(u) : 0.0f);
         }
         av = max_over_groups(row16_max(av));
         ex = __builtin_amdgcn_readfirstlane(
@@ -1073,7 +1213,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     m_ref[nr] = m_limit[nr] == kNothing ? kNothing : m_use[nr];
     a_row[nr] = a_exp - e_of(m_limit[nr]) - 8;
   }
-  KernelArgs &end_args = *kernel_args();
+  KernelArgs &end_args = *kernel_args<MASK>();
   const int tid = fresh((int)threadIdx.x);
   auto out_at = [&](int i) {
     const RowAt ra = row_at(i);
@@ -1206,32 +1346,32 @@ struct Plan {
 // Largest number of 16-row tiles of a wave's block: what its registers hold.
 constexpr int max_tiles(int head_dim) { return head_dim <= 128 ? 2 : 1; }
 
-template <int D, int BS, int DT, int NR, bool MERGE>
-hipError_t launch_one(const AttnArgs &a, hipStream_t stream) {
+template <int D, int BS, int DT, int NR, bool MERGE, bool MASK>
+hipError_t launch_one(const ArgsOf<MASK> &a, hipStream_t stream) {
   const dim3 grid((unsigned)(a.wg_blocks * a.splits), (unsigned)a.kv.kv_heads,
                   (unsigned)a.kv.batch);
-  hipLaunchKernelGGL((kv_attention_kernel<D, BS, DT, NR, MERGE>), grid,
+  hipLaunchKernelGGL((kv_attention_kernel<D, BS, DT, NR, MERGE, MASK>), grid,
                      dim3(Attn<D, BS, DT, NR, MERGE>::kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
-template <int D, int BS, int DT>
-hipError_t launch_main(const AttnArgs &a, const Plan &p, hipStream_t stream) {
+template <int D, int BS, int DT, bool MASK>
+hipError_t launch_main(const ArgsOf<MASK> &a, const Plan &p, hipStream_t stream) {
   constexpr int T = max_tiles(D);
-  if (!p.merge) return launch_one<D, BS, DT, T, false>(a, stream);
+  if (!p.merge) return launch_one<D, BS, DT, T, false, MASK>(a, stream);
   if constexpr (T > 1) {
-    if (p.tiles > 1) return launch_one<D, BS, DT, T, true>(a, stream);
+    if (p.tiles > 1) return launch_one<D, BS, DT, T, true, MASK>(a, stream);
   }
-  return launch_one<D, BS, DT, 1, true>(a, stream);
+  return launch_one<D, BS, DT, 1, true, MASK>(a, stream);
 }
 
-// Instantiated for each element type in a file of its own.
-template <int DT>
-hipError_t launch_shape(const AttnArgs &a, const Plan &p, int head_dim, int blocksize,
+// Instantiated for each element type, plain and masked, in a file of its own.
+template <int DT, bool MASK>
+hipError_t launch_shape(const ArgsOf<MASK> &a, const Plan &p, int head_dim, int blocksize,
                         hipStream_t stream) {
   switch (head_dim * 1000 + blocksize) {
 #define NF4_KV_CASE(DV, BSV) \
-  case DV * 1000 + BSV: return launch_main<DV, BSV, DT>(a, p, stream);
+  case DV * 1000 + BSV: return launch_main<DV, BSV, DT, MASK>(a, p, stream);
     NF4_KV_CASE(64, 32)
     NF4_KV_CASE(64, 64)
     NF4_KV_CASE(96, 32)
@@ -1248,9 +1388,15 @@ hipError_t launch_shape(const AttnArgs &a, const Plan &p, int head_dim, int bloc
   return hipErrorNotSupported;
 }
 
-extern template hipError_t launch_shape<kBF16>(const AttnArgs &, const Plan &, int, int, hipStream_t);
-extern template hipError_t launch_shape<kFP16>(const AttnArgs &, const Plan &, int, int, hipStream_t);
-extern template hipError_t launch_shape<kFP32>(const AttnArgs &, const Plan &, int, int, hipStream_t);
+#define NF4_KV_SHAPES(DT, MASK)                                                              \
+  template hipError_t launch_shape<DT, MASK>(const ArgsOf<MASK> &, const Plan &, int, int, \
+                                             hipStream_t);
+extern NF4_KV_SHAPES(kBF16, false)
+extern NF4_KV_SHAPES(kFP16, false)
+extern NF4_KV_SHAPES(kFP32, false)
+extern NF4_KV_SHAPES(kBF16, true)
+extern NF4_KV_SHAPES(kFP16, true)
+extern NF4_KV_SHAPES(kFP32, true)
 
 }  // namespace kvattn
 }  // namespace nf4

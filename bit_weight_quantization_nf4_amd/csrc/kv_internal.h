@@ -5,6 +5,7 @@
 
 #include "nf4_internal.h"
 #include "nf4_kv.h"
+#include "nf4_kv_mask.h"
 
 namespace nf4 {
 
@@ -38,6 +39,7 @@ hipError_t launch_kv_read(const KvArgs &kv, const KvShape &sh, void *k, void *v,
 // What a call's split goes by.
 struct KvAttentionSizes {
   int32_t batch, max_rows, max_len, heads, kv_heads, head_dim, dtype, window;
+  int32_t sinks = 0;  // of the masked form
 };
 
 struct KvAttentionCall {
@@ -47,6 +49,11 @@ struct KvAttentionCall {
   float scale;
   int32_t causal;
   void *workspace;
+  // the masked form (nf4_kv_mask.h)
+  bool masked = false;
+  const uint32_t *tree = nullptr;
+  int64_t tree_stride = 0;
+  int32_t tree_words = 0;
 };
 
 // Workspace bytes of a call, and whether its launches stay within the device's grid

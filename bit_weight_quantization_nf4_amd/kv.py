@@ -1,4 +1,4 @@
-"""Python binding of the 4-bit key/value cache (``include/nf4_kv.h``): keys and
+"""Python binding of the 4-bit key/value cache (``include/nf4_kv.h``, ``nf4_kv_mask.h``): keys and
 values quantized as they are written into a paged cache, read back, and attended
 to in their 4 bits. Argument marshalling only, as in the package's other calls.
 
@@ -47,6 +47,13 @@ _SIGNATURES = [
      [_CACHE, _ROWS, _P, _I64, _I64, _I32, _I32, ctypes.c_float, _I32, _I32, _I32, _I32, _P, _I64,
       _I64, _P, _I64, _P]),
 ]
+# and of nf4_kv_mask.h
+_MASK_SIGNATURES = [
+    ("nf4_kv_attention_masked_workspace_bytes", _I64, [_I32] * 9),
+    ("nf4_kv_attention_masked", _I32,
+     [_CACHE, _ROWS, _P, _I64, _I64, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _I64, _I32, _I32,
+      _I32, _P, _I64, _I64, _P, _I64, _P]),
+]
 
 _fns = None
 
@@ -54,12 +61,16 @@ _fns = None
 def _lib():
     global _fns
     if _fns is None:
-        _fns = _lib_functions(_SIGNATURES)
+        _fns = _lib_functions(_SIGNATURES + _MASK_SIGNATURES)
     return _fns
 
 
 def kv_exported_names() -> list[str]:
     return [s[0] for s in _SIGNATURES]
+
+
+def kv_mask_exported_names() -> list[str]:
+    return [s[0] for s in _MASK_SIGNATURES]
 
 
 def _page_stride(shape, stride) -> int:
@@ -265,16 +276,21 @@ def _int32(n: int) -> int:
 
 def kv_attention_workspace_bytes(batch: int, max_rows: int, max_len: int, num_heads: int,
                                  num_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
-                                 window: int = 0) -> int:
-    """nf4_kv_attention_workspace_bytes on the current device."""
+                                 window: int = 0, sinks: int = 0) -> int:
+    """nf4_kv_attention_workspace_bytes on the current device (with ``sinks``
+    nf4_kv_attention_masked_workspace_bytes)."""
     sizes = map(_int32, (batch, max_rows, max_len, num_heads, num_kv_heads, head_dim))
+    if sinks:
+        return _lib().nf4_kv_attention_masked_workspace_bytes(*sizes, _DT[dtype], _int32(window),
+                                                              _int32(sinks))
     return _lib().nf4_kv_attention_workspace_bytes(*sizes, _DT[dtype], _int32(window))
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
                  row_offsets: torch.Tensor | None = None, max_rows: int = 0, max_len: int = 0,
                  scale: float | None = None, causal: bool = True, window: int = 0,
-                 out: torch.Tensor | None = None) -> torch.Tensor:
+                 out: torch.Tensor | None = None, sinks: int = 0,
+                 tree: torch.Tensor | None = None) -> torch.Tensor:
     """nf4_kv_attention (with a workspace this call allocates): attention of q
     [rows, heads, head_dim] to the cache, in q's dtype. ``max_rows`` is the most
     rows of a sequence where row_offsets is given (0: that many as there are
@@ -282,7 +298,12 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
     both only size the launch, but rows of a sequence past max_rows stay
     unwritten, and a batch of many sequences without max_rows takes several times
     as long. ``scale`` defaults to head_dim ** -0.5. Rows behind the last
-    offset are left as they are: unspecified without ``out``."""
+    offset are left as they are: unspecified without ``out``.
+
+    With ``sinks`` or ``tree`` nf4_kv_attention_masked (causal only): ``sinks`` first
+    positions stay visible behind a ``window``; ``tree``, int32 [rows, words] of 32 bits
+    each, says which of its sequence's rows in the call a row sees (bit j % 32 of word
+    j // 32 for the j-th; its own among them), in place of those before it."""
     _check_rows(q, cache, "kv_attention")
     total, heads, d = q.shape
     if out is None:
@@ -307,15 +328,42 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
     if max_len <= 0:
         max_len = rows.table_cols * cache.page_size
     max_rows, max_len, window = _int32(max_rows), _int32(max_len), _int32(window)
+    sinks = _int32(sinks)
+    masked = sinks != 0 or tree is not None
+    if masked and not causal:
+        raise ValueError("kv_attention: sinks and a tree are for causal attention")
+    tree_at, tree_stride, tree_words = None, 0, 0
+    if tree is not None:
+        if tree.dtype is not torch.int32 or tree.get_device() != cache.index:
+            raise TypeError("kv_attention expects an int32 tree on the cache's GPU")
+        if tree.dim() != 2 or tree.shape[0] != total:
+            raise ValueError("kv_attention expects a tree [rows, words]")
+        tree_words = tree.shape[1]
+        if (tree_words > 1 and tree.stride(1) != 1) or (total > 1 and tree.stride(0) < tree_words):
+            tree = tree.contiguous()
+        tree_stride = tree.stride(0) if total > 1 else tree_words
+        # (without words nothing is read, but the call is one with a tree)
+        tree_at = tree.data_ptr() or cache.desc.k_packed
     qr, qh = strides
     orow, ohead = out_strides
     kv_heads, dt = cache.num_kv_heads, _DT[q.dtype]
 
     def run(stream):
         lib = _lib()
-        need = lib.nf4_kv_attention_workspace_bytes(rows.batch, max_rows, max_len, heads, kv_heads,
-                                                    d, dt, window)
+        if masked:
+            need = lib.nf4_kv_attention_masked_workspace_bytes(
+                rows.batch, max_rows, max_len, heads, kv_heads, d, dt, window, sinks)
+        else:
+            need = lib.nf4_kv_attention_workspace_bytes(rows.batch, max_rows, max_len, heads,
+                                                        kv_heads, d, dt, window)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        if masked:
+            return lib.nf4_kv_attention_masked(
+                cache.desc, rows, q.data_ptr(), qr, qh, heads, dt,
+                d ** -0.5 if scale is None else scale, window, sinks, tree_at, tree_stride,
+                tree_words, max_rows, max_len, out.data_ptr(), orow, ohead,
+                None if ws is None else ws.data_ptr(), max(need, 0),
+                stream), "nf4_kv_attention_masked"
         return lib.nf4_kv_attention(
             cache.desc, rows, q.data_ptr(), qr, qh, heads, dt, d ** -0.5 if scale is None else scale,
             int(causal), window, max_rows, max_len, out.data_ptr(), orow, ohead,
@@ -326,4 +374,4 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
 
 
 __all__ = ["KVCache", "KVCacheDesc", "KVRowsDesc", "kv_write", "kv_read", "kv_attention",
-           "kv_attention_workspace_bytes", "kv_exported_names"]
+           "kv_attention_workspace_bytes", "kv_exported_names", "kv_mask_exported_names"]
