@@ -1,14 +1,22 @@
 // mx_gemm.hip -- products of many rows with a microscaled 4-bit weight.
 //
-// y[m][f] = sum_k x[m][k] w[f][k] on 16x16x128 matrix-core steps, the weight as the first
+// y[m][f] = sum_k x[m][k] w[f][k] on 32x32x64 matrix-core steps, the weight as the first
 // operand. A workgroup computes a tile of features x rows of x, its waves parts of it: FT x TT
-// tiles of 16 x 16. K goes by 256: both operands' codes (128 bytes a row) and scales are
-// brought straight to LDS, into one of two buffers while the other is multiplied.
+// tiles of 32 x 32 each. K goes by 256: both operands' codes, 128 bytes a row, and scales
+// are brought straight to LDS, into one of two stages, and multiplied in two steps of 128. A wave
+// reads a step's operands into registers while the step before is multiplied, so a stage is free
+// for new loads from its second step on, and these have that step and the next to come.
+// (Whole cache lines: with steps of 64 bytes a row each line came twice; 2048 x 14336 x 4096: 98
+// us.)
 //
-// Which rows of the operands make up a matrix-core tile is free: tile i of a wave takes rows FT m
-// + i (m < 16), so a lane finds the scales of its FT rows side by side in LDS, and holds FT
-// neighbouring features of a result. A row's eight 16-byte pieces lie at places xor'ed with a
-// number of the row that differs between the rows which are read together.
+// Which rows of the operands make up a matrix-core tile is free. Tile i of a wave takes rows FT p
+// + i, p < 32: a lane finds the scales of its FT rows side by side in LDS and holds runs of 4 FT
+// neighbouring features of a result.
+//
+// LDS: the sixteen 16-byte pieces of two neighbouring rows lie at places xor'ed with p, which
+// differs between the sixteen lanes that are read together.
+#include <type_traits>
+
 #include "mx_internal.h"
 
 namespace nf4 {
@@ -21,180 +29,413 @@ struct GemmArgs {
   void *y;
   int64_t ldy;
   int32_t f_tiles, m_tiles;
+  // ranges of K: 128-wide steps of each (even), and how far their results lie apart
+  int32_t split_steps;
+  int64_t split_stride;
 };
 
-constexpr int kPieces = 8;               // 16-byte pieces of a row in LDS: 256 elements
-constexpr int kRowBytes = 16 * kPieces;
+constexpr int kStages = 2;
+constexpr int kBufferFlags = 0x00020000;
+// s_waitcnt: all LDS reads, and all but n of the loads.
+constexpr int waitcnt(int n) { return 0x0070 | (n & 15) | (n >> 4) << 14; }
 
-typedef const __attribute__((address_space(1))) uint32_t *GlobalWords;
-typedef __attribute__((address_space(3))) uint32_t *LdsWords;
+typedef __attribute__((address_space(3))) void *LdsPtr;
 
-template <int BYTES>
-__device__ __forceinline__ void to_lds(const void *src, void *dst) {
-  static_assert(BYTES == 16 || BYTES == 4, "a lane's piece");
-  if constexpr (BYTES == 16)
-    __builtin_amdgcn_global_load_lds((GlobalWords)(uintptr_t)src, (LdsWords)dst, 16, 0, 0);
-  else
-    __builtin_amdgcn_global_load_lds((GlobalWords)(uintptr_t)src, (LdsWords)dst, 4, 0, 0);
+// A place in LDS that loads write to, as one that the compiler knows nothing of: it would have
+// every read of what may be the same array wait for them. The kernel's own waits and barriers
+// order the two.
+__device__ __forceinline__ LdsPtr lds_place(void *p) {
+  uint32_t at = (uint32_t)(uintptr_t)(LdsPtr)p;
+  asm("" : "+s"(at));
+  return (LdsPtr)(uintptr_t)at;
+}
+
+// A wave-uniform value that 64-bit arithmetic left in vector registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint8_t *uniform(const uint8_t *p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<uint8_t *>((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 |
+                                     (uint32_t)uniform((int)v));
+}
+
+// 32x32x64 step on E2M1 operands: acc += A(32x64) B(64x32). Lane (p = lane & 31, h = lane >> 5) gives
+// elements 32 h .. 32 h + 31 of row p of A and of column p of B, and these blocks' scales as byte S
+// of sa and sb; it holds rows 8 q + 4 h + r of column p at acc[4 q + r].
+template <int S>
+__device__ __forceinline__ f32x16 mfma_mx32(mx_u32x4 a, mx_u32x4 b, f32x16 acc, uint32_t sa,
+                                            uint32_t sb) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, acc, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// The order of a step's instructions: the loads first, LA behind each product, then the LDS reads,
+// one behind each product, then the other products.
+template <int PRODUCTS, int READS, int LOADS, int LA = 1>
+__device__ __forceinline__ void interleave() {
+  if constexpr (PRODUCTS > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (LOADS > 0) {
+      __builtin_amdgcn_sched_group_barrier(0x020, LOADS < LA ? LOADS : LA, 0);
+      interleave<PRODUCTS - 1, READS, (LOADS < LA ? 0 : LOADS - LA), LA>();
+    } else if constexpr (READS > 0) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      interleave<PRODUCTS - 1, READS - 1, 0, LA>();
+    } else {
+      interleave<PRODUCTS - 1, 0, 0, LA>();
+    }
+  }
 }
 
 // WF x WT waves, each with FT x TT tiles (features x rows of x).
-template <int OUT, int FT, int TT, int WF, int WT>
-__global__ __launch_bounds__(64 * WF * WT) void mx_gemm_kernel(GemmArgs a) {
+template <int OUT, int FT, int TT, int WF, int WT, int WAVES_PER_EU>
+__global__ __launch_bounds__(64 * WF * WT) __attribute__((amdgpu_waves_per_eu(WAVES_PER_EU, WAVES_PER_EU)))
+void mx_gemm_kernel(GemmArgs a) {
   constexpr int kWaves = WF * WT;
-  constexpr int BF = 16 * FT * WF, BT = 16 * TT * WT;
+  constexpr int BF = 32 * FT * WF, BT = 32 * TT * WT;
   constexpr int kRows = BF + BT;  // of both operands, the weight's first
-  __shared__ __attribute__((aligned(16))) uint8_t codes[2][kRows][kRowBytes];
-  __shared__ __attribute__((aligned(16))) uint32_t scales[2][2][kRows];  // [buffer][half][row]
+  constexpr int kLoads = kRows / 8 / kWaves, kLoadsF = BF / 8 / kWaves;
+  static_assert(BF % (8 * kWaves) == 0 && BT % (8 * kWaves) == 0, "a wave's loads of each operand");
+  constexpr int kScaleLoads = 2 * kRows / 64 / kWaves;  // 64 rows of a half each
+  static_assert(2 * kRows % (64 * kWaves) == 0 && BF % 64 == 0, "whole loads");
+  static_assert(FT > 1 && TT > 1 && (FT & (FT - 1)) == 0 && (TT & (TT - 1)) == 0, "two rows of one p");
+  __shared__ __attribute__((aligned(128))) uint8_t codes[kStages][128 * kRows];
+  __shared__ __attribute__((aligned(16))) uint32_t scales[kStages][2][kRows];
+  __shared__ __attribute__((aligned(16))) float bias[BF];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
+  const int pl = lane & 31, h = lane >> 5;
   const int wf = wave % WF, wt = wave / WF;
-  const int fb = (int)blockIdx.x % a.f_tiles, mb = (int)blockIdx.x / a.f_tiles;
+  const int tiles = a.f_tiles * a.m_tiles;
+  const int split = uniform((int)blockIdx.x / tiles), tile = (int)blockIdx.x - split * tiles;
+  const int mb = uniform(tile / a.f_tiles), fb = tile - mb * a.f_tiles;
   const int64_t f0 = (int64_t)fb * BF, m0 = (int64_t)mb * BT;
-  const int f_last = (int)(a.w.rows - f0 < BF ? a.w.rows - f0 : BF) - 1;
-  const int m_last = (int)(a.x.rows - m0 < BT ? a.x.rows - m0 : BT) - 1;
-  const int64_t half = a.w.padded / 2;
-  const int steps = a.w.padded / kMxStep;  // of 128
-  const int pairs = (steps + 1) / 2;
+  const int f_rows = uniform((int)(a.w.rows - f0 < BF ? a.w.rows - f0 : BF));
+  const int m_rows = uniform((int)(a.x.rows - m0 < BT ? a.x.rows - m0 : BT));
+  const uint32_t half = (uint32_t)a.w.padded / 2;
+  const int step0 = split * a.split_steps, left = a.w.padded / kMxStep - step0;
+  const int steps = left < a.split_steps ? left : a.split_steps;
 
-  // a row's number that its pieces' places are xor'ed with
-  auto turn_f = [](int row) { return row / FT & 7; };
-  auto turn_m = [](int row) { return row / TT & 7; };
-
-  // rows of both operands past their last repeat it; nothing of theirs is stored
-  constexpr int kLoads = kRows / 8 / kWaves;
-  static_assert(kRows % (8 * kWaves) == 0 && BF % 8 == 0, "whole loads");
-  const uint8_t *src[kLoads];
-  int piece[kLoads];
+  // a load brings 8 rows' codes, or 64 rows' scales; rows past the last read zeros
+  const __amdgpu_buffer_rsrc_t fc = __builtin_amdgcn_make_buffer_rsrc(
+      uniform(a.w.codes + f0 * half), (short)0, (int)((uint32_t)f_rows * half), kBufferFlags);
+  const __amdgpu_buffer_rsrc_t mc = __builtin_amdgcn_make_buffer_rsrc(
+      uniform(a.x.codes + m0 * half), (short)0, (int)((uint32_t)m_rows * half), kBufferFlags);
+  uint32_t code_at[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = 8 * (wave * kLoads + i) + (lane >> 3);
-    const bool of_w = r < BF;
-    int row = of_w ? r : r - BF;
-    piece[i] = (lane & 7) ^ (of_w ? turn_f(row) : turn_m(row));
-    const int last = of_w ? f_last : m_last;
-    row = row < last ? row : last;
-    src[i] = (of_w ? a.w.codes + (f0 + row) * half : a.x.codes + (m0 + row) * half);
+    const bool of_w = i < kLoadsF;
+    const int two = 8 * (wave + kWaves * (of_w ? i : i - kLoadsF)) + 2 * (lane >> 4);  // rows two, two + 1
+    const int piece = (lane & 15) ^ (two / (of_w ? FT : TT) & 15);
+    code_at[i] = (uint32_t)(two + (piece >> 3)) * half + 16 * (piece & 7) + 64 * (uint32_t)step0;
   }
-  // scales: 64 rows of one half a load
-  constexpr int kScaleLoads = 2 * kRows / 64;
-  static_assert(kRows % 64 == 0 && BF % 64 == 0, "whole loads");
-  auto load = [&](int buf, int p) {
-    const bool whole = 2 * p + 1 < steps;  // both halves are there
+  // the wave's scales: loads wave, wave + kWaves, ... of the halves' rows
+  const int64_t stride_f = 4 * a.w.rows, stride_m = 4 * a.x.rows;
+  const uint8_t *base_f = uniform(a.w.scales + step0 * stride_f + 4 * f0);
+  const uint8_t *base_m = uniform(a.x.scales + step0 * stride_m + 4 * m0);
+  // stage b, of the stages in order. (Past the last step: loads of zeros, so that each stage
+  // issues as many. Of a last one's second half, which is not there, the codes are the next row's
+  // first, or zeros: nothing multiplies them.)
+  auto fill = [&](int b) {
+    const int stage = b % kStages;
+    const bool there = 2 * b < steps;
+    const uint32_t at = there ? 128u * (uint32_t)b : 0u;
+    const uint32_t none = there ? 0u : 0x80000000u;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int c = whole ? piece[i] : piece[i] & 3;
-      to_lds<16>(src[i] + (int64_t)p * kRowBytes + 16 * c, codes[buf][8 * (wave * kLoads + i)]);
+      const LdsPtr dst = lds_place(&codes[stage][1024 * (wave + kWaves * i)]);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(i < kLoadsF ? fc : mc, dst, 16,
+                                               (int)(code_at[i] | none), (int)at, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < (kScaleLoads + kWaves - 1) / kWaves; ++i) {
-      const int s = wave + kWaves * i;
-      if (s < kScaleLoads) {
-        const int h = s / (kRows / 64), r0 = 64 * (s % (kRows / 64));
-        const bool of_w = r0 < BF;
-        int row = (of_w ? r0 : r0 - BF) + lane;
-        const int last = of_w ? f_last : m_last;
-        row = row < last ? row : last;
-        const int64_t t = whole ? 2 * p + h : 2 * p;
-        const uint8_t *from = of_w ? a.w.scales + 4 * (t * a.w.rows + f0 + row)
-                                   : a.x.scales + 4 * (t * a.x.rows + m0 + row);
-        to_lds<4>(from, &scales[buf][h][r0]);
-      }
+    for (int i = 0; i < kScaleLoads; ++i) {
+      const int l = wave + kWaves * i, s = l / (kRows / 64), r0 = 64 * (l % (kRows / 64));
+      const bool of_w = r0 < BF, here = 2 * b + s < steps;
+      const uint8_t *base = (of_w ? base_f : base_m) + (s ? (of_w ? stride_f : stride_m) : 0);
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          uniform(base), (short)0, here ? 4 * (of_w ? f_rows : m_rows) : 0, kBufferFlags);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, lds_place(&scales[stage][s][r0]), 4,
+                                               4 * ((of_w ? r0 : r0 - BF) + lane), 0, 0, 0);
     }
+    base_f += there ? 2 * stride_f : 0;
+    base_m += there ? 2 * stride_m : 0;
   };
 
-  f32x4 acc[FT][TT];
+  const int row_f = FT * (32 * wf + pl), row_m = TT * (32 * wt + pl);
+  struct Operands {
+    mx_u32x4 f[FT][2], m[TT][2];  // both halves of the step
+    uint32_t sf[FT], sm[TT];
+  };
+  auto place = [&](int row, int piece) {
+    return 128 * (row & ~1) + 16 * ((8 * (row & 1) + piece) ^ (pl & 15));
+  };
+  // step t's operands
+  auto read = [&](int t, Operands &o) {
+    const int stage = t / 2 % kStages, c = 4 * (t & 1);
+#pragma unroll
+    for (int i = 0; i < FT; ++i) o.sf[i] = scales[stage][t & 1][row_f + i];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) o.sm[j] = scales[stage][t & 1][BF + row_m + j];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int i = 0; i < FT; ++i)
+        o.f[i][s] = *reinterpret_cast<const mx_u32x4 *>(&codes[stage][place(row_f + i, c + 2 * s + h)]);
+#pragma unroll
+      for (int j = 0; j < TT; ++j)
+        o.m[j][s] = *reinterpret_cast<const mx_u32x4 *>(&codes[stage][128 * BF + place(row_m + j, c + 2 * s + h)]);
+    }
+  };
+  f32x16 acc[FT][TT];
+  auto multiply = [&](const Operands &o) {
+    // a lane's scales of the step's halves: bytes 0 and 2
+    uint32_t sf[FT], sm[TT];
+#pragma unroll
+    for (int i = 0; i < FT; ++i) sf[i] = o.sf[i] >> (8 * h);
+#pragma unroll
+    for (int j = 0; j < TT; ++j) sm[j] = o.sm[j] >> (8 * h);
+#pragma unroll
+    for (int i = 0; i < FT; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) acc[i][j] = mfma_mx32<0>(o.f[i][0], o.m[j][0], acc[i][j], sf[i], sm[j]);
+#pragma unroll
+    for (int i = 0; i < FT; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) acc[i][j] = mfma_mx32<2>(o.f[i][1], o.m[j][1], acc[i][j], sf[i], sm[j]);
+  };
+  constexpr int kMem = kLoads + kScaleLoads;
+  constexpr int kLds = 2 * (FT + TT) + (FT + 3) / 4 + (TT + 3) / 4, kProducts = 2 * FT * TT;
+  // Step t: the operands of step t + 1 on their way while it is multiplied; in a stage's second
+  // step, from which on nobody reads it, the loads of the stage after the next too. (The reads are
+  // done at each barrier.) Then the loads of the next stage have come, before its first operands are
+  // read. Bare barriers: a fence would wait for all loads.
+  auto first = [&](int t, const Operands &now, Operands &next) {
+    read(t + 1, next);
+    multiply(now);
+    interleave<kProducts, kLds, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(waitcnt(0));
+    __builtin_amdgcn_s_barrier();
+  };
+  auto second = [&](int t, const Operands &now, Operands &next) {
+    fill(t / 2 + 2);
+    read(t + 1, next);
+    multiply(now);
+    interleave<kProducts, kLds, kMem>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  fill(0);
+  fill(1);
+  for (int i = threadIdx.x; i < BF; i += 64 * kWaves) {
+    float v = 0.0f;
+    if (a.bias != nullptr && i < f_rows) {
+      if constexpr (OUT == kFP32) v = static_cast<const float *>(a.bias)[f0 + i];
+      else v = widen16<OUT>(static_cast<const uint16_t *>(a.bias)[f0 + i]);
+    }
+    bias[i] = v;
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt(0));
+  __syncthreads();
+  // the sums begin with the bias
 #pragma unroll
   for (int i = 0; i < FT; ++i)
 #pragma unroll
-    for (int j = 0; j < TT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  const int row_f = wf * 16 * FT + FT * n, row_m = wt * 16 * TT + TT * n;
-  const int at_f = turn_f(row_f), at_m = turn_m(row_m);  // the same for the lane's FT (TT) rows
-  load(0, 0);
-  for (int p = 0; p < pairs; ++p) {
-    const int buf = p & 1;
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-    __syncthreads();
-    if (p + 1 < pairs) load(buf ^ 1, p + 1);
+    for (int j = 0; j < TT; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (2 * p + h < steps) {
-        mx_u32x4 fa[FT], fm[TT];
-        uint32_t sa[FT], sm[TT];
-#pragma unroll
-        for (int i = 0; i < FT; ++i) {
-          fa[i] = *reinterpret_cast<const mx_u32x4 *>(
-              &codes[buf][row_f + i][16 * ((4 * h + g) ^ at_f)]);
-          sa[i] = scales[buf][h][row_f + i] >> (8 * g);
-        }
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          fm[j] = *reinterpret_cast<const mx_u32x4 *>(
-              &codes[buf][BF + row_m + j][16 * ((4 * h + g) ^ at_m)]);
-          sm[j] = scales[buf][h][BF + row_m + j] >> (8 * g);
-        }
-#pragma unroll
-        for (int i = 0; i < FT; ++i)
-#pragma unroll
-          for (int j = 0; j < TT; ++j) acc[i][j] = mfma_mx(fa[i], fm[j], acc[i][j], sa[i], sm[j]);
-      }
-    }
+      for (int e = 0; e < 16; ++e)
+        acc[i][j][e] = bias[FT * (32 * wf + 8 * (e / 4) + 4 * h + e % 4) + i];
+  Operands o0, o1;
+  read(0, o0);
+  int t = 0;
+  for (; t + 1 < steps; t += 2) {
+    first(t, o0, o1);
+    second(t + 1, o1, o0);
   }
+  if (t < steps) multiply(o0);
+  // Loads past the last step may still be on their way to LDS, and other waves at its operands.
+  __builtin_amdgcn_s_waitcnt(waitcnt(0));
+  __syncthreads();
 
-  // lane (n, g): rows TT n + j of x, features FT (4 g + r) + i
+  // Results leave through the wave's own part of LDS, 32 rows of x at a time, as whole lines. Of
+  // row TT p + j of x a lane has features FT (8 q + 4 h + r) + i: a run of 4 FT for each q.
+  using Out = std::conditional_t<OUT == kFP32, float, uint16_t>;
+  constexpr int kRun = 4 * FT, kWide = 32 * FT;     // features of a run, of the wave
+  constexpr int kPitch = kWide * sizeof(Out) + 16;  // (apart by a piece: no bank conflicts)
+  constexpr int kEach = 16 / sizeof(Out), kPerRow = kWide / kEach;  // a lane's piece
+  static_assert(32 * kPitch * kWaves <= sizeof(codes), "room");
+  Out *out = static_cast<Out *>(a.y) + split * a.split_stride;
+  uint8_t *mine = codes[0] + wave * (32 * kPitch);
+  const int f_first = 32 * FT * wf;  // of the tile
+  const bool even = (a.ldy * sizeof(Out)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
-    const int m = row_m + j;
-    if (m > m_last) continue;
+    __builtin_amdgcn_sched_barrier(0);  // (rows ahead of their turn would spill)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int f = wf * 16 * FT + FT * (4 * g + r);
-      const int64_t at = (m0 + m) * a.ldy + f0 + f;
+    for (int q = 0; q < 4; ++q) {
+      float v[kRun];
 #pragma unroll
-      for (int i = 0; i < FT; ++i) {
-        if (f + i > f_last) continue;
-        float v = acc[i][j][r];
-        if (a.bias != nullptr) {
-          if constexpr (OUT == kFP32) v += static_cast<const float *>(a.bias)[f0 + f + i];
-          else v += widen16<OUT>(static_cast<const uint16_t *>(a.bias)[f0 + f + i]);
+      for (int e = 0; e < kRun; ++e) v[e] = acc[e % FT][j][4 * q + e / FT];
+      uint4 *dst = reinterpret_cast<uint4 *>(mine + pl * kPitch + kRun * (2 * q + h) * sizeof(Out));
+#pragma unroll
+      for (int e = 0; e < kRun; e += kEach) {
+        if constexpr (OUT == kFP32)
+          dst[e / kEach] = make_uint4(__float_as_uint(v[e]), __float_as_uint(v[e + 1]),
+                                      __float_as_uint(v[e + 2]), __float_as_uint(v[e + 3]));
+        else
+          dst[e / kEach] = make_uint4(pack2<OUT>(v[e], v[e + 1]), pack2<OUT>(v[e + 2], v[e + 3]),
+                                      pack2<OUT>(v[e + 4], v[e + 5]), pack2<OUT>(v[e + 6], v[e + 7]));
+      }
+    }
+#pragma unroll 2
+    for (int k = 0; k < 32 * kPerRow / 64; ++k) {
+      const int at = 64 * k + lane, row = at / kPerRow, f = f_first + at % kPerRow * kEach;
+      const uint4 piece = *reinterpret_cast<const uint4 *>(mine + row * kPitch + at % kPerRow * 16);
+      const int m = TT * (32 * wt + row) + j;
+      if (m >= m_rows) continue;
+      Out *dst = out + (m0 + m) * a.ldy + f0 + f;
+      if (even && f + kEach <= f_rows) {
+        *reinterpret_cast<uint4 *>(dst) = piece;
+      } else {
+        const uint32_t w[4] = {piece.x, piece.y, piece.z, piece.w};
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          if (f + e >= f_rows) continue;
+          if constexpr (OUT == kFP32) dst[e] = __uint_as_float(w[e]);
+          else dst[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
         }
-        if constexpr (OUT == kFP32) static_cast<float *>(a.y)[at + i] = v;
-        else static_cast<uint16_t *>(a.y)[at + i] = (uint16_t)out_bits<OUT>(v);
       }
     }
   }
 }
 
-template <int OUT, int FT, int TT, int WF, int WT>
-hipError_t launch(GemmArgs a, hipStream_t stream) {
-  a.f_tiles = (int32_t)((a.w.rows + 16 * FT * WF - 1) / (16 * FT * WF));
-  a.m_tiles = (int32_t)((a.x.rows + 16 * TT * WT - 1) / (16 * TT * WT));
-  hipLaunchKernelGGL((mx_gemm_kernel<OUT, FT, TT, WF, WT>),
-                     dim3((unsigned)((int64_t)a.f_tiles * a.m_tiles)), dim3(64 * WF * WT), 0,
-                     stream, a);
+// Joins the ranges of K: y = sum over the ranges, in order, and the bias. Four features a thread.
+template <int OUT>
+__global__ __launch_bounds__(256) void mx_gemm_join_kernel(const float *part, int splits,
+                                                           int64_t split_stride, int64_t pitch,
+                                                           const void *bias, int64_t M, int64_t N,
+                                                           void *y, int64_t ldy) {
+  const int64_t quads = pitch / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= M * quads) return;
+  const int64_t m = i / quads, f = 4 * (i - m * quads);
+  const float *p = part + m * pitch + f;
+  f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll 4
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * split_stride);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (f + e >= N) continue;
+    float r = v[e];
+    if constexpr (OUT == kFP32) {
+      if (bias != nullptr) r += static_cast<const float *>(bias)[f + e];
+      static_cast<float *>(y)[m * ldy + f + e] = r;
+    } else {
+      if (bias != nullptr) r += widen16<OUT>(static_cast<const uint16_t *>(bias)[f + e]);
+      static_cast<uint16_t *>(y)[m * ldy + f + e] = (uint16_t)out_bits<OUT>(r);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+  bool large;       // tiles of 256 x 256, else of 128 x 128
+  int splits;       // ranges of K
+  int split_steps;  // 128-wide steps of each
+};
+
+int64_t tiles_of(int64_t M, int64_t N, bool large) {
+  const int side = large ? 256 : 128;
+  return ceil_div(M, side) * ceil_div(N, side);
+}
+
+int64_t pitch_of(int64_t N) { return ceil_div(N, 4) * 4; }  // of a range's results
+
+// Tiles and ranges by about the time that they take. In us, of 256-wide stages: a workgroup of
+// large tiles has a CU to itself and takes 1.9 a stage where all CUs work, and 6 to begin and end; of
+// small tiles 0.6 and 3, but 1.25 and 4 where two share a CU; a second launch 4 and its traffic.
+// (2048 x 14336 x 4096: large 75, small 80; 8192 cubed 280, 337; 4096 x 4096 x 4096: 40, 46; 1024 x
+// 11008 x 4096: 32, 39; 512 x 4096 x 4096: 25, 13; 1024 x 4096 x 14336: 58, 43. 128 x 4096 x 14336 in
+// 1, 2, 4, 6, 8 ranges: 38, 26, 19, 18, 19; x 4096: 12.1, 13.6, 14.1, 16.1, 18.8.)
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  const int64_t cus = device_cu_count(), steps = mx_padded(K) / kMxStep, stages = ceil_div(steps, 2);
+  const int64_t large = tiles_of(M, N, true), small = tiles_of(M, N, false);
+  Plan best{true, 1, (int)steps};
+  double least = (double)ceil_div(large, cus) * (1.9 * (double)stages + 6);
+  for (int64_t s = 1; s <= stages && (s == 1 || s * small <= 2 * cus); ++s) {
+    const int64_t each = ceil_div(stages, s);
+    if (ceil_div(stages, each) != s) continue;  // the same ranges as of fewer
+    double t = s * small <= cus ? 0.6 * (double)each + 3
+                                : ((double)(s * small) / (double)(2 * cus) + 0.25) * (1.25 * (double)each + 4);
+    if (s > 1) t += 4 + (double)(s * M) * (double)N * 8 / 4.5e6;
+    if (t >= least) continue;
+    least = t;
+    best = Plan{false, (int)s, (int)(s > 1 ? 2 * each : steps)};
+  }
+  return best;
+}
+
+template <int OUT, int FT, int TT, int WF, int WT, int WAVES_PER_EU>
+hipError_t launch(GemmArgs a, int splits, hipStream_t stream) {
+  a.f_tiles = (int32_t)ceil_div(a.w.rows, 32 * FT * WF);
+  a.m_tiles = (int32_t)ceil_div(a.x.rows, 32 * TT * WT);
+  hipLaunchKernelGGL((mx_gemm_kernel<OUT, FT, TT, WF, WT, WAVES_PER_EU>),
+                     dim3((unsigned)((int64_t)a.f_tiles * a.m_tiles * splits)), dim3(64 * WF * WT),
+                     0, stream, a);
+  return hipGetLastError();
+}
+
+template <int OUT>
+hipError_t launch_plan(const GemmArgs &a, const Plan &plan, hipStream_t stream) {
+  if (plan.large) return launch<OUT, 2, 4, 4, 2, 2>(a, plan.splits, stream);
+  return launch<OUT, 2, 2, 2, 2, 2>(a, plan.splits, stream);
+}
+
+template <int OUT>
+hipError_t launch_as(GemmArgs a, const Plan &plan, void *workspace, hipStream_t stream) {
+  if (plan.splits == 1) return launch_plan<OUT>(a, plan, stream);
+  GemmArgs b = a;
+  b.bias = nullptr;
+  b.y = workspace;
+  b.ldy = pitch_of(a.w.rows);
+  b.split_stride = a.x.rows * b.ldy;
+  const hipError_t e = launch_plan<kFP32>(b, plan, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((mx_gemm_join_kernel<OUT>),
+                     dim3((unsigned)ceil_div(a.x.rows * (b.ldy / 4), 256)), dim3(256), 0, stream,
+                     static_cast<const float *>(workspace), plan.splits, b.split_stride, b.ldy,
+                     a.bias, a.x.rows, a.w.rows, a.y, a.ldy);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t mx_gemm_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
-
-bool mx_gemm_fits(int64_t M, int64_t N) {
-  return ((M + 127) / 128) * ((N + 127) / 128) * 512 <= 0xffffffffll;
+int64_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  const Plan p = plan_of(M, N, K);
+  return p.splits == 1 ? 0 : 4 * p.splits * M * pitch_of(N);
 }
 
-hipError_t launch_mx_gemm(const MxMatrix &x, const MxProduct &p, void *, hipStream_t stream) {
+bool mx_gemm_fits(int64_t M, int64_t N) {
+  // (products with several ranges are far smaller)
+  return tiles_of(M, N, false) * 256 <= 0xffffffffll;
+}
+
+hipError_t launch_mx_gemm(const MxMatrix &x, const MxProduct &p, void *workspace,
+                          hipStream_t stream) {
+  const Plan plan = plan_of(x.rows, p.w.rows, p.w.cols);
   GemmArgs a{};
   a.w = p.w;
   a.x = x;
   a.bias = p.bias;
   a.y = p.y;
   a.ldy = p.ldy;
-  if (p.out_dtype == kFP32) return launch<kFP32, 4, 4, 2, 2>(a, stream);
-  if (p.out_dtype == kFP16) return launch<kFP16, 4, 4, 2, 2>(a, stream);
-  return launch<kBF16, 4, 4, 2, 2>(a, stream);
+  a.split_steps = plan.split_steps;
+  if (p.out_dtype == kFP32) return launch_as<kFP32>(a, plan, workspace, stream);
+  if (p.out_dtype == kFP16) return launch_as<kFP16>(a, plan, workspace, stream);
+  return launch_as<kBF16>(a, plan, workspace, stream);
 }
 
 }  // namespace nf4

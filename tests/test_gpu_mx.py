@@ -157,7 +157,11 @@ def check_product(y, x64, w64, bias, k, note=""):
 SHAPES = [(1, 1, 1), (1, 16, 128), (1, 11, 1003), (2, 33, 256), (1, 300, 4096), (3, 17, 4224),
           (16, 65, 384), (5, 1000, 11008), (17, 40, 640), (32, 31, 129), (33, 100, 1024),
           (64, 130, 2048), (65, 1, 128), (65, 129, 130), (128, 128, 512), (200, 333, 1003),
-          (257, 255, 384), (513, 640, 256), (300, 1, 4096), (1000, 520, 896)]
+          (257, 255, 384), (513, 640, 256), (300, 1, 4096), (1000, 520, 896),
+          # K in several ranges, the last one shorter, with an odd number of steps
+          (130, 200, 5000), (70, 256, 8192), (100, 33, 14336),
+          # tiles of 256 x 256, ragged at both ends
+          (3900, 4050, 300), (4096, 4096, 128)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
