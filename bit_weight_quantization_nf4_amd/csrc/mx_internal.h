@@ -38,7 +38,7 @@ struct MxProduct {
 };
 
 // Products of few rows (mx_gemv.hip). Up to mx_gemv_max_rows() rows of x; launch_mx_gemv_quantizing
-// takes x as it is, where mx_gemv_quantizes() says that its rows fit a workgroup.
+// takes x as it is, where mx_gemv_quantizes() says so.
 int mx_gemv_max_rows();
 bool mx_gemv_quantizes(int64_t M, int64_t K);
 hipError_t launch_mx_gemv(const MxMatrix &x, const MxProduct &p, hipStream_t stream);
@@ -74,23 +74,24 @@ struct MxEight {
   uint32_t w[DT == kFP32 ? 8 : 4];
 };
 
+// (of any alignment: the memory instructions take it, 16 bytes at once)
+typedef mx_u32x4 mx_any_u32x4 __attribute__((aligned(2)));
+
 template <int DT>
 __device__ __forceinline__ MxEight<DT> mx_load_eight(const void *row, int64_t col) {
   MxEight<DT> e;
-  const auto *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) +
-                                                  col * (DT == kFP32 ? 4 : 2));
+  const auto *p = reinterpret_cast<const mx_any_u32x4 *>(static_cast<const char *>(row) +
+                                                         col * (DT == kFP32 ? 4 : 2));
 #pragma unroll
   for (int i = 0; i < (DT == kFP32 ? 2 : 1); ++i) {
-    const uint4 v = p[i];
-    e.w[4 * i] = v.x;
-    e.w[4 * i + 1] = v.y;
-    e.w[4 * i + 2] = v.z;
-    e.w[4 * i + 3] = v.w;
+    const mx_u32x4 v = p[i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e.w[4 * i + j] = v[j];
   }
   return e;
 }
 
-// The same element by element: rows of any alignment, zeros from `cols` on.
+// The same element by element: zeros from `cols` on.
 template <int DT>
 __device__ __forceinline__ MxEight<DT> mx_load_ragged(const void *row, int64_t col, int64_t cols) {
   MxEight<DT> e;

@@ -1,23 +1,27 @@
 // mx_quantize.hip -- microscaled 4-bit quantisation of a matrix, and its reverse.
 //
-// A workgroup takes 32 rows of 512 columns, a wave 8 of the rows; a lane holds 8 neighbouring
+// A workgroup takes 32 rows of 512 columns, a wave 8 of the rows (4 and 1 where that leaves CUs
+// without work); a lane holds 8 neighbouring
 // elements (16 bytes of 16-bit ones), so a block of 32 is four lanes, and its largest
 // magnitude two lane exchanges. Codes leave as a dword a lane, scales through LDS as whole
 // 128-byte lines of 32 rows.
+#include <type_traits>
+
 #include "mx_internal.h"
 
 namespace nf4 {
 
 namespace {
 
-constexpr int kRows = 32, kCols = 512, kThreads = 256, kWaves = 4, kWaveRows = kRows / kWaves;
+constexpr int kCols = 512, kThreads = 256, kWaves = 4;
 
-template <int DT, bool ALIGNED>
+template <int DT, int kWaveRows>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *x, int64_t rows,
                                                                int32_t cols, int32_t padded,
                                                                int64_t ld, int32_t col_tiles,
                                                                uint8_t *codes, uint8_t *scales) {
-  __shared__ uint8_t s_lds[kCols / kMxStep][kRows][4];
+  constexpr int kRows = kWaves * kWaveRows;
+  __shared__ __attribute__((aligned(4))) uint8_t s_lds[kCols / kMxStep][kRows][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row0 = (int64_t)(blockIdx.x / (unsigned)col_tiles) * kRows;
   const int32_t col0 = (int32_t)(blockIdx.x % (unsigned)col_tiles) * kCols;
@@ -29,7 +33,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *x, in
     const int r = wave + kWaves * i;
     if (r >= here) continue;
     const char *row = static_cast<const char *>(x) + (row0 + r) * ld * (DT == kFP32 ? 4 : 2);
-    if (ALIGNED && col + 8 <= cols) e[i] = mx_load_eight<DT>(row, col);
+    if (col + 8 <= cols) e[i] = mx_load_eight<DT>(row, col);
     else e[i] = mx_load_ragged<DT>(row, col, cols);
   }
 #pragma unroll
@@ -49,9 +53,10 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *x, in
         *reinterpret_cast<const uint32_t *>(s_lds[t][r]);
 }
 
-template <int DT, bool ALIGNED>
+template <int DT, int kWaveRows>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxMatrix m, int32_t col_tiles,
                                                                  void *out, int64_t ld) {
+  constexpr int kRows = kWaves * kWaveRows;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row0 = (int64_t)(blockIdx.x / (unsigned)col_tiles) * kRows;
   const int32_t col = (int32_t)(blockIdx.x % (unsigned)col_tiles) * kCols + 8 * lane;
@@ -85,9 +90,12 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxMatrix m, int
     const int64_t at = (row0 + r) * ld + col;
     if constexpr (DT == kFP32) {
       float *p = static_cast<float *>(out) + at;
-      if (ALIGNED && col + 8 <= m.cols) {
-        reinterpret_cast<f32x4 *>(p)[0] = f32x4{f[0].x, f[0].y, f[1].x, f[1].y};
-        reinterpret_cast<f32x4 *>(p)[1] = f32x4{f[2].x, f[2].y, f[3].x, f[3].y};
+      if (col + 8 <= m.cols) {
+        auto *q = reinterpret_cast<mx_any_u32x4 *>(p);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          q[j] = mx_u32x4{__float_as_uint(f[2 * j].x), __float_as_uint(f[2 * j].y),
+                          __float_as_uint(f[2 * j + 1].x), __float_as_uint(f[2 * j + 1].y)};
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -98,8 +106,8 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxMatrix m, int
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = pack2<DT>(f[j].x, f[j].y);
-      if (ALIGNED && col + 8 <= m.cols) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (col + 8 <= m.cols) {
+        *reinterpret_cast<mx_any_u32x4 *>(p) = mx_u32x4{w[0], w[1], w[2], w[3]};
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -109,63 +117,60 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxMatrix m, int
   }
 }
 
-bool rows_aligned(const void *p, int64_t rows, int64_t ld, int dtype) {
-  const int64_t bytes = ld * (dtype == kFP32 ? 4 : 2);
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || bytes % 16 == 0);
+int64_t col_tiles_of(int64_t cols) { return (mx_padded(cols) + kCols - 1) / kCols; }
+int64_t tiles_of(int64_t rows, int64_t cols, int tile_rows) {
+  return (rows + tile_rows - 1) / tile_rows * col_tiles_of(cols);
 }
 
-int64_t tiles_of(int64_t rows, int64_t cols) {
-  return (rows + kRows - 1) / kRows * ((mx_padded(cols) + kCols - 1) / kCols);
-}
-
-template <int DT>
-void quantize_as(bool aligned, unsigned grid, const void *x, int64_t rows, int32_t cols, int64_t ld,
-                 int32_t col_tiles, uint8_t *codes, uint8_t *scales, hipStream_t stream) {
-  const int32_t padded = (int32_t)mx_padded(cols);
-  if (aligned)
-    hipLaunchKernelGGL((mx_quantize_kernel<DT, true>), dim3(grid), dim3(kThreads), 0, stream, x,
-                       rows, cols, padded, ld, col_tiles, codes, scales);
-  else
-    hipLaunchKernelGGL((mx_quantize_kernel<DT, false>), dim3(grid), dim3(kThreads), 0, stream, x,
-                       rows, cols, padded, ld, col_tiles, codes, scales);
+// Rows of a wave: 8, or 1 where two workgroups a CU of 32 rows are not reached. (16 x 11008: 4.4 us
+// and 2.2.)
+template <typename F>
+void by_rows(int64_t rows, int64_t cols, F &&run) {
+  if (tiles_of(rows, cols, 8 * kWaves) >= 2 * device_cu_count()) run(std::integral_constant<int, 8>{});
+  else run(std::integral_constant<int, 1>{});
 }
 
 template <int DT>
-void dequantize_as(bool aligned, unsigned grid, const MxMatrix &m, int32_t col_tiles, void *out,
-                   int64_t ld, hipStream_t stream) {
-  if (aligned)
-    hipLaunchKernelGGL((mx_dequantize_kernel<DT, true>), dim3(grid), dim3(kThreads), 0, stream, m,
-                       col_tiles, out, ld);
-  else
-    hipLaunchKernelGGL((mx_dequantize_kernel<DT, false>), dim3(grid), dim3(kThreads), 0, stream, m,
-                       col_tiles, out, ld);
+void quantize_as(const void *x, int64_t rows, int32_t cols, int64_t ld, uint8_t *codes,
+                 uint8_t *scales, hipStream_t stream) {
+  by_rows(rows, cols, [&](auto wave_rows) {
+    constexpr int R = decltype(wave_rows)::value;
+    hipLaunchKernelGGL((mx_quantize_kernel<DT, R>), dim3((unsigned)tiles_of(rows, cols, R * kWaves)),
+                       dim3(kThreads), 0, stream, x, rows, cols, (int32_t)mx_padded(cols), ld,
+                       (int32_t)col_tiles_of(cols), codes, scales);
+  });
+}
+
+template <int DT>
+void dequantize_as(const MxMatrix &m, void *out, int64_t ld, hipStream_t stream) {
+  by_rows(m.rows, m.cols, [&](auto wave_rows) {
+    constexpr int R = decltype(wave_rows)::value;
+    hipLaunchKernelGGL((mx_dequantize_kernel<DT, R>),
+                       dim3((unsigned)tiles_of(m.rows, m.cols, R * kWaves)), dim3(kThreads), 0,
+                       stream, m, (int32_t)col_tiles_of(m.cols), out, ld);
+  });
 }
 
 }  // namespace
 
+// (where waves have one row, there are fewer workgroups than twice eight times the CUs)
 bool mx_elementwise_fits(int64_t rows, int64_t cols) {
-  return tiles_of(rows, cols) * kThreads <= 0xffffffffll;
+  return tiles_of(rows, cols, 8 * kWaves) * kThreads <= 0xffffffffll;
 }
 
 hipError_t launch_mx_quantize(const void *x, int dtype, int64_t rows, int32_t cols, int64_t ld,
                               uint8_t *codes, uint8_t *scales, hipStream_t stream) {
-  const unsigned grid = (unsigned)tiles_of(rows, cols);
-  const int32_t col_tiles = (int32_t)((mx_padded(cols) + kCols - 1) / kCols);
-  const bool al = rows_aligned(x, rows, ld, dtype);
-  if (dtype == kFP32) quantize_as<kFP32>(al, grid, x, rows, cols, ld, col_tiles, codes, scales, stream);
-  else if (dtype == kFP16) quantize_as<kFP16>(al, grid, x, rows, cols, ld, col_tiles, codes, scales, stream);
-  else quantize_as<kBF16>(al, grid, x, rows, cols, ld, col_tiles, codes, scales, stream);
+  if (dtype == kFP32) quantize_as<kFP32>(x, rows, cols, ld, codes, scales, stream);
+  else if (dtype == kFP16) quantize_as<kFP16>(x, rows, cols, ld, codes, scales, stream);
+  else quantize_as<kBF16>(x, rows, cols, ld, codes, scales, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const MxMatrix &m, int dtype, void *out, int64_t ld,
                                 hipStream_t stream) {
-  const unsigned grid = (unsigned)tiles_of(m.rows, m.cols);
-  const int32_t col_tiles = (int32_t)((m.padded + kCols - 1) / kCols);
-  const bool al = rows_aligned(out, m.rows, ld, dtype);
-  if (dtype == kFP32) dequantize_as<kFP32>(al, grid, m, col_tiles, out, ld, stream);
-  else if (dtype == kFP16) dequantize_as<kFP16>(al, grid, m, col_tiles, out, ld, stream);
-  else dequantize_as<kBF16>(al, grid, m, col_tiles, out, ld, stream);
+  if (dtype == kFP32) dequantize_as<kFP32>(m, out, ld, stream);
+  else if (dtype == kFP16) dequantize_as<kFP16>(m, out, ld, stream);
+  else dequantize_as<kBF16>(m, out, ld, stream);
   return hipGetLastError();
 }
 

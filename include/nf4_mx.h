@@ -48,7 +48,7 @@ typedef struct nf4_mx_matrix {
 int64_t nf4_mx_padded(int64_t cols);
 
 /* Quantizes x [rows][cols] of `dtype`, rows row_stride elements apart (at least cols;
- * any alignment of the type's own; 16-byte aligned rows are read fastest). */
+ * any alignment of the type's own). */
 nf4_status nf4_mx_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols,
                            int64_t row_stride, uint8_t *codes, uint8_t *scales, void *stream);
 
