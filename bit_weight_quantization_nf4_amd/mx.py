@@ -69,9 +69,21 @@ class MXTensor:
         index = codes.get_device()
         if index < 0 or scales.get_device() != index:
             raise TypeError("MXTensor expects two tensors on one GPU")
+        self._set(codes, scales, rows, cols, index)
+
+    def _set(self, codes, scales, rows, cols, index):
         self.codes, self.scales, self.shape = codes, scales, (rows, cols)
         self.index = index  # of the GPU
         self.desc = MXMatrixDesc(codes.data_ptr(), scales.data_ptr(), rows, cols)
+
+    @classmethod
+    def _like(cls, x: torch.Tensor, rows: int, cols: int, index: int) -> "MXTensor":
+        """An uninitialised matrix beside x, on the GPU ``index``."""
+        padded = -(-cols // 128) * 128
+        t = cls.__new__(cls)
+        t._set(x.new_empty((rows, padded // 2), dtype=torch.uint8),
+               x.new_empty((padded // 128, rows, 4), dtype=torch.uint8), rows, cols, index)
+        return t
 
     @property
     def device(self) -> torch.device:
@@ -89,62 +101,72 @@ class MXTensor:
         return self.codes.numel() + self.scales.numel()
 
 
-def _call(index: int, run) -> None:
-    """run(stream) -> (status, name) with the GPU ``index`` current, on its current stream."""
-    if index == torch.cuda.current_device():
-        status, name = run(torch._C._cuda_getCurrentRawStream(index))
+# a device's current stream and the current device, without the objects around them
+_stream_of = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
+
+
+def _call(index: int, name: str, *args) -> None:
+    """The entry point `name` with the GPU ``index`` current, on its current stream."""
+    fn = getattr(_lib(), name)
+    if index == _current():
+        status = fn(*args, _stream_of(index))
     else:
         with torch.cuda.device(index):
-            status, name = run(torch._C._cuda_getCurrentRawStream(index))
+            status = fn(*args, _stream_of(index))
     if status:
         _check(status, name)
 
 
 def _input(x: torch.Tensor, what: str):
-    """(tensor, row stride) of x as [rows, cols] with unit element stride."""
+    """(tensor, rows, cols, row stride) of x as [rows, cols] with unit element stride."""
     if x.dtype not in _DT or not x.is_cuda:
         raise TypeError(f"{what} expects bf16 / fp16 / fp32 values on the GPU")
+    if x.dim() == 2:
+        rows, cols = x.shape
+        ld, one = x.stride()
+        if (one == 1 or cols <= 1) and (ld >= cols or rows <= 1):
+            return x, rows, cols, ld if rows > 1 else cols
     if x.dim() == 0:
         raise ValueError(f"{what} expects rows of values")
     cols = x.shape[-1]
-    if x.dim() != 2 or (cols > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < cols):
-        x = x.reshape(x.numel() // cols if cols else 0, cols).contiguous()
-    return x, (x.stride(0) if x.shape[0] > 1 else cols)
+    rows = x.numel() // cols if cols else 0
+    return x.reshape(rows, cols).contiguous(), rows, cols, cols
 
 
-def _output(out, shape, dtype, index: int, what: str):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index)), shape[1]
-    if out.dtype not in _DT or out.get_device() != index or out.shape != shape or \
-            (shape[1] > 1 and out.stride(1) != 1) or (shape[0] > 1 and out.stride(0) < shape[1]):
-        raise ValueError(f"{what}: out must be a [{shape[0]}, {shape[1]}] view with unit column "
-                         "stride on the same GPU")
-    return out, (out.stride(0) if shape[0] > 1 else shape[1])
+def _output(out, rows: int, cols: int, index: int, what: str) -> int:
+    """The row stride of an output that the caller gives."""
+    if out.dtype not in _DT or out.get_device() != index or out.shape != (rows, cols) or \
+            (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
+        raise ValueError(f"{what}: out must be a [{rows}, {cols}] view with unit column stride "
+                         "on the same GPU")
+    return out.stride(0) if rows > 1 else cols
 
 
 def mx_quantize(x: torch.Tensor, out: MXTensor | None = None) -> MXTensor:
     """nf4_mx_quantize: x [..., cols] (bf16 / fp16 / fp32, rows of any stride) as a
     microscaled matrix of its rows, into ``out`` where given."""
-    x, ld = _input(x, "mx_quantize")
-    rows, cols = x.shape
+    x, rows, cols, ld = _input(x, "mx_quantize")
     index = x.get_device()
     if out is None:
-        out = MXTensor.empty(rows, cols, x.device)
+        out = MXTensor._like(x, rows, cols, index)
     elif out.shape != (rows, cols) or out.index != index:
         raise ValueError("mx_quantize: out must be of x's shape, on its GPU")
-    _call(index, lambda stream: (_lib().nf4_mx_quantize(
-        x.data_ptr(), _DT[x.dtype], rows, cols, ld, out.desc.codes, out.desc.scales, stream),
-        "nf4_mx_quantize"))
+    _call(index, "nf4_mx_quantize", x.data_ptr(), _DT[x.dtype], rows, cols, ld, out.desc.codes,
+          out.desc.scales)
     return out
 
 
 def mx_dequantize(m: MXTensor, dtype=torch.bfloat16, out: torch.Tensor | None = None):
     """nf4_mx_dequantize: the values [rows, cols] in ``dtype`` (or into ``out``, in its dtype)."""
-    if out is None and dtype not in _DT:
-        raise TypeError("mx_dequantize gives bf16, fp16 or fp32")
-    out, ld = _output(out, m.shape, dtype, m.index, "mx_dequantize")
-    _call(m.index, lambda stream: (_lib().nf4_mx_dequantize(
-        m.desc, _DT[out.dtype], out.data_ptr(), ld, stream), "nf4_mx_dequantize"))
+    rows, ld = m.shape
+    if out is None:
+        if dtype not in _DT:
+            raise TypeError("mx_dequantize gives bf16, fp16 or fp32")
+        out = m.codes.new_empty(m.shape, dtype=dtype)
+    else:
+        ld = _output(out, rows, ld, m.index, "mx_dequantize")
+    _call(m.index, "nf4_mx_dequantize", m.desc, _DT[out.dtype], out.data_ptr(), ld)
     return out
 
 
@@ -163,39 +185,45 @@ def mx_linear(x, w: MXTensor, bias: torch.Tensor | None = None, out_dtype=None,
     here. out_dtype defaults to x's, for an MXTensor to bf16; the bias is of that type, and is
     added before the rounding to it."""
     N, K = w.shape
+    index = w.index
     quantized = isinstance(x, MXTensor)
     if quantized:
-        ldx, index = 0, x.index
-        dtype = out_dtype or torch.bfloat16
+        M, cols = x.shape
+        dtype = torch.bfloat16
     else:
-        x, ldx = _input(x, "mx_linear")
-        index, dtype = x.get_device(), out_dtype or x.dtype
+        x, M, cols, ldx = _input(x, "mx_linear")
+        dtype = x.dtype
     if out is not None:
         dtype = out.dtype
+    elif out_dtype is not None:
+        dtype = out_dtype
     if dtype not in _DT:
         raise TypeError("mx_linear gives bf16, fp16 or fp32")
-    M = x.shape[0]
-    if x.shape[1] != K or index != w.index:
+    if cols != K or (x.index if quantized else x.get_device()) != index:
         raise ValueError("mx_linear expects x [..., K] and w (N, K) on one GPU")
+    bp = None
     if bias is not None:
         if bias.dtype != dtype or bias.get_device() != index or bias.numel() != N:
             raise ValueError("mx_linear expects a bias of N elements of the output's dtype on the "
                              "same GPU")
         bias = bias.reshape(-1).contiguous()
-    out, ldy = _output(out, (M, N), dtype, index, "mx_linear")
-    bp = None if bias is None else bias.data_ptr()
-
-    def run(stream):
-        lib = _lib()
+        bp = bias.data_ptr()
+    ldy = N
+    if out is None:
+        out = w.codes.new_empty((M, N), dtype=dtype)
+    else:
+        ldy = _output(out, M, N, index, "mx_linear")
+    if index == _current():
         need = mx_workspace_bytes(M, N, K, quantized)
-        ws, nbytes, _keep = _workspace(need, out.device)
-        if quantized:
-            return lib.nf4_mx_matmul(x.desc, w.desc, bp, _DT[dtype], out.data_ptr(), ldy, ws,
-                                     nbytes, stream), "nf4_mx_matmul"
-        return lib.nf4_mx_linear(x.data_ptr(), _DT[x.dtype], ldx, M, w.desc, bp, _DT[dtype],
-                                 out.data_ptr(), ldy, ws, nbytes, stream), "nf4_mx_linear"
-
-    _call(index, run)
+    else:
+        with torch.cuda.device(index):
+            need = mx_workspace_bytes(M, N, K, quantized)
+    ws, nbytes, _keep = _workspace(need, out.device) if need > 0 else (None, 0, None)
+    if quantized:
+        _call(index, "nf4_mx_matmul", x.desc, w.desc, bp, _DT[dtype], out.data_ptr(), ldy, ws, nbytes)
+    else:
+        _call(index, "nf4_mx_linear", x.data_ptr(), _DT[x.dtype], ldx, M, w.desc, bp, _DT[dtype],
+              out.data_ptr(), ldy, ws, nbytes)
     return out
 
 
