@@ -147,7 +147,7 @@ nf4_status attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, const K
   const KvAttentionSizes z{
       kv.batch, kv.offsets == nullptr ? kv.uniform : (max_rows > 0 ? max_rows : kv.total_rows),
       max_len > 0 ? max_len : kv.capacity, num_heads, kv.kv_heads, sh.head_dim, dtype, window,
-      sinks};
+      sinks, c.masked};
   if (!kv_attention_fits(z)) return NF4_ERR_UNSUPPORTED;
   st = nf4_device_check();
   if (st != NF4_OK) return st;
@@ -223,8 +223,15 @@ int64_t nf4_kv_attention_masked_workspace_bytes(int32_t batch, int32_t max_rows,
                                                 int32_t head_dim, int32_t dtype, int32_t window,
                                                 int32_t sinks) {
   if (sinks < 0) return -1;
-  return attention_bytes(
-      {batch, max_rows, max_len, num_heads, num_kv_heads, head_dim, dtype, window, sinks});
+  KvAttentionSizes z{batch, max_rows, max_len, num_heads, num_kv_heads, head_dim, dtype, window, sinks,
+                     true};
+  const int64_t bytes = attention_bytes(z);
+  if (bytes < 0 || (window > 0 && sinks > 0)) return bytes;
+  // (without a tree these are nf4_kv_attention's)
+  z.masked = false;
+  z.sinks = 0;
+  const int64_t plain = attention_bytes(z);
+  return bytes > plain ? bytes : plain;
 }
 
 nf4_status nf4_kv_attention(const nf4_kv_cache *cache, const nf4_kv_rows *rows, const void *q,
@@ -269,7 +276,9 @@ nf4_status nf4_kv_attention_masked(const nf4_kv_cache *cache, const nf4_kv_rows 
   c.scale = scale;
   c.causal = 1;
   c.workspace = workspace;
-  c.masked = true;
+  // first positions are in sight anyway where there is no window
+  if (window == 0) sinks = 0;
+  c.masked = tree != nullptr || sinks > 0;
   c.tree = tree;
   c.tree_stride = tree_stride;
   c.tree_words = tree_words;

@@ -30,8 +30,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv_attention_join_kernel(Args
   const int wb = args.wg_blocks == 1 ? 0 : pair / args.wg_rows, row = pair - wb * args.wg_rows;
   const Block blk = block_of<MASK>(args, sequence_of(args, seq), wb * args.wg_rows, args.wg_rows);
   if (pair >= blk.pairs) return;
-  const int range = range_of(blk, args.splits, align);
-  const int pieces = range > 0 ? (span_of(blk) - 1) / range + 1 : 0;  // (no sum past 2^31)
+  const int range = range_of<MASK>(args, blk, align), span = span_of(blk);
+  const int pieces = MASK && span <= 0 ? 0 : range > 0 ? (span - 1) / range + 1 : 0;  // (no sum past 2^31)
+  if (MASK && pieces == 1) return;  // the row's workgroup has written it
   const int64_t base = item_of(args, seq, h, wb) * args.splits * args.part_rows + row;
   auto part_row = [&](int i) { return base + (int64_t)i * args.part_rows; };
 
@@ -161,11 +162,19 @@ Plan plan_of(const KvAttentionSizes &z) {
       best = cost;
       s = c;
     }
+    // The masked form has its ranges of one length, and half as many again: of uneven sequences
+    // no workgroup is then left with a long one. (16 of 64 to 4 rows at 6000 to 375 positions, 32
+    // heads of 8: 156 us in three ranges, 216 in two; all of 64 at 6000: 242, 229.)
+    if (z.masked && !p.merge && items > 0) {
+      const int64_t more = ceil_div(3 * slots, 2 * items);
+      if (s > 1 && more > s) s = more;
+    }
     const int64_t least = p.merge ? kMinRange * 128 / weight : kMinRangeApart;
     const int64_t most = ceil_div(span, least > 0 ? least : 1);
     if (s > most) s = most;
   }
   if (s < 1) s = 1;
+  p.least_range = s > 1 ? (int)ceil_div(span, s) : 0;
   p.splits = (int)s;
   p.part_rows = (int)(pairs < p.wg_rows ? pairs : p.wg_rows);
   p.stats = s > 1 ? items * s * p.part_rows : 0;
@@ -234,7 +243,8 @@ bool kv_attention_fits(const KvAttentionSizes &z) {
     return false;
   if (z.heads / z.kv_heads > 65535) return false;  // a head's number is exact in row_at
   const Plan p = plan_of(z);
-  return (int64_t)p.wg_blocks * p.splits * (64 * kMergeWaves) <= 0xffffffffll;
+  const int64_t heads = z.masked ? z.kv_heads : 1;  // the masked form has them in one dimension
+  return p.wg_blocks * heads * p.splits * (64 * kMergeWaves) <= 0xffffffffll;
 }
 
 hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAttentionSizes &z,
@@ -272,6 +282,7 @@ hipError_t launch_kv_attention(const KvArgs &kv, const KvShape &sh, const KvAtte
   a.tree = c.tree;
   a.tree_stride = c.tree_stride;
   a.tree_words = c.tree_words;
+  a.least_range = p.least_range;
   return launch_type<true>(a, p, sh, stream);
 }
 

@@ -104,6 +104,7 @@ struct MaskedArgs : AttnArgs {
   int32_t tree_words;   // 32-bit words of a row's mask
   const uint32_t *tree; // null: rows see what is before them
   int64_t tree_stride;  // words between rows
+  int32_t least_range;  // positions of a range, but for a block's last
 };
 
 // The kernels read their arguments through this type, from the argument segment
@@ -150,10 +151,13 @@ struct Block {
 // Positions that a block goes through.
 __device__ __forceinline__ int span_of(const Block &b) { return b.sink_hi + (b.hi - b.lo); }
 
-// Positions of a range: equal multiples of `align`.
-__device__ __forceinline__ int range_of(const Block &b, int splits, int align) {
+// Positions of a range: equal multiples of `align`. In the masked form no fewer than the
+// longest sequence's, so that uneven sequences are in pieces of equal length.
+template <bool MASK = false>
+__device__ __forceinline__ int range_of(KernelArgsOf<MASK> &a, const Block &b, int align) {
   const int total = span_of(b);
-  const int range = splits == 1 ? total : (total + splits - 1) / splits;
+  int range = a.splits == 1 ? total : (total + a.splits - 1) / a.splits;
+  if constexpr (MASK) range = range > a.least_range ? range : a.least_range;
   return (range + align - 1) / align * align;
 }
 
@@ -469,17 +473,20 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   const uint32_t lane_off = 4u * (lane & 31);
   KernelArgsOf<MASK> &args = *kernel_args<MASK>();
   const auto &kv = args.kv;
-  const int h = (int)blockIdx.y, seq = (int)blockIdx.z;
-  int wb = (int)blockIdx.x, split = 0;
+  // (masked form: heads first, which are alike in work, so that these and not uneven blocks and
+  // ranges take turns on the XCDs)
+  const int item_x = MASK ? (int)blockIdx.x / kv.kv_heads : (int)blockIdx.x;
+  const int h = MASK ? (int)blockIdx.x - item_x * kv.kv_heads : (int)blockIdx.y, seq = (int)blockIdx.z;
+  int wb = item_x, split = 0;
   if (args.splits > 1) {
-    wb = (int)blockIdx.x / args.splits;
-    split = (int)blockIdx.x - wb * args.splits;
+    wb = item_x / args.splits;
+    split = item_x - wb * args.splits;
   }
   // blocks of later rows see more positions: they come first
   wb = args.wg_blocks - 1 - wb;
   const Sequence of = sequence_of(args, seq);
   const Block item = block_of<MASK>(args, of, wb * args.wg_rows, args.wg_rows);
-  const int range = range_of(item, args.splits, kStep * TW);
+  const int range = range_of<MASK>(args, item, kStep * TW);
   int begin, end;
   // masked form: the range's first steps, before `begin`'s, that are of the first positions
   int sink_begin = 0, sink_steps = 0;
@@ -501,7 +508,8 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     // behind; with one range the rows that see nothing are still written
     if (item.row0 >= item.pairs || (begin >= item.hi && args.splits > 1)) return;
   }
-  const bool whole_item = args.splits == 1;
+  // (masked form: a block of one range leaves nothing to join)
+  const bool whole_item = args.splits == 1 || (MASK && range >= span_of(item));
   const int64_t part_row0 = (item_of(args, seq, h, wb) * args.splits + split) * args.part_rows;
   // a wave's own rows may see less, and there may be none
   const Block blk = MERGE ? item : block_of<MASK>(args, of, item.row0 + wave * A::kRows, A::kRows);
@@ -1339,6 +1347,7 @@ struct Plan {
   int tiles;              // 16-row tiles of a wave's block of rows
   int wg_rows, wg_blocks;
   int splits, align;      // ranges of positions, their granularity
+  int least_range;        // positions of one in the longest sequence
   int part_rows;
   int64_t part_floats, stats;  // totals
 };
@@ -1348,8 +1357,8 @@ constexpr int max_tiles(int head_dim) { return head_dim <= 128 ? 2 : 1; }
 
 template <int D, int BS, int DT, int NR, bool MERGE, bool MASK>
 hipError_t launch_one(const ArgsOf<MASK> &a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.wg_blocks * a.splits), (unsigned)a.kv.kv_heads,
-                  (unsigned)a.kv.batch);
+  dim3 grid((unsigned)(a.wg_blocks * a.splits), (unsigned)a.kv.kv_heads, (unsigned)a.kv.batch);
+  if (MASK) grid = dim3(grid.x * grid.y, 1, grid.z);
   hipLaunchKernelGGL((kv_attention_kernel<D, BS, DT, NR, MERGE, MASK>), grid,
                      dim3(Attn<D, BS, DT, NR, MERGE>::kThreads), 0, stream, a);
   return hipGetLastError();

@@ -40,6 +40,7 @@ hipError_t launch_kv_read(const KvArgs &kv, const KvShape &sh, void *k, void *v,
 struct KvAttentionSizes {
   int32_t batch, max_rows, max_len, heads, kv_heads, head_dim, dtype, window;
   int32_t sinks = 0;  // of the masked form
+  bool masked = false;
 };
 
 struct KvAttentionCall {
