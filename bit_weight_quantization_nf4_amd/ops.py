@@ -1,4 +1,4 @@
-"""torch.library operators over the C ABI, and a ``Linear4bit``-style module.
+"""torch.library operators over the C ABI, a ``Linear4bit``-style module, and ``LinearMX``.
 
 [gitcode page on the bitsandbytes 0.46.0 release, section on the custom-op
  rework: the quantized operations are functional operators registered with
@@ -27,6 +27,12 @@ arithmetic of the method runs in Python:
   nf4::kv_attention(Tensor q, k_packed, k_absmax, v_packed, v_absmax, block_table,
       kv_lens, Tensor? row_offsets, int blocksize, str quant_type, int max_rows,
       int max_len, float? scale, bool causal, int window) -> Tensor
+  nf4::kv_attention_masked(Tensor q, k_packed, k_absmax, v_packed, v_absmax, block_table,
+      kv_lens, Tensor? row_offsets, int blocksize, str quant_type, int max_rows,
+      int max_len, float? scale, int window, int sinks, Tensor? tree) -> Tensor
+  nf4::mx_quantize(Tensor x) -> (codes, scales)
+  nf4::mx_dequantize(Tensor codes, scales, int[] shape, ScalarType dtype) -> Tensor
+  nf4::mx_linear(Tensor x, codes, scales, Tensor? bias, int N, int K) -> Tensor
 Scale tensors a double-quant mode does not use are passed as empty tensors.
 Each operator has a fake (meta) implementation for tracing. The operators
 are inference operators: no autograd formula is registered.
@@ -38,9 +44,11 @@ import math
 import torch
 from torch import nn
 
-from . import KVCache, QuantState, _dq, dequantize as _dequantize, \
+from . import KVCache, MXTensor, QuantState, _dq, dequantize as _dequantize, \
     kv_attention as _kv_attention, kv_read as _kv_read, kv_write as _kv_write, \
-    linear as _linear, quantize as _quantize
+    linear as _linear, mx_dequantize as _mx_dequantize, mx_linear as _mx_linear, \
+    mx_quantize as _mx_quantize, quantize as _quantize
+from .mx import mx_padded
 
 
 def _state(packed, absmax, absmax_q, absmax_scale, absmax_offset, shape, blocksize, quant_type,
@@ -179,6 +187,62 @@ def _(q, k_packed, k_absmax, v_packed, v_absmax, block_table, kv_lens, row_offse
     return q.new_empty(q.shape)
 
 
+@torch.library.custom_op("nf4::kv_attention_masked", mutates_args=())
+def kv_attention_masked_op(q: torch.Tensor, k_packed: torch.Tensor, k_absmax: torch.Tensor,
+                           v_packed: torch.Tensor, v_absmax: torch.Tensor,
+                           block_table: torch.Tensor, kv_lens: torch.Tensor,
+                           row_offsets: torch.Tensor | None, blocksize: int, quant_type: str,
+                           max_rows: int = 0, max_len: int = 0, scale: float | None = None,
+                           window: int = 0, sinks: int = 0,
+                           tree: torch.Tensor | None = None) -> torch.Tensor:
+    cache = KVCache(k_packed, k_absmax, v_packed, v_absmax, blocksize, quant_type)
+    return _kv_attention(q, cache, block_table, kv_lens, row_offsets, max_rows, max_len, scale,
+                         True, window, sinks=sinks, tree=tree)
+
+
+@kv_attention_masked_op.register_fake
+def _(q, k_packed, k_absmax, v_packed, v_absmax, block_table, kv_lens, row_offsets, blocksize,
+      quant_type, max_rows=0, max_len=0, scale=None, window=0, sinks=0, tree=None):
+    return q.new_empty(q.shape)
+
+
+@torch.library.custom_op("nf4::mx_quantize", mutates_args=())
+def mx_quantize_op(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    t = _mx_quantize(x)
+    return t.codes, t.scales
+
+
+@mx_quantize_op.register_fake
+def _(x):
+    cols = x.shape[-1]
+    rows, padded = x.numel() // cols if cols else 0, mx_padded(cols)
+    return (x.new_empty((rows, padded // 2), dtype=torch.uint8),
+            x.new_empty((padded // 128, rows, 4), dtype=torch.uint8))
+
+
+@torch.library.custom_op("nf4::mx_dequantize", mutates_args=())
+def mx_dequantize_op(codes: torch.Tensor, scales: torch.Tensor, shape: list[int],
+                     dtype: torch.dtype) -> torch.Tensor:
+    return _mx_dequantize(MXTensor(codes, scales, tuple(shape)), dtype)
+
+
+@mx_dequantize_op.register_fake
+def _(codes, scales, shape, dtype):
+    return codes.new_empty(tuple(shape), dtype=dtype)
+
+
+@torch.library.custom_op("nf4::mx_linear", mutates_args=())
+def mx_linear_op(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                 bias: torch.Tensor | None, N: int, K: int) -> torch.Tensor:
+    y = _mx_linear(x.reshape(-1, K), MXTensor(codes, scales, (N, K)), bias)
+    return y.reshape(*x.shape[:-1], N)
+
+
+@mx_linear_op.register_fake
+def _(x, codes, scales, bias, N, K):
+    return x.new_empty((*x.shape[:-1], N))
+
+
 class Linear4bit(nn.Module):
     """A linear layer whose weight is stored as NF4/FP4 4-bit codes with block
     scales (optionally double-quantized) once the module is on the GPU.
@@ -272,5 +336,76 @@ class Linear4bit(nn.Module):
                                     self.double_quant)
 
 
-__all__ = ["Linear4bit", "quantize_op", "dequantize_op", "linear_op", "kv_write_op",
-           "kv_write_values_op", "kv_read_op", "kv_attention_op"]
+class LinearMX(nn.Module):
+    """A linear layer in microscaled 4 bits: its weight is stored as E2M1 codes with a power of
+    two for each 32 of a row once the module is on the GPU, and its inputs are quantized so in
+    each call (nf4::mx_linear); sums are fp32.
+
+    Until then it holds a dense ``weight`` [out_features, in_features] (and ``bias``), as
+    Linear4bit does; moving the module to a GPU replaces the weight by the buffers
+    ``weight_codes`` and ``weight_scales``. The forward pass casts its input to
+    ``compute_dtype``, in which the output is.
+    """
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True,
+                 compute_dtype=torch.bfloat16, device=None, dtype=None):
+        super().__init__()
+        if compute_dtype not in (torch.bfloat16, torch.float16, torch.float32):
+            raise ValueError("compute_dtype must be bf16, fp16 or fp32")
+        self.in_features = in_features
+        self.out_features = out_features
+        self.compute_dtype = compute_dtype
+        self.weight = nn.Parameter(torch.empty(out_features, in_features, device=device,
+                                               dtype=dtype), requires_grad=False)
+        if bias:
+            self.bias = nn.Parameter(torch.empty(out_features, device=device, dtype=dtype),
+                                     requires_grad=False)
+        else:
+            self.register_parameter("bias", None)
+        # nn.Linear's default initialisation, for modules not loaded from a checkpoint
+        nn.init.kaiming_uniform_(self.weight, a=math.sqrt(5))
+        if self.bias is not None:
+            bound = 1 / math.sqrt(in_features) if in_features > 0 else 0
+            nn.init.uniform_(self.bias, -bound, bound)
+        self.quantized = False
+        if self.weight.is_cuda:
+            self._quantize()
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"bias={self.bias is not None}, compute_dtype={self.compute_dtype}, "
+                f"quantized={self.quantized}")
+
+    @torch.no_grad()
+    def _quantize(self) -> None:
+        w = self.weight.detach()
+        if w.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+            w = w.float()
+        codes, scales = torch.ops.nf4.mx_quantize(w)
+        del self.weight
+        self.register_parameter("weight", None)
+        self.register_buffer("weight_codes", codes)
+        self.register_buffer("weight_scales", scales)
+        if self.bias is not None:
+            self.bias = nn.Parameter(self.bias.detach().to(self.compute_dtype), requires_grad=False)
+        self.quantized = True
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        # quantization happens when the dense weight reaches the GPU
+        if not self.quantized and self.weight is not None and self.weight.is_cuda:
+            self._quantize()
+        return self
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if not self.quantized:
+            raise RuntimeError("LinearMX runs on the GPU: move it there with .to('cuda')")
+        x = x.to(self.compute_dtype)
+        bias = self.bias if self.bias is None else self.bias.to(self.compute_dtype)
+        return torch.ops.nf4.mx_linear(x, self.weight_codes, self.weight_scales, bias,
+                                       self.out_features, self.in_features)
+
+
+__all__ = ["Linear4bit", "LinearMX", "quantize_op", "dequantize_op", "linear_op", "kv_write_op",
+           "kv_write_values_op", "kv_read_op", "kv_attention_op", "kv_attention_masked_op",
+           "mx_quantize_op", "mx_dequantize_op", "mx_linear_op"]
