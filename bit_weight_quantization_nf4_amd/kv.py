@@ -100,15 +100,17 @@ class KVCache:
         nb = 2 * half // blocksize if blocksize > 0 else 0
         if v_packed.shape != shape:
             raise ValueError("KVCache expects codes of one shape, contiguous in a page")
-        stride = _page_stride(shape, k_packed.stride())
-        if stride < 0 or _page_stride(shape, v_packed.stride()) != stride:
+        dense = k_packed.is_contiguous() and v_packed.is_contiguous() and \
+            k_absmax.is_contiguous() and v_absmax.is_contiguous()
+        stride = heads * page_size * half if dense else _page_stride(shape, k_packed.stride())
+        if not dense and (stride < 0 or _page_stride(shape, v_packed.stride()) != stride):
             raise ValueError("KVCache expects codes of one shape, contiguous in a page")
         if k_absmax.dtype is not torch.float32 or v_absmax.dtype is not torch.float32 or \
                 sshape != (pages, heads, page_size, nb) or v_absmax.shape != sshape:
             raise ValueError("KVCache expects fp32 scales [pages, kv heads, page_size, "
                              "head_dim / blocksize]")
-        sstride = _page_stride(sshape, k_absmax.stride())
-        if sstride < 0 or _page_stride(sshape, v_absmax.stride()) != sstride:
+        sstride = heads * page_size * nb if dense else _page_stride(sshape, k_absmax.stride())
+        if not dense and (sstride < 0 or _page_stride(sshape, v_absmax.stride()) != sstride):
             raise ValueError("KVCache expects scales contiguous in a page, keys' and values' "
                              "pages equally far apart")
         index = k_packed.get_device()
@@ -146,12 +148,13 @@ class KVCache:
 
 def _rows(cache: KVCache, total: int, block_table, kv_lens, row_offsets, what: str) -> KVRowsDesc:
     int32 = torch.int32
+    shape, lens_shape = block_table.shape, kv_lens.shape
     if block_table.dtype is not int32 or kv_lens.dtype is not int32 or \
-            block_table.dim() != 2 or kv_lens.dim() != 1:
+            len(shape) != 2 or len(lens_shape) != 1:
         raise TypeError(f"{what} expects int32 block_table [batch, pages] and kv_lens [batch]")
-    batch, cols = block_table.shape
+    batch, cols = shape
     stride, inner = block_table.stride()
-    if kv_lens.shape[0] != batch or not kv_lens.is_contiguous() or \
+    if lens_shape[0] != batch or not kv_lens.is_contiguous() or \
             (cols > 1 and inner != 1) or (batch > 1 and stride < cols):
         raise ValueError(f"{what}: block_table needs unit column stride, kv_lens [batch]")
     index = cache.index
@@ -171,26 +174,31 @@ def _strides(t: torch.Tensor):
     """(row, head) strides of [rows, heads, head_dim] for the ABI, None where it does not
     take the tensor as it is. The stride of a single row or head addresses nothing and may
     be anything."""
-    r, h, e = t.stride()
     n, heads, d = t.shape
+    es = t.element_size()
+    if t.is_contiguous():
+        return (heads * d, d) if not (d * es | t.data_ptr()) & 15 else None
+    r, h, e = t.stride()
     if n <= 1:
         r = heads * d
     if heads <= 1:
         h = d
-    es = t.element_size()
     if e == 1 and r >= d and h >= d and not (r * es | h * es | t.data_ptr()) & 15:
         return r, h
     return None
 
 
 def _empty_rows(t: torch.Tensor) -> torch.Tensor:
+    if t.is_contiguous():
+        return torch.empty_like(t)
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _check_rows(t: torch.Tensor, cache: KVCache, what: str) -> None:
     if t.dtype not in _DT or t.get_device() != cache.index:
         raise TypeError(f"{what} expects bf16 / fp16 / fp32 rows on the cache's GPU")
-    if t.dim() != 3 or t.shape[2] != cache.head_dim:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
         raise ValueError(f"{what} expects rows [rows, heads, head_dim]")
 
 
@@ -203,13 +211,14 @@ def _aligned_copy(t: torch.Tensor) -> torch.Tensor:
 # the raw handle of a device's current stream: building a Stream object takes longer
 # than the launch itself
 _stream_of = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
 
 
 def _call(cache: KVCache, run) -> None:
     """run(stream) -> (status, name) with the cache's device current, on its current
     stream."""
     index = cache.index
-    if index == torch.cuda.current_device():
+    if index == _current():
         status, name = run(_stream_of(index))
     else:
         with torch.cuda.device(index):

@@ -58,7 +58,7 @@ class MXTensor:
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, shape):
         rows, cols = shape
-        padded = mx_padded(cols)
+        padded = -(-cols // 128) * 128
         u8 = torch.uint8
         if codes.dtype is not u8 or scales.dtype is not u8 or codes.shape != (rows, padded // 2) or \
                 scales.shape != (padded // 128, rows, 4):
