@@ -77,14 +77,14 @@ struct MxEight {
 // (of any alignment: the memory instructions take it, 16 bytes at once)
 typedef mx_u32x4 mx_any_u32x4 __attribute__((aligned(2)));
 
-template <int DT>
+template <int DT, bool ONCE = false>  // ONCE: not kept in the caches
 __device__ __forceinline__ MxEight<DT> mx_load_eight(const void *row, int64_t col) {
   MxEight<DT> e;
   const auto *p = reinterpret_cast<const mx_any_u32x4 *>(static_cast<const char *>(row) +
                                                          col * (DT == kFP32 ? 4 : 2));
 #pragma unroll
   for (int i = 0; i < (DT == kFP32 ? 2 : 1); ++i) {
-    const mx_u32x4 v = p[i];
+    const mx_u32x4 v = ONCE ? __builtin_nontemporal_load(p + i) : p[i];
 #pragma unroll
     for (int j = 0; j < 4; ++j) e.w[4 * i + j] = v[j];
   }

@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kCols = 512, kThreads = 256, kWaves = 4;
 
-template <int DT, int kWaveRows>
+template <int DT, int kWaveRows, bool ONCE>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *x, int64_t rows,
                                                                int32_t cols, int32_t padded,
                                                                int64_t ld, int32_t col_tiles,
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *x, in
     const int r = wave + kWaves * i;
     if (r >= here) continue;
     const char *row = static_cast<const char *>(x) + (row0 + r) * ld * (DT == kFP32 ? 4 : 2);
-    if (col + 8 <= cols) e[i] = mx_load_eight<DT>(row, col);
+    if (col + 8 <= cols) e[i] = mx_load_eight<DT, ONCE>(row, col);
     else e[i] = mx_load_ragged<DT>(row, col, cols);
   }
 #pragma unroll
@@ -53,7 +53,13 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *x, in
         *reinterpret_cast<const uint32_t *>(s_lds[t][r]);
 }
 
-template <int DT, int kWaveRows>
+template <bool ONCE>
+__device__ __forceinline__ void put(mx_u32x4 v, mx_any_u32x4 *p) {
+  if constexpr (ONCE) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
+template <int DT, int kWaveRows, bool ONCE>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxMatrix m, int32_t col_tiles,
                                                                  void *out, int64_t ld) {
   constexpr int kRows = kWaves * kWaveRows;
@@ -94,8 +100,8 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxMatrix m, int
         auto *q = reinterpret_cast<mx_any_u32x4 *>(p);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          q[j] = mx_u32x4{__float_as_uint(f[2 * j].x), __float_as_uint(f[2 * j].y),
-                          __float_as_uint(f[2 * j + 1].x), __float_as_uint(f[2 * j + 1].y)};
+          put<ONCE>(mx_u32x4{__float_as_uint(f[2 * j].x), __float_as_uint(f[2 * j].y),
+                             __float_as_uint(f[2 * j + 1].x), __float_as_uint(f[2 * j + 1].y)}, q + j);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -107,7 +113,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxMatrix m, int
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = pack2<DT>(f[j].x, f[j].y);
       if (col + 8 <= m.cols) {
-        *reinterpret_cast<mx_any_u32x4 *>(p) = mx_u32x4{w[0], w[1], w[2], w[3]};
+        put<ONCE>(mx_u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<mx_any_u32x4 *>(p));
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -123,19 +129,28 @@ int64_t tiles_of(int64_t rows, int64_t cols, int tile_rows) {
 }
 
 // Rows of a wave: 8, or 1 where two workgroups a CU of 32 rows are not reached. (16 x 11008: 4.4 us
-// and 2.2.)
+// and 2.2.) From kOnceBytes of values on these go past the caches, which the codes then have to
+// themselves. (In bf16, quantized and restored, other inputs each time: 11008 x 4096 42.5 us, 49.5
+// through the caches, 8192 x 4096 33, 39; 2048 x 4096 quantized in 7.0 and 6.6.)
+constexpr int64_t kOnceBytes = (int64_t)64 << 20;
+
 template <typename F>
-void by_rows(int64_t rows, int64_t cols, F &&run) {
-  if (tiles_of(rows, cols, 8 * kWaves) >= 2 * device_cu_count()) run(std::integral_constant<int, 8>{});
-  else run(std::integral_constant<int, 1>{});
+void by_size(int64_t rows, int64_t cols, int64_t bytes_each, F &&run) {
+  using std::integral_constant;
+  if (tiles_of(rows, cols, 8 * kWaves) < 2 * device_cu_count())
+    run(integral_constant<int, 1>{}, std::false_type{});
+  else if (rows * cols * bytes_each < kOnceBytes)
+    run(integral_constant<int, 8>{}, std::false_type{});
+  else
+    run(integral_constant<int, 8>{}, std::true_type{});
 }
 
 template <int DT>
 void quantize_as(const void *x, int64_t rows, int32_t cols, int64_t ld, uint8_t *codes,
                  uint8_t *scales, hipStream_t stream) {
-  by_rows(rows, cols, [&](auto wave_rows) {
+  by_size(rows, cols, DT == kFP32 ? 4 : 2, [&](auto wave_rows, auto once) {
     constexpr int R = decltype(wave_rows)::value;
-    hipLaunchKernelGGL((mx_quantize_kernel<DT, R>), dim3((unsigned)tiles_of(rows, cols, R * kWaves)),
+    hipLaunchKernelGGL((mx_quantize_kernel<DT, R, decltype(once)::value>), dim3((unsigned)tiles_of(rows, cols, R * kWaves)),
                        dim3(kThreads), 0, stream, x, rows, cols, (int32_t)mx_padded(cols), ld,
                        (int32_t)col_tiles_of(cols), codes, scales);
   });
@@ -143,9 +158,9 @@ void quantize_as(const void *x, int64_t rows, int32_t cols, int64_t ld, uint8_t 
 
 template <int DT>
 void dequantize_as(const MxMatrix &m, void *out, int64_t ld, hipStream_t stream) {
-  by_rows(m.rows, m.cols, [&](auto wave_rows) {
+  by_size(m.rows, m.cols, DT == kFP32 ? 4 : 2, [&](auto wave_rows, auto once) {
     constexpr int R = decltype(wave_rows)::value;
-    hipLaunchKernelGGL((mx_dequantize_kernel<DT, R>),
+    hipLaunchKernelGGL((mx_dequantize_kernel<DT, R, decltype(once)::value>),
                        dim3((unsigned)tiles_of(m.rows, m.cols, R * kWaves)), dim3(kThreads), 0,
                        stream, m, (int32_t)col_tiles_of(m.cols), out, ld);
   });

@@ -111,6 +111,27 @@ def test_quantize_strided_views_and_outputs(nf4, dtype):
     assert torch.equal(again.codes, t.codes) and torch.equal(again.scales, t.scales)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_large_matrices_are_their_parts(nf4, dtype):
+    """Past 64 MiB, 32 rows a workgroup, and a few rows (which test_quantize_and_restore holds to
+    the reference): the same bits from the kernels that each size takes, rows that end in no
+    workgroup's last, columns in no block's."""
+    rows, cols = 8331 if dtype.itemsize == 2 else 4203, 4099
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, cols, generator=g, device="cuda") * torch.exp(
+        torch.randn(rows, 1, generator=g, device="cuda"))
+    x = x.to(dtype)
+    whole = nf4.mx_quantize(x)
+    for out in (dtype, torch.bfloat16):
+        v = nf4.mx_dequantize(whole, out)
+        for lo, hi in ((0, 3001), (3001, 3300), (rows - 77, rows)):
+            t = nf4.mx_quantize(x[lo:hi])
+            assert torch.equal(t.codes, whole.codes[lo:hi])
+            assert torch.equal(t.scales, whole.scales[:, lo:hi])
+            assert torch.equal(nf4.mx_dequantize(t, out), v[lo:hi])
+    check_quantized(nf4, x[rows - 33:].cpu(), x[rows - 33:])
+
+
 def test_restore_every_scale_and_code(nf4):
     codes = torch.arange(16).repeat(256, 8)
     scales = torch.arange(256)[:, None].repeat(1, 4)
