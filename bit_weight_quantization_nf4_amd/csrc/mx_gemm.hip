@@ -355,16 +355,18 @@ int64_t tiles_of(int64_t M, int64_t N, bool large) {
 int64_t pitch_of(int64_t N) { return ceil_div(N, 4) * 4; }  // of a range's results
 
 // Tiles and ranges by about the time that they take. In us, of 256-wide stages: a workgroup of
-// large tiles has a CU to itself and takes 1.9 a stage where all CUs work, and 6 to begin and end; of
-// small tiles 0.6 and 3, but 1.25 and 4 where two share a CU; a second launch 4 and its traffic.
-// (2048 x 14336 x 4096: large 75, small 80; 8192 cubed 280, 337; 4096 x 4096 x 4096: 40, 46; 1024 x
-// 11008 x 4096: 32, 39; 512 x 4096 x 4096: 25, 13; 1024 x 4096 x 14336: 58, 43. 128 x 4096 x 14336 in
+// large tiles has a CU to itself and takes 1.9 a stage where all CUs work, down to 1.3 with few, and
+// 6 to begin and end; of small tiles 0.6 and 3, but 1.25 and 4 where two share a CU; a second launch 4 and its traffic.
+// (2048 x 14336 x 4096: large 75, small 80; 8192 cubed 280, 337; 4096 x 4096 x 4096: 40, 46; 2048 x
+// 11008 x 4096: 60, 66, x 4096: 30, 25; 512 x 4096 x 4096: 25, 13; 1024 x 4096 x 14336: 58, 43. 128 x 4096 x 14336 in
 // 1, 2, 4, 6, 8 ranges: 38, 26, 19, 18, 19; x 4096: 12.1, 13.6, 14.1, 16.1, 18.8.)
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t cus = device_cu_count(), steps = mx_padded(K) / kMxStep, stages = ceil_div(steps, 2);
   const int64_t large = tiles_of(M, N, true), small = tiles_of(M, N, false);
   Plan best{true, 1, (int)steps};
-  double least = (double)ceil_div(large, cus) * (1.9 * (double)stages + 6);
+  const int64_t rest = large % cus;  // of the last round of workgroups
+  double least = (double)(large / cus) * (1.9 * (double)stages + 6);
+  if (rest > 0) least += (1.3 + 0.6 * (double)rest / (double)cus) * (double)stages + 6;
   for (int64_t s = 1; s <= stages && (s == 1 || s * small <= 2 * cus); ++s) {
     const int64_t each = ceil_div(stages, s);
     if (ceil_div(stages, each) != s) continue;  // the same ranges as of fewer
