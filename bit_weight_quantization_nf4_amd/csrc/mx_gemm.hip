@@ -6,15 +6,21 @@
 // are brought straight to LDS, into one of two stages, and multiplied in two steps of 128. A wave
 // reads a step's operands into registers while the step before is multiplied, so a stage is free
 // for new loads from its second step on, and these have that step and the next to come.
-// (Whole cache lines: with steps of 64 bytes a row each line came twice; 2048 x 14336 x 4096: 98
-// us.)
+// (Whole cache lines: with steps of 64 bytes a row each line came twice; 2048 x 14336 x 4096, with
+// four waves of 128 x 128 each, 98 us and 89.)
 //
 // Which rows of the operands make up a matrix-core tile is free. Tile i of a wave takes rows FT p
 // + i, p < 32: a lane finds the scales of its FT rows side by side in LDS and holds runs of 4 FT
 // neighbouring features of a result.
 //
 // LDS: the sixteen 16-byte pieces of two neighbouring rows lie at places xor'ed with p, which
-// differs between the sixteen lanes that are read together.
+// differs between the sixteen lanes that are read together (no conflicts; 8192 cubed 318 -> 276 us).
+//
+// What bounds it, on one MI355X: 8192 cubed takes 250 to 280 us, 3.9 to 4.4 PFLOP/s; without its
+// loads and stores 209 us, 5.3 PFLOP/s, where a single workgroup's steps take half the time that
+// they do with all CUs at work: the matrix cores' clock under that load. 2048 x 14336 x 4096, 448
+// tiles in two rounds of 256: 66 to 75 us, 3.2 to 3.7 PFLOP/s; the second round leaves a quarter of
+// the CUs idle, and each round's results, 33 MB, are written while nothing is multiplied.
 #include <type_traits>
 
 #include "mx_internal.h"
@@ -122,28 +128,30 @@ void mx_gemm_kernel(GemmArgs a) {
   const __amdgpu_buffer_rsrc_t mc = __builtin_amdgcn_make_buffer_rsrc(
       uniform(a.x.codes + m0 * half), (short)0, (int)((uint32_t)m_rows * half), kBufferFlags);
   uint32_t code_at[kLoads];
+  uint32_t late = 0;  // loads (by bit) of which the lane's piece is of the stage's second half
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const bool of_w = i < kLoadsF;
     const int two = 8 * (wave + kWaves * (of_w ? i : i - kLoadsF)) + 2 * (lane >> 4);  // rows two, two + 1
     const int piece = (lane & 15) ^ (two / (of_w ? FT : TT) & 15);
     code_at[i] = (uint32_t)(two + (piece >> 3)) * half + 16 * (piece & 7) + 64 * (uint32_t)step0;
+    late |= (uint32_t)(piece >> 2 & 1) << i;
   }
   // the wave's scales: loads wave, wave + kWaves, ... of the halves' rows
   const int64_t stride_f = 4 * a.w.rows, stride_m = 4 * a.x.rows;
   const uint8_t *base_f = uniform(a.w.scales + step0 * stride_f + 4 * f0);
   const uint8_t *base_m = uniform(a.x.scales + step0 * stride_m + 4 * m0);
-  // stage b, of the stages in order. (Past the last step: loads of zeros, so that each stage
-  // issues as many. Of a last one's second half, which is not there, the codes are the next row's
-  // first, or zeros: nothing multiplies them.)
+  // stage b, of the stages in order. (What is past the last step, a stage or its second half, is
+  // loaded as zeros, so that each stage issues as many loads and none leaves the matrix.)
   auto fill = [&](int b) {
     const int stage = b % kStages;
     const bool there = 2 * b < steps;
     const uint32_t at = there ? 128u * (uint32_t)b : 0u;
-    const uint32_t none = there ? 0u : 0x80000000u;
+    const uint32_t out = !there ? 0xffffffffu : 2 * b + 1 < steps ? 0u : late;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const LdsPtr dst = lds_place(&codes[stage][1024 * (wave + kWaves * i)]);
+      const uint32_t none = out << (31 - i) & 0x80000000u;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(i < kLoadsF ? fc : mc, dst, 16,
                                                (int)(code_at[i] | none), (int)at, 0, 0);
     }
@@ -356,10 +364,11 @@ int64_t pitch_of(int64_t N) { return ceil_div(N, 4) * 4; }  // of a range's resu
 
 // Tiles and ranges by about the time that they take. In us, of 256-wide stages: a workgroup of
 // large tiles has a CU to itself and takes 1.9 a stage where all CUs work, down to 1.3 with few, and
-// 6 to begin and end; of small tiles 0.6 and 3, but 1.25 and 4 where two share a CU; a second launch 4 and its traffic.
-// (2048 x 14336 x 4096: large 75, small 80; 8192 cubed 280, 337; 4096 x 4096 x 4096: 40, 46; 2048 x
-// 11008 x 4096: 60, 66, x 4096: 30, 25; 512 x 4096 x 4096: 25, 13; 1024 x 4096 x 14336: 58, 43. 128 x 4096 x 14336 in
-// 1, 2, 4, 6, 8 ranges: 38, 26, 19, 18, 19; x 4096: 12.1, 13.6, 14.1, 16.1, 18.8.)
+// 6 to begin and end; of small tiles 0.6 and 3, but 1.25 and 4 where two share a CU; a second launch 4
+// and its traffic. (2048 x 14336 x 4096: large 75, small 80; 8192 cubed 280, 337; 4096 x 4096 x 4096:
+// 40, 46; 2048 x 11008 x 4096: 60, 66, x 4096: 30, 25; 512 x 4096 x 4096: 25, 13; 1024 x 4096 x 14336:
+// 58, 43. 128 x 4096 x 14336 in 1, 2, 4, 6, 8 ranges: 38, 26, 19, 18, 19; x 4096: 12.1, 13.6, 14.1,
+// 16.1, 18.8.)
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t cus = device_cu_count(), steps = mx_padded(K) / kMxStep, stages = ceil_div(steps, 2);
   const int64_t large = tiles_of(M, N, true), small = tiles_of(M, N, false);
@@ -367,7 +376,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t rest = large % cus;  // of the last round of workgroups
   double least = (double)(large / cus) * (1.9 * (double)stages + 6);
   if (rest > 0) least += (1.3 + 0.6 * (double)rest / (double)cus) * (double)stages + 6;
-  for (int64_t s = 1; s <= stages && (s == 1 || s * small <= 2 * cus); ++s) {
+  for (int64_t s = 1; s <= stages && s <= 32 && (s == 1 || s * small <= 2 * cus); ++s) {
     const int64_t each = ceil_div(stages, s);
     if (ceil_div(stages, each) != s) continue;  // the same ranges as of fewer
     double t = s * small <= cus ? 0.6 * (double)each + 3

@@ -77,7 +77,8 @@ nf4_status nf4_mx_matmul(const nf4_mx_matrix *x, const nf4_mx_matrix *w, const v
 
 /* The same with x [M][K] of x_dtype, rows ldx elements apart, which the call quantizes as
  * nf4_mx_quantize does: bitwise nf4_mx_matmul's result on that. Workspace:
- * nf4_mx_linear_workspace_bytes(M, N, K). */
+ * nf4_mx_linear_workspace_bytes(M, N, K). (Products of matrices without columns are not
+ * supported.) */
 nf4_status nf4_mx_linear(const void *x, int32_t x_dtype, int64_t ldx, int64_t M,
                          const nf4_mx_matrix *w, const void *bias, int32_t out_dtype, void *y,
                          int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream);

@@ -312,3 +312,61 @@ def test_streams_and_graphs(nf4, m):
         eager = nf4.mx_quantize(x)
         assert torch.equal(out, y) and torch.equal(same, y)
         assert torch.equal(back, nf4.mx_dequantize(eager))
+
+
+@pytest.mark.parametrize("m", [1, 12, 50, 130, 700])
+@pytest.mark.parametrize("k", [300, 640, 5000])
+def test_what_lies_behind_a_matrix_has_no_part(nf4, m, k):
+    """Matrices at the end of a buffer, with codes and NaN scales of no concern behind them (an
+    odd number of 128-wide steps ends inside a stage)."""
+    n = 200
+    x, w = nf4.mx_quantize(rows_of(m, k, torch.float32, 1).cuda()), weight_of(nf4, n, k, 2)
+    want = nf4.mx_linear(x, w)
+
+    def surrounded(t):
+        out = []
+        for a, fill in ((t.codes, 0x77), (t.scales, 255)):
+            room = torch.full((a.numel() + 4096,), fill, dtype=torch.uint8, device="cuda")
+            out.append(room[:a.numel()].view(a.shape).copy_(a))
+        return nf4.MXTensor(*out, t.shape)
+
+    assert torch.equal(nf4.mx_linear(surrounded(x), surrounded(w)), want)
+    assert bool(torch.isfinite(want).all())
+
+
+def test_calls_at_once_and_graphs_that_share_memory(nf4):
+    """Products with workspaces (x quantized, ranges of K) in flight on streams of their own, and
+    in two graphs of one pool, replayed in turn beside eager work: each is what it is alone."""
+    shapes = [(100, 33, 14336), (20, 300, 4096), (300, 260, 2048)]
+    ws = [weight_of(nf4, n, k, n) for _, n, k in shapes]
+    xs = [rows_of(m, k, torch.bfloat16, m).cuda() for m, _, k in shapes]
+
+    def step():
+        return [nf4.mx_linear(x, w) for x, w in zip(xs, ws)]
+
+    want = step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(step())
+    torch.cuda.synchronize()
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    graphs, held = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=graphs[0].pool() if graphs else None):
+            held.append(step())
+        graphs.append(g)
+    for _ in range(3):
+        for g, out in zip(graphs, held):
+            for t in out:
+                t.fill_(0)
+            g.replay()
+            again = step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+            assert all(torch.equal(a, b) for a, b in zip(again, want))
