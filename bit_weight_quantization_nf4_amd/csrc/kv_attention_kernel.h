@@ -62,6 +62,25 @@
 //     well within a SIMD. Each wave decodes the same codes for rows of its own.
 //   - short calls: 9 us, of which the arguments' way, the table and the merge of the
 //     waves are 6.
+//
+// The masked form (MASK: a window with sinks, or a tree of drafted rows) is the same kernel with
+// other limits. A block's steps are the sinks', then those from the window's first on: one
+// loop over both with a jump between them, so a range may hold the end of one and the
+// beginning of the other, and a step that all rows see takes no masks. Of a tree, only the steps
+// that reach into the call's rows look at the rows' bits. Its bounds are the ones above:
+//   - 32 uneven sequences of one row, window 4096 and 4 sinks (134.6 MB): 34 us, 4.0 TB/s,
+//     and 4 us of joining;
+//   - 512 and 256 fp16 rows in a window of 2048 with 33 sinks (26.2 GFLOP of the
+//     definition's): 145 us, 180 TFLOP/s: 192 workgroups of waves with rows of their own, so a
+//     SIMD has one wave or none, which takes 66 steps of some 4600 cycles;
+//   - trees of 26 rows at 131071 positions, 8 heads of a kv head, FP4, blocks of 32 (27.9 GFLOP):
+//     86 us, 325 TFLOP/s, and 4 of joining. A wave's step is 548 VALU instructions and 48
+//     MFMA; the SIMDs issue VALU in 71 of 100 cycles, MFMA in 22.
+//   - 16 uneven trees of up to 64 rows at up to 6000 positions (36.4 GFLOP): 155 us, 17 of
+//     them joining.
+// Tried: waves that share a step's lookups through LDS (17 % fewer cycles a step, but the
+// waves then wait for each other, and no call was faster); 8 waves of 128 registers (110
+// spilled).
 #pragma once
 
 #include <type_traits>

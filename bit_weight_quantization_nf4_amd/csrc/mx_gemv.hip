@@ -6,6 +6,11 @@
 // turn, batches of kBatch steps' loads in flight at once, and add their sums up in wave order.
 // With few rows of x the workgroup quantizes them itself into LDS while the weight's first
 // batch is on its way; else x is quantized before and its codes are read beside the weight's.
+//
+// What bounds it, on one MI355X: the weight's bytes, each of which comes once, and a launch's own
+// 2 us. One row, 11008 x 4096 (23.9 MB): 6.7 us, 3.6 TB/s; a kernel that hardly does a thing takes
+// 2.2 there, and what is left moves at 5.3 TB/s (a copy: 5.2). 16 rows, 4096 x 11008: 8.1 us, and
+// 2.2 to 3.0 for the launch that quantizes x. 64 rows, 11008 x 4096: 12 us and 2.5.
 #include "mx_internal.h"
 
 namespace nf4 {

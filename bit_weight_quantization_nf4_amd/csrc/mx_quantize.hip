@@ -1,10 +1,16 @@
 // mx_quantize.hip -- microscaled 4-bit quantisation of a matrix, and its reverse.
 //
+// With a = max |x| of a block of 32, its scale is 2^(floor(log2 a) - 2): a's exponent bits less 2,
+// so x / scale is exact, lies below 8, and is rounded once, to the nearest of E2M1's values.
+//
 // A workgroup takes 32 rows of 512 columns, a wave 8 of the rows (4 and 1 where that leaves CUs
-// without work); a lane holds 8 neighbouring
-// elements (16 bytes of 16-bit ones), so a block of 32 is four lanes, and its largest
-// magnitude two lane exchanges. Codes leave as a dword a lane, scales through LDS as whole
-// 128-byte lines of 32 rows.
+// without work); a lane holds 8 neighbouring elements (16 bytes of 16-bit ones), so a block of 32
+// is four lanes, and its largest magnitude two lane exchanges. Codes leave as a dword a lane,
+// scales through LDS as whole 128-byte lines of 32 rows.
+//
+// What bounds it, on one MI355X: HBM. 11008 x 4096 in bf16 (114 MB): quantized in 22 to 23 us, 5.0
+// TB/s, restored in 17, 6.7 TB/s (four fifths of it writes); a copy moves 5.2. One row of 4096: 2.2
+// us each, a launch.
 #include <type_traits>
 
 #include "mx_internal.h"
