@@ -115,6 +115,8 @@ constexpr int kApartMinRows = 128;
 // 4096 176.7 whole, 162.9 in two).
 constexpr int64_t kSplitFrom = 2048, kMinRange = 512;
 constexpr int64_t kSplitFromApart = 4096, kMinRangeApart = 2048;
+// From how many positions on the masked form's blocks are shared by waves (below).
+constexpr int64_t kSharedFrom = 1536;
 // What a range costs besides its positions, in positions.
 constexpr int64_t kRangeCost = 700;
 
@@ -125,8 +127,19 @@ Plan plan_of(const KvAttentionSizes &z) {
   Plan p;
   const int64_t pairs = (int64_t)z.max_rows * (z.heads / z.kv_heads);
   const int64_t apart_blocks = ceil_div(pairs, 16 * max_tiles(z.head_dim) * kApartWaves);
-  p.merge = pairs < kApartMinRows ||
-            (int64_t)z.batch * z.kv_heads * apart_blocks < device_cu_count();
+  const int64_t apart_items = (int64_t)z.batch * z.kv_heads * apart_blocks;
+  // positions that a row sees at most
+  int64_t span = z.max_len;
+  const int64_t reach = (int64_t)z.window + z.sinks + z.max_rows;
+  if (z.window > 0 && span > reach) span = reach;
+  p.merge = pairs < kApartMinRows || apart_items < device_cu_count();
+  // The masked form also shares blocks up to one and a half workgroups a CU, where sequences are
+  // long: a second workgroup of a CU makes both slower, and blocks a quarter as large leave
+  // fewer CUs idle behind uneven sequences. (32 bf16 heads of 8, us shared and apart: windows of
+  // 512, 2048 and 8192 with 4 x 256 rows 62 and 41, 114 and 113, 326 and 330; with 4 x 1024
+  // 238 and 106, 431 and 295, 1261 and 1017. 16 trees of 64 rows at 3000 152 and 152, of 64 to 4
+  // rows at 3000 to 188 94 and 147; 4 of 300 at 6000 308 and 388, uneven 178 and 319.)
+  if (z.masked && span >= kSharedFrom && 2 * apart_items <= 3 * device_cu_count()) p.merge = true;
   // More rows than a tile's: blocks of two tiles look a position's codes up once for both.
   // (8 kv heads of 128 in bf16, 16 sequences at 6000 positions: 20 rows a kv head 43 us, in
   // one-tile blocks 53; 48 rows 63, 70; 96 rows 118, 114. Short calls lose by the second
@@ -136,14 +149,12 @@ Plan plan_of(const KvAttentionSizes &z) {
   p.wg_blocks = (int)ceil_div(pairs, p.wg_rows);
   p.align = kStep * (p.merge ? kMergeWaves : 1);
   const int64_t items = (int64_t)z.batch * z.kv_heads * p.wg_blocks;
-  // positions that a row sees at most, in units of the time that one takes at 16 bits
-  // and head_dim 128
-  int64_t span = z.max_len;
-  const int64_t reach = (int64_t)z.window + z.sinks + z.max_rows;
-  if (z.window > 0 && span > reach) span = reach;
+  // positions count in units of the time that one takes at 16 bits and head_dim 128
   const int64_t weight = z.head_dim * (z.dtype == kFP32 ? 3 : 1);
   int64_t s = 1;
-  if (span * weight >= (p.merge ? kSplitFrom : kSplitFromApart) * 128) {
+  // (masked blocks of waves with rows of their own are short or many: whole)
+  const bool whole = z.masked && !p.merge;
+  if (!whole && span * weight >= (p.merge ? kSplitFrom : kSplitFromApart) * 128) {
     // as many ranges as fill the device once, or twice where workgroups of uneven
     // sequences share a CU, whichever is done first: every round of workgroups takes a
     // range's time. (Sequences up to 8000, 8 kv heads, one row: 40 of them 64.6 us with
@@ -161,13 +172,6 @@ Plan plan_of(const KvAttentionSizes &z) {
       if (cost >= best) continue;
       best = cost;
       s = c;
-    }
-    // The masked form has its ranges of one length, and half as many again: of uneven sequences
-    // no workgroup is then left with a long one. (16 of 64 to 4 rows at 6000 to 375 positions, 32
-    // heads of 8: 156 us in three ranges, 216 in two; all of 64 at 6000: 242, 229.)
-    if (z.masked && !p.merge && items > 0) {
-      const int64_t more = ceil_div(3 * slots, 2 * items);
-      if (s > 1 && more > s) s = more;
     }
     const int64_t least = p.merge ? kMinRange * 128 / weight : kMinRangeApart;
     const int64_t most = ceil_div(span, least > 0 ? least : 1);
@@ -197,14 +201,16 @@ template <int D, int DT, bool MASK>
 hipError_t launch_join(const ArgsOf<MASK> &a, const Plan &p, hipStream_t stream) {
   const int rows = a.max_rows * a.group;
   dim3 grid((unsigned)rows, (unsigned)a.kv.kv_heads, (unsigned)a.kv.batch);
-  if (p.merge) {
-    hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, false, MASK>), grid, dim3(64 * kJoinWaves), 0,
-                       stream, a, p.align);
-  } else {
-    grid.x = (unsigned)ceil_div(rows, kJoinWaves);
-    hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, true, MASK>), grid, dim3(64 * kJoinWaves), 0,
-                       stream, a, p.align);
+  if constexpr (!MASK) {
+    if (!p.merge) {
+      grid.x = (unsigned)ceil_div(rows, kJoinWaves);
+      hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, true, MASK>), grid, dim3(64 * kJoinWaves),
+                         0, stream, a, p.align);
+      return hipGetLastError();
+    }
   }
+  hipLaunchKernelGGL((kv_attention_join_kernel<D, DT, false, MASK>), grid, dim3(64 * kJoinWaves), 0,
+                     stream, a, p.align);
   return hipGetLastError();
 }
 

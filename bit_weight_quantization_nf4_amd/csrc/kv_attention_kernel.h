@@ -528,7 +528,7 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
     if (item.row0 >= item.pairs || (begin >= item.hi && args.splits > 1)) return;
   }
   // (masked form: a block of one range leaves nothing to join)
-  const bool whole_item = args.splits == 1 || (MASK && range >= span_of(item));
+  const bool whole_item = (MASK && !MERGE) || args.splits == 1 || (MASK && range >= span_of(item));
   const int64_t part_row0 = (item_of(args, seq, h, wb) * args.splits + split) * args.part_rows;
   // a wave's own rows may see less, and there may be none
   const Block blk = MERGE ? item : block_of<MASK>(args, of, item.row0 + wave * A::kRows, A::kRows);

@@ -357,3 +357,16 @@ def test_binding_refusals(nf4, orc):  # noqa: F811
             call_with(**kw)
     with pytest.raises(nf4.Nf4Error):
         call_with(sinks=-1, window=5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_many_blocks_at_long_tables(nf4, orc, dtype):  # noqa: F811
+    """Blocks enough for waves with rows of their own where max_len is long (each is then whole),
+    and as many as are just shared."""
+    for kvh in (96, 256):
+        case = (dtype, "nf4", 64, 32, 4 * kvh, kvh, 16, [105, 70, 0], [32, 9, 0])
+        masks = mref.random_trees(case[8], 17)
+        for window, sinks, trees in ((0, 0, masks), (40, 3, masks), (40, 3, None)):
+            for max_len in (1, 1 << 17):
+                print(kvh, window, max_len, flush=True)
+                run(nf4, orc, case, 1700 + kvh, window, sinks, trees, max_len=max_len)
