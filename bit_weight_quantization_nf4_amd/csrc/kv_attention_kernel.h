@@ -455,7 +455,9 @@ __global__ __launch_bounds__((Attn<D, BS, DT, NR, MERGE>::kThreads)) __attribute
   constexpr int P = A::P, NB = A::NB, PB = A::PB, NS = A::NS;
   constexpr int kWaves = A::kWaves, kThreads = A::kThreads;
   constexpr int TW = MERGE ? kWaves : 1;  // waves that share a block's steps
-  __shared__ __attribute__((aligned(16))) char lds[kTableBytes];
+  // (at LDS address 0, where the most aligned variable goes: an LDS read's own offset holds 16 bits,
+  // and past them each lookup has an addition of its own, 64 of 346 VALU instructions of a step)
+  __shared__ __attribute__((aligned(1024))) char lds[kTableBytes];
   // the waves' results where they merge; before, the queries they share
   __shared__ __attribute__((aligned(16))) float merge_buf[A::kMergeFloats];
   __shared__ float wave_m[MERGE ? kWaves : 1][A::kRows];
