@@ -71,16 +71,18 @@
 //   - 32 uneven sequences of one row, window 4096 and 4 sinks (134.6 MB): 34 us, 4.0 TB/s,
 //     and 4 us of joining;
 //   - 512 and 256 fp16 rows in a window of 2048 with 33 sinks (26.2 GFLOP of the
-//     definition's): 145 us, 180 TFLOP/s: 192 workgroups of waves with rows of their own, so a
-//     SIMD has one wave or none, which takes 66 steps of some 4600 cycles;
+//     definition's): 98 us, 267 TFLOP/s (waves with rows of their own: 145; 192 workgroups leave a
+//     SIMD one wave or none);
 //   - trees of 26 rows at 131071 positions, 8 heads of a kv head, FP4, blocks of 32 (27.9 GFLOP):
-//     86 us, 325 TFLOP/s, and 4 of joining. A wave's step is 548 VALU instructions and 48
-//     MFMA; the SIMDs issue VALU in 71 of 100 cycles, MFMA in 22.
-//   - 16 uneven trees of up to 64 rows at up to 6000 positions (36.4 GFLOP): 155 us, 17 of
-//     them joining.
+//     83 us, 336 TFLOP/s, and 4 of joining. A wave's step is 484 VALU instructions and 48
+//     MFMA; the SIMDs issue VALU in 7 of 10 cycles, MFMA in 2.
+//   - 16 uneven trees of up to 64 rows at up to 6000 positions (36.4 GFLOP): 133 us, 275
+//     TFLOP/s. A step is 282 VALU instructions and 48 MFMA; with two waves on a SIMD it takes 2300
+//     to 2600 cycles of each.
 // Tried: waves that share a step's lookups through LDS (17 % fewer cycles a step, but the
 // waves then wait for each other, and no call was faster); 8 waves of 128 registers (110
-// spilled).
+// spilled); values' lookups ahead of the exponentials, and lookups and products dealt out
+// evenly (no difference).
 #pragma once
 
 #include <type_traits>
