@@ -3,7 +3,7 @@
 // With a = max |x| of a block of 32, its scale is 2^(floor(log2 a) - 2): a's exponent bits less 2,
 // so x / scale is exact, lies below 8, and is rounded once, to the nearest of E2M1's values.
 //
-// A workgroup takes 32 rows of 512 columns, a wave 8 of the rows (4 and 1 where that leaves CUs
+// A workgroup takes 32 rows of 512 columns, a wave 8 of the rows (1 where CUs would be left
 // without work); a lane holds 8 neighbouring elements (16 bytes of 16-bit ones), so a block of 32
 // is four lanes, and its largest magnitude two lane exchanges. Codes leave as a dword a lane,
 // scales through LDS as whole 128-byte lines of 32 rows.
@@ -71,59 +71,73 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxMatrix m, int
   constexpr int kRows = kWaves * kWaveRows;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row0 = (int64_t)(blockIdx.x / (unsigned)col_tiles) * kRows;
-  const int32_t col = (int32_t)(blockIdx.x % (unsigned)col_tiles) * kCols + 8 * lane;
+  // Eight elements of a row a lane, 16 bytes of 16-bit values; of fp32 values four and four that
+  // are half a tile on, so that each store's 16 bytes of the lanes are neighbours. (11008 x 4096:
+  // 38 us, with eight neighbouring ones 83.)
+  constexpr int kEach = DT == kFP32 ? 4 : 8, kPieces = 8 / kEach;
+  const int32_t col0 = (int32_t)(blockIdx.x % (unsigned)col_tiles) * kCols + kEach * lane;
   const int here = (int)(m.rows - row0 < kRows ? m.rows - row0 : kRows);
-  if (col >= m.cols) return;
-  uint32_t c[kWaveRows], s[kWaveRows];
+  uint32_t c[kWaveRows][kPieces], s[kWaveRows][kPieces];
 #pragma unroll
   for (int i = 0; i < kWaveRows; ++i) {
     const int r = wave + kWaves * i;
     if (r >= here) continue;
-    c[i] = *reinterpret_cast<const uint32_t *>(m.codes + (row0 + r) * (m.padded / 2) + col / 2);
-    s[i] = m.scales[4 * ((int64_t)(col / kMxStep) * m.rows + row0 + r) + (col / kMxBlock & 3)];
+#pragma unroll
+    for (int h = 0; h < kPieces; ++h) {
+      const int32_t col = col0 + h * (kCols / kPieces);
+      if (col >= m.cols) continue;
+      const uint8_t *at = m.codes + (row0 + r) * (m.padded / 2) + col / 2;
+      if constexpr (kEach == 4) c[i][h] = *reinterpret_cast<const uint16_t *>(at);
+      else c[i][h] = *reinterpret_cast<const uint32_t *>(at);
+      s[i][h] = m.scales[4 * ((int64_t)(col / kMxStep) * m.rows + row0 + r) + (col / kMxBlock & 3)];
+    }
   }
 #pragma unroll
   for (int i = 0; i < kWaveRows; ++i) {
     const int r = wave + kWaves * i;
     if (r >= here) continue;
-    // elements in order from the low nibble on
-    const uint32_t v = (c[i] & 0x0f0f0f0fu) << 4 | (c[i] >> 4 & 0x0f0f0f0fu);
-    const float scale = __uint_as_float(s[i] << 23);
-    const bool nan = s[i] == 255;
-    f32x2 f[4];
-    f[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, 0);
-    f[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, 1);
-    f[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, 2);
-    f[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, 3);
-    if (nan) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = f32x2{__builtin_nanf(""), __builtin_nanf("")};
-    }
-    const int64_t at = (row0 + r) * ld + col;
-    if constexpr (DT == kFP32) {
-      float *p = static_cast<float *>(out) + at;
-      if (col + 8 <= m.cols) {
-        auto *q = reinterpret_cast<mx_any_u32x4 *>(p);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          put<ONCE>(mx_u32x4{__float_as_uint(f[2 * j].x), __float_as_uint(f[2 * j].y),
-                             __float_as_uint(f[2 * j + 1].x), __float_as_uint(f[2 * j + 1].y)}, q + j);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col + j < m.cols) p[j] = f[j / 2][j % 2];
+    for (int h = 0; h < kPieces; ++h) {
+      const int32_t col = col0 + h * (kCols / kPieces);
+      if (col >= m.cols) continue;
+      // elements in order from the low nibble on
+      const uint32_t v = (c[i][h] & 0x0f0f0f0fu) << 4 | (c[i][h] >> 4 & 0x0f0f0f0fu);
+      const float scale = __uint_as_float(s[i][h] << 23);
+      f32x2 f[4];
+      f[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, 0);
+      f[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, 1);
+      if constexpr (kEach == 8) {
+        f[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, 2);
+        f[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, 3);
       }
-    } else {
-      uint16_t *p = static_cast<uint16_t *>(out) + at;
-      uint32_t w[4];
+      if (s[i][h] == 255) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack2<DT>(f[j].x, f[j].y);
-      if (col + 8 <= m.cols) {
-        put<ONCE>(mx_u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<mx_any_u32x4 *>(p));
+        for (int j = 0; j < kEach / 2; ++j) f[j] = f32x2{__builtin_nanf(""), __builtin_nanf("")};
+      }
+      const int64_t at = (row0 + r) * ld + col;
+      if constexpr (DT == kFP32) {
+        float *p = static_cast<float *>(out) + at;
+        if (col + 4 <= m.cols) {
+          put<ONCE>(mx_u32x4{__float_as_uint(f[0].x), __float_as_uint(f[0].y),
+                             __float_as_uint(f[1].x), __float_as_uint(f[1].y)},
+                    reinterpret_cast<mx_any_u32x4 *>(p));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col + j < m.cols) p[j] = f[j / 2][j % 2];
+        }
       } else {
+        uint16_t *p = static_cast<uint16_t *>(out) + at;
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col + j < m.cols) p[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+        for (int j = 0; j < 4; ++j) w[j] = pack2<DT>(f[j].x, f[j].y);
+        if (col + 8 <= m.cols) {
+          put<ONCE>(mx_u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<mx_any_u32x4 *>(p));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col + j < m.cols) p[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+        }
       }
     }
   }
@@ -134,8 +148,8 @@ int64_t tiles_of(int64_t rows, int64_t cols, int tile_rows) {
   return (rows + tile_rows - 1) / tile_rows * col_tiles_of(cols);
 }
 
-// Rows of a wave: 8, or 1 where two workgroups a CU of 32 rows are not reached. (16 x 11008: 4.4 us
-// and 2.2.) From kOnceBytes of values on these go past the caches, which the codes then have to
+// Rows of a wave: 8, or 1 where four workgroups a CU of 32 rows are not reached. (Quantized: 16 x
+// 11008 4.4 us and 2.2, 2048 x 4096 4.9 and 4.4, 1024 x 14336 7.1 and 6.7.) From kOnceBytes of values on these go past the caches, which the codes then have to
 // themselves. (In bf16, quantized and restored, other inputs each time: 11008 x 4096 42.5 us, 49.5
 // through the caches, 8192 x 4096 33, 39; 2048 x 4096 quantized in 7.0 and 6.6.)
 constexpr int64_t kOnceBytes = (int64_t)64 << 20;
@@ -143,7 +157,7 @@ constexpr int64_t kOnceBytes = (int64_t)64 << 20;
 template <typename F>
 void by_size(int64_t rows, int64_t cols, int64_t bytes_each, F &&run) {
   using std::integral_constant;
-  if (tiles_of(rows, cols, 8 * kWaves) < 2 * device_cu_count())
+  if (tiles_of(rows, cols, 8 * kWaves) < 4 * device_cu_count())
     run(integral_constant<int, 1>{}, std::false_type{});
   else if (rows * cols * bytes_each < kOnceBytes)
     run(integral_constant<int, 8>{}, std::false_type{});
@@ -156,9 +170,10 @@ void quantize_as(const void *x, int64_t rows, int32_t cols, int64_t ld, uint8_t 
                  uint8_t *scales, hipStream_t stream) {
   by_size(rows, cols, DT == kFP32 ? 4 : 2, [&](auto wave_rows, auto once) {
     constexpr int R = decltype(wave_rows)::value;
-    hipLaunchKernelGGL((mx_quantize_kernel<DT, R, decltype(once)::value>), dim3((unsigned)tiles_of(rows, cols, R * kWaves)),
-                       dim3(kThreads), 0, stream, x, rows, cols, (int32_t)mx_padded(cols), ld,
-                       (int32_t)col_tiles_of(cols), codes, scales);
+    hipLaunchKernelGGL((mx_quantize_kernel<DT, R, decltype(once)::value>),
+                       dim3((unsigned)tiles_of(rows, cols, R * kWaves)), dim3(kThreads), 0, stream,
+                       x, rows, cols, (int32_t)mx_padded(cols), ld, (int32_t)col_tiles_of(cols),
+                       codes, scales);
   });
 }
 
