@@ -55,7 +55,7 @@ struct Plan {
 
 Plan plan_of(int64_t M, int64_t N, int64_t K, bool raw) {
   Plan p{Plan::kGemm, 0, 0, 0};
-  if (M <= mx_gemv_max_rows()) p.kind = Plan::kGemv;
+  if (mx_gemv_takes(M, N, K)) p.kind = Plan::kGemv;
   if (raw && p.kind == Plan::kGemv && mx_gemv_quantizes(M, K)) p.kind = Plan::kGemvQuantizing;
   if (raw && p.kind != Plan::kGemvQuantizing) {
     const int64_t padded = mx_padded(K);

@@ -275,7 +275,6 @@ void mx_gemm_kernel(GemmArgs a) {
   Out *out = static_cast<Out *>(a.y) + split * a.split_stride;
   uint8_t *mine = codes[0] + wave * (32 * kPitch);
   const int f_first = 32 * FT * wf;  // of the tile
-  const bool even = (a.ldy * sizeof(Out)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
     __builtin_amdgcn_sched_barrier(0);  // (rows ahead of their turn would spill)
@@ -302,8 +301,8 @@ void mx_gemm_kernel(GemmArgs a) {
       const int m = TT * (32 * wt + row) + j;
       if (m >= m_rows) continue;
       Out *dst = out + (m0 + m) * a.ldy + f0 + f;
-      if (even && f + kEach <= f_rows) {
-        *reinterpret_cast<uint4 *>(dst) = piece;
+      if (f + kEach <= f_rows) {  // (of any alignment: the memory instructions take it)
+        *reinterpret_cast<mx_any_u32x4 *>(dst) = mx_u32x4{piece.x, piece.y, piece.z, piece.w};
       } else {
         const uint32_t w[4] = {piece.x, piece.y, piece.z, piece.w};
 #pragma unroll

@@ -1,8 +1,8 @@
-// mx_gemv.hip -- products of few rows with a microscaled 4-bit weight.
+// mx_gemv.hip -- products of few rows, and small ones, with a microscaled 4-bit weight.
 //
 // y[m][f] = sum_k x[m][k] w[f][k], both in 4 bits, 16x16x128 matrix-core steps with the weight
 // as the first operand: a lane's 16 bytes of codes go to the instruction as they come from
-// memory. A workgroup has 16 FT features and all of K; its waves take the 128-wide steps in
+// memory. A workgroup has 16 FT features, 16 TT rows of x and all of K; its waves take the 128-wide steps in
 // turn, batches of kBatch steps' loads in flight at once, and add their sums up in wave order.
 // With few rows of x the workgroup quantizes them itself into LDS while the weight's first
 // batch is on its way; else x is quantized before and its codes are read beside the weight's.
@@ -83,13 +83,16 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemv_kernel(GemvArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int64_t f0 = (int64_t)blockIdx.x * (16 * FT);
+  const int m0 = RAW < 0 ? (int)blockIdx.y * (16 * TT) : 0;
+  const int m_rows = a.M - m0 < 16 * TT ? a.M - m0 : 16 * TT;
   const int64_t half = a.w.padded / 2;
   const int steps = a.w.padded / kMxStep;
 
   // Loads go by buffers: rows past the last one, and steps, read zeros and cost nothing.
   const int f_rows = uniform((int)(a.w.rows - f0 < 16 * FT ? a.w.rows - f0 : 16 * FT));
   const __amdgpu_buffer_rsrc_t wr = buffer_of(a.w.codes + f0 * half, (uint32_t)f_rows * (uint32_t)half);
-  const __amdgpu_buffer_rsrc_t xr = buffer_of(a.x.codes, RAW < 0 ? (uint32_t)a.M * (uint32_t)half : 0u);
+  const __amdgpu_buffer_rsrc_t xr = RAW < 0
+      ? buffer_of(a.x.codes + m0 * half, (uint32_t)m_rows * (uint32_t)half) : buffer_of(nullptr, 0);
   constexpr int XB = RAW < 0 ? TT : 1;
   // Scales go by four steps a load, one for each lane of the four that share a row: a byte a lane
   // and step cost 1 us of 9 at 16 rows.
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemv_kernel(GemvArgs a) {
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
           b.xc[u][j] = codes_of(xr, 16 * j + n);
-          if (u % 4 == 0) b.xs[u / 4][j] = load_scales(a.x, 16 * j + n, t0, u / 4);
+          if (u % 4 == 0) b.xs[u / 4][j] = load_scales(a.x, m0 + 16 * j + n, t0, u / 4);
         }
       }
     }
@@ -213,7 +216,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemv_kernel(GemvArgs a) {
     const int ij = at >> 8, f = at & 15, m = at >> 4 & 15;
     const int i = ij / TT, j = ij - i * TT;
     const int64_t feature = f0 + 16 * i + f;
-    const int row = 16 * j + m;
+    const int row = m0 + 16 * j + m;
     if (row >= a.M || feature >= a.w.rows) continue;
     float v = 0.0f;
 #pragma unroll
@@ -227,8 +230,9 @@ constexpr int kWaves = 8;
 
 template <int RAW, int OUT, int TT, int FT, int kBatch, int kEights = 1>
 hipError_t launch(const GemvArgs &a, hipStream_t stream) {
-  const unsigned grid = (unsigned)((a.w.rows + 16 * FT - 1) / (16 * FT));
-  hipLaunchKernelGGL((mx_gemv_kernel<RAW, OUT, TT, FT, kWaves, kBatch, kEights>), dim3(grid),
+  const dim3 grid((unsigned)((a.w.rows + 16 * FT - 1) / (16 * FT)),
+                  (unsigned)(((int64_t)a.M + 16 * TT - 1) / (16 * TT)));
+  hipLaunchKernelGGL((mx_gemv_kernel<RAW, OUT, TT, FT, kWaves, kBatch, kEights>), grid,
                      dim3(64 * kWaves), 0, stream, a);
   return hipGetLastError();
 }
@@ -255,12 +259,17 @@ hipError_t launch_raw(const GemvArgs &a, int out_dtype, hipStream_t stream) {
   return launch_one_tile<RAW, kBF16>(a, stream);
 }
 
+// Tiles of 16 features and 16 TT rows.
+int64_t tiles_of(int64_t N, int64_t M, int TT) {
+  return (N + 15) / 16 * ((M + 16 * TT - 1) / (16 * TT));
+}
+
 // More rows of x are read again by every workgroup: these take as many features as leave one for
 // each CU. (64 rows, 11008 x 4096: 17.1 us with 16 features, 16.6 with 32, 11.9 with 64; 4096 x
 // 4096: 7.5, 8.9, 11.7. 32 rows: 11.1, 10.3, 9.0; 5.5, 6.5, 8.8.)
 template <int OUT, int TT>
 hipError_t launch_features(const GemvArgs &a, hipStream_t stream) {
-  const int64_t tiles = (a.w.rows + 15) / 16, cus = device_cu_count();
+  const int64_t tiles = tiles_of(a.w.rows, a.M, TT), cus = device_cu_count();
   if (tiles <= cus) return launch<-1, OUT, TT, 1, 4>(a, stream);
   if (tiles <= 2 * cus) return launch<-1, OUT, TT, 2, 4>(a, stream);
   return launch<-1, OUT, TT, 4, 4>(a, stream);
@@ -285,7 +294,15 @@ GemvArgs args_of(const MxProduct &p, int M) {
 
 }  // namespace
 
-int mx_gemv_max_rows() { return 64; }
+// Products of more rows than 64 come here where the device has a CU for each two of their tiles and
+// rows are not long. (Here and in mx_gemm.hip's kernel, us: 128 x 1024 x 1024 4.2 and 5.8, 256 x
+// 1024 x 4096 7.2 and 10.9, 512 x 1024 x 8192 14.6 and 16.3, 128 x 4096 x 4096 9.0 and 13.6; longer
+// rows, 256 x 1024 x 14336, 19.8 and 16.3; more tiles, 256 x 4096 x 1024, 7.2 and 6.1.)
+constexpr int64_t kGemvMaxK = 8192;
+
+bool mx_gemv_takes(int64_t M, int64_t N, int64_t K) {
+  return M <= 64 || (tiles_of(N, M, 4) <= 2 * device_cu_count() && K <= kGemvMaxK);
+}
 
 // Every workgroup quantizes all of x, which has to cost less than a launch before: about 2.2 us.
 // (One weight after another: 4 rows, 11008 x 4096 8.4 us and 9.0, 8 rows, 4096 x 4096 5.7 and 5.7,

@@ -37,9 +37,9 @@ struct MxProduct {
   int64_t ldy;
 };
 
-// Products of few rows (mx_gemv.hip). Up to mx_gemv_max_rows() rows of x; launch_mx_gemv_quantizing
+// Products of few rows (mx_gemv.hip), where mx_gemv_takes() says so; launch_mx_gemv_quantizing
 // takes x as it is, where mx_gemv_quantizes() says so.
-int mx_gemv_max_rows();
+bool mx_gemv_takes(int64_t M, int64_t N, int64_t K);
 bool mx_gemv_quantizes(int64_t M, int64_t K);
 hipError_t launch_mx_gemv(const MxMatrix &x, const MxProduct &p, hipStream_t stream);
 hipError_t launch_mx_gemv_quantizing(const void *x, int x_dtype, int64_t ldx, int M,

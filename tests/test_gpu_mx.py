@@ -370,3 +370,36 @@ def test_calls_at_once_and_graphs_that_share_memory(nf4):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want))
             assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(65, 8300, 129), (130, 5003, 300), (333, 2801, 1003), (700, 1537, 640),
+                                   (1030, 777, 385), (128, 1500, 8321), (300, 260, 12000)])
+def test_tiles_of_many_rows(nf4, m, n, k, dtype):
+    """Products past the small ones' kernel: rows, columns and steps that end inside a tile or a
+    stage, ranges of K; outputs at any distance and alignment, which keep what is beside them."""
+    x = nf4.mx_quantize(rows_of(m, k, torch.float32, 3).cuda())
+    w = weight_of(nf4, n, k, 4)
+    bias = rows_of(1, n, dtype, 5)[0]
+    room = torch.full((m + 2, n + 9), 9.0, dtype=dtype, device="cuda")
+    y = nf4.mx_linear(x, w, bias.cuda(), out=room[1:-1, 5:n + 5])
+    x64, w64 = dense(x), dense(w)
+    check_product(y, x64, w64, bias, k, (m, n, k))
+    assert torch.equal(nf4.mx_linear(x, w, bias.cuda(), out_dtype=dtype), y)
+    room[1:-1, 5:n + 5] = 9.0
+    assert bool((room == 9.0).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(65, 20, 300), (333, 700, 640), (2000, 16, 129), (500, 17, 4096),
+                                   (129, 4096, 256)])
+def test_small_products_of_many_rows(nf4, m, n, k):
+    """Blocks of 64 rows in the kernel of few rows, each the bits of its rows alone."""
+    x = nf4.mx_quantize(rows_of(m, k, torch.float32, 6).cuda())
+    w = weight_of(nf4, n, k, 7)
+    y = nf4.mx_linear(x, w, out_dtype=torch.float32)
+    check_product(y, dense(x), dense(w), None, k, (m, n, k))
+    raw = rows_of(m, k, torch.float32, 6).cuda()
+    assert torch.equal(nf4.mx_linear(raw, w), y)
+    for lo in range(0, m, 64):
+        part = nf4.mx_linear(nf4.mx_quantize(raw[lo:lo + 64]), w, out_dtype=torch.float32)
+        assert torch.equal(part, y[lo:lo + 64])
