@@ -19,7 +19,7 @@
 // What bounds it, on one MI355X: 8192 cubed takes 250 to 280 us, 3.9 to 4.4 PFLOP/s; without its
 // loads and stores 209 us, 5.3 PFLOP/s, where a single workgroup's steps take half the time that
 // they do with all CUs at work: the matrix cores' clock under that load. 2048 x 14336 x 4096, 448
-// tiles in two rounds of 256: 66 to 75 us, 3.2 to 3.7 PFLOP/s; the second round leaves a quarter of
+// tiles in two rounds of 256: 64 to 75 us, 3.2 to 3.7 PFLOP/s; the second round leaves a quarter of
 // the CUs idle, and each round's results, 33 MB, are written while nothing is multiplied.
 #include <type_traits>
 
