@@ -403,3 +403,21 @@ def test_small_products_of_many_rows(nf4, m, n, k):
     for lo in range(0, m, 64):
         part = nf4.mx_linear(nf4.mx_quantize(raw[lo:lo + 64]), w, out_dtype=torch.float32)
         assert torch.equal(part, y[lo:lo + 64])
+
+
+@pytest.mark.parametrize("m,n", [(130, 4200), (700, 1100), (260, 9000)])
+@pytest.mark.parametrize("k", [300, 640, 1003])
+def test_what_lies_behind_a_large_matrix_has_no_part(nf4, m, n, k):
+    """The same of products past the small ones' kernel, of a last stage of one step and of two."""
+    x, w = nf4.mx_quantize(rows_of(m, k, torch.float32, 1).cuda()), weight_of(nf4, n, k, 2)
+    want = nf4.mx_linear(x, w)
+
+    def surrounded(t):
+        out = []
+        for a, fill in ((t.codes, 0x77), (t.scales, 255)):
+            room = torch.full((a.numel() + 4096,), fill, dtype=torch.uint8, device="cuda")
+            out.append(room[:a.numel()].view(a.shape).copy_(a))
+        return nf4.MXTensor(*out, t.shape)
+
+    assert torch.equal(nf4.mx_linear(surrounded(x), surrounded(w)), want)
+    check_product(want, dense(x), dense(w), None, k, (m, n, k))
