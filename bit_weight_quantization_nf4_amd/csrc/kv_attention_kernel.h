@@ -252,7 +252,13 @@ __device__ __forceinline__ Block block_of(KernelArgsOf<MASK> &args, const Sequen
     b.lo = seen_begin(a, end0);
     b.all_hi = within(a, end0);
     b.all_lo = seen_begin(a, end1);
-    if (b.hi <= b.lo) b.lo = b.hi = 0;
+    if (b.hi <= b.lo) {
+      // the window begins behind the table's positions, of which the first ones stay in sight
+      int first = 0;
+      if constexpr (MASK) first = b.hi > 0 ? (args.sinks < b.hi ? args.sinks : b.hi) : 0;
+      b.lo = 0;
+      b.hi = first;
+    }
     b.lo &= ~(kStep - 1);
     if constexpr (MASK) {
       const int sinks = args.sinks < b.hi ? args.sinks : b.hi;
