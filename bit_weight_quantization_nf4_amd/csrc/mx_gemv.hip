@@ -30,12 +30,14 @@ struct GemvArgs {
   int64_t ldx;
 };
 
-// Elements of x that a workgroup quantizes itself at most, and LDS for them.
-constexpr int kRawElements = 20480, kRawBytes = kRawElements / 32 * 17 + 16 * 16;
+// Elements of x that a workgroup quantizes itself at most, and LDS for them (of a row, a gap of 16
+// bytes and up to 12 of rounding).
+constexpr int kRawElements = 20480, kRawBytes = kRawElements / 32 * 17 + 16 * (16 + 12);
 
-// bytes of a quantized row in LDS: its codes, padded against bank conflicts, and scales
+// bytes of a quantized row in LDS: its codes, padded against bank conflicts, and scales, up to a
+// multiple of 16, for rows are read in pieces of 16
 __host__ __device__ constexpr int64_t raw_row_bytes(int64_t padded) {
-  return padded / 2 + 16 + padded / kMxBlock;
+  return (padded / 2 + 16 + padded / kMxBlock + 15) / 16 * 16;
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
