@@ -430,7 +430,7 @@ int64_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 bool mx_gemm_fits(int64_t M, int64_t N) {
   // (products with several ranges are far smaller)
-  return tiles_of(M, N, false) * 256 <= 0xffffffffll;
+  return tiles_of(M, N, false) * 256 <= 0xffffffffll && tiles_of(M, N, true) * 512 <= 0xffffffffll;
 }
 
 hipError_t launch_mx_gemm(const MxMatrix &x, const MxProduct &p, void *workspace,

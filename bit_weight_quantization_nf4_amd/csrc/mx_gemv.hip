@@ -269,11 +269,17 @@ int64_t tiles_of(int64_t N, int64_t M, int TT) {
 // More rows of x are read again by every workgroup: these take as many features as leave one for
 // each CU. (64 rows, 11008 x 4096: 17.1 us with 16 features, 16.6 with 32, 11.9 with 64; 4096 x
 // 4096: 7.5, 8.9, 11.7. 32 rows: 11.1, 10.3, 9.0; 5.5, 6.5, 8.8.)
+int features_of(int64_t N, int64_t M) {  // 16-feature tiles of a workgroup
+  if (M <= 16) return 1;
+  const int64_t tiles = tiles_of(N, M, M <= 32 ? 2 : 4), cus = device_cu_count();
+  return tiles <= cus ? 1 : tiles <= 2 * cus ? 2 : 4;
+}
+
 template <int OUT, int TT>
 hipError_t launch_features(const GemvArgs &a, hipStream_t stream) {
-  const int64_t tiles = tiles_of(a.w.rows, a.M, TT), cus = device_cu_count();
-  if (tiles <= cus) return launch<-1, OUT, TT, 1, 4>(a, stream);
-  if (tiles <= 2 * cus) return launch<-1, OUT, TT, 2, 4>(a, stream);
+  const int features = features_of(a.w.rows, a.M);
+  if (features == 1) return launch<-1, OUT, TT, 1, 4>(a, stream);
+  if (features == 2) return launch<-1, OUT, TT, 2, 4>(a, stream);
   return launch<-1, OUT, TT, 4, 4>(a, stream);
 }
 
@@ -303,6 +309,9 @@ GemvArgs args_of(const MxProduct &p, int M) {
 constexpr int64_t kGemvMaxK = 8192;
 
 bool mx_gemv_takes(int64_t M, int64_t N, int64_t K) {
+  // (what passes the device's grid has few enough tiles of the other kernel)
+  const int64_t wide = 16 * features_of(N, M);
+  if ((N + wide - 1) / wide * (64 * kWaves) > 0xffffffffll) return false;
   return M <= 64 || (tiles_of(N, M, 4) <= 2 * device_cu_count() && K <= kGemvMaxK);
 }
 
