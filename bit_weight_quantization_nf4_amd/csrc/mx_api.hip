@@ -106,11 +106,20 @@ nf4_status run_product(const MxMatrix *x, const void *raw, int32_t x_dtype, int6
   if (st != NF4_OK) return st;
   const Plan plan = plan_of(M, N, K, x == nullptr);
   if (workspace_size < plan.codes + plan.scales + plan.product) return NF4_ERR_SCRATCH;
-  if (log_on())
-    log_msg("mx product M=%lld N=%lld K=%lld: %s%s", (long long)M, (long long)N, (long long)K,
-            plan.kind == Plan::kGemm ? "mx_gemm_kernel" : "mx_gemv_kernel",
-            x != nullptr ? ""
-            : plan.kind == Plan::kGemvQuantizing ? ", x quantized in it" : " after mx_quantize_kernel");
+  if (log_on()) {
+    const char *how = x != nullptr ? ""
+                      : plan.kind == Plan::kGemvQuantizing ? ", x quantized in it"
+                                                           : " after mx_quantize_kernel";
+    if (plan.kind == Plan::kGemm) {
+      const MxGemmShape shape = mx_gemm_shape(M, N, K);
+      log_msg("mx product M=%lld N=%lld K=%lld: mx_gemm_kernel%s, tiles of %d, %d range(s) of %d steps",
+              (long long)M, (long long)N, (long long)K, how, shape.tile, shape.splits,
+              shape.split_steps);
+    } else {
+      log_msg("mx product M=%lld N=%lld K=%lld: mx_gemv_kernel%s", (long long)M, (long long)N,
+              (long long)K, how);
+    }
+  }
   if (plan.kind == Plan::kGemvQuantizing)
     return from_hip(launch_mx_gemv_quantizing(raw, x_dtype, ldx, (int)M, p, stream));
   MxMatrix own;

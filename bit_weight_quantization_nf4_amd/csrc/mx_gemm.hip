@@ -433,6 +433,11 @@ bool mx_gemm_fits(int64_t M, int64_t N) {
   return tiles_of(M, N, false) * 256 <= 0xffffffffll && tiles_of(M, N, true) * 512 <= 0xffffffffll;
 }
 
+MxGemmShape mx_gemm_shape(int64_t M, int64_t N, int64_t K) {
+  const Plan p = plan_of(M, N, K);
+  return MxGemmShape{p.large ? 256 : 128, p.splits, p.split_steps};
+}
+
 hipError_t launch_mx_gemm(const MxMatrix &x, const MxProduct &p, void *workspace,
                           hipStream_t stream) {
   const Plan plan = plan_of(x.rows, p.w.rows, p.w.cols);

@@ -48,6 +48,11 @@ hipError_t launch_mx_gemv_quantizing(const void *x, int x_dtype, int64_t ldx, in
 // Products of many rows (mx_gemm.hip).
 int64_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 bool mx_gemm_fits(int64_t M, int64_t N);
+// Side of its tiles, ranges of K and their 128-wide steps.
+struct MxGemmShape {
+  int tile, splits, split_steps;
+};
+MxGemmShape mx_gemm_shape(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_gemm(const MxMatrix &x, const MxProduct &p, void *workspace,
                           hipStream_t stream);
 
