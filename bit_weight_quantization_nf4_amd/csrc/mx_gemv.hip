@@ -2,8 +2,9 @@
 //
 // y[m][f] = sum_k x[m][k] w[f][k], both in 4 bits, 16x16x128 matrix-core steps with the weight
 // as the first operand: a lane's 16 bytes of codes go to the instruction as they come from
-// memory. A workgroup has 16 FT features, 16 TT rows of x and all of K; its waves take the 128-wide steps in
-// turn, batches of kBatch steps' loads in flight at once, and add their sums up in wave order.
+// memory. A workgroup has 16 FT features, 16 TT rows of x and all of K; its waves take the
+// 128-wide steps in turn, batches of kBatch steps' loads in flight at once, and add their sums up
+// in wave order.
 // With few rows of x the workgroup quantizes them itself into LDS while the weight's first
 // batch is on its way; else x is quantized before and its codes are read beside the weight's.
 //

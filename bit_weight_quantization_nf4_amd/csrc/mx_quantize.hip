@@ -3,14 +3,14 @@
 // With a = max |x| of a block of 32, its scale is 2^(floor(log2 a) - 2): a's exponent bits less 2,
 // so x / scale is exact, lies below 8, and is rounded once, to the nearest of E2M1's values.
 //
-// A workgroup takes 32 rows of 512 columns, a wave 8 of the rows (1 where CUs would be left
-// without work); a lane holds 8 neighbouring elements (16 bytes of 16-bit ones), so a block of 32
+// A workgroup takes 32 rows of 512 columns, a wave 8 of the rows (1 where that leaves fewer than four
+// workgroups a CU); a lane holds 8 neighbouring elements (16 bytes of 16-bit ones), so a block of 32
 // is four lanes, and its largest magnitude two lane exchanges. Codes leave as a dword a lane,
 // scales through LDS as whole 128-byte lines of 32 rows.
 //
 // What bounds it, on one MI355X: HBM. 11008 x 4096 in bf16 (114 MB): quantized in 22 to 23 us, 5.0
-// TB/s, restored in 17, 6.7 TB/s (four fifths of it writes); a copy moves 5.2. One row of 4096: 2.2
-// us each, a launch.
+// TB/s, restored in 17, 6.7 TB/s (four fifths of it writes); a copy moves 5.2. In fp32 (203 MB): 44 us,
+// 4.6 TB/s, and 35, 5.9 TB/s. One row of 4096: 2.2 us each, a launch.
 #include <type_traits>
 
 #include "mx_internal.h"
@@ -149,15 +149,17 @@ int64_t tiles_of(int64_t rows, int64_t cols, int tile_rows) {
 }
 
 // Rows of a wave: 8, or 1 where four workgroups a CU of 32 rows are not reached. (Quantized: 16 x
-// 11008 4.4 us and 2.2, 2048 x 4096 4.9 and 4.4, 1024 x 14336 7.1 and 6.7.) From kOnceBytes of values on these go past the caches, which the codes then have to
-// themselves. (In bf16, quantized and restored, other inputs each time: 11008 x 4096 42.5 us, 49.5
-// through the caches, 8192 x 4096 33, 39; 2048 x 4096 quantized in 7.0 and 6.6.)
+// 11008 4.4 us and 2.2, 2048 x 4096 4.9 and 4.4, 1024 x 14336 7.1 and 6.7.) From kOnceBytes of values
+// on these go past the caches, which the codes then have to themselves. (In bf16, quantized and
+// restored, other inputs each time: 11008 x 4096 42.5 us, 49.5 through the caches, 8192 x 4096 33,
+// 39; 2048 x 4096 quantized in 7.0 and 6.6.)
+constexpr int kWideFrom = 4;  // workgroups a CU
 constexpr int64_t kOnceBytes = (int64_t)64 << 20;
 
 template <typename F>
 void by_size(int64_t rows, int64_t cols, int64_t bytes_each, F &&run) {
   using std::integral_constant;
-  if (tiles_of(rows, cols, 8 * kWaves) < 4 * device_cu_count())
+  if (tiles_of(rows, cols, 8 * kWaves) < kWideFrom * device_cu_count())
     run(integral_constant<int, 1>{}, std::false_type{});
   else if (rows * cols * bytes_each < kOnceBytes)
     run(integral_constant<int, 8>{}, std::false_type{});
@@ -189,7 +191,7 @@ void dequantize_as(const MxMatrix &m, void *out, int64_t ld, hipStream_t stream)
 
 }  // namespace
 
-// (where waves have one row, there are fewer workgroups than twice eight times the CUs)
+// (where waves have one row, there are fewer than 8 kWideFrom workgroups a CU)
 bool mx_elementwise_fits(int64_t rows, int64_t cols) {
   return tiles_of(rows, cols, 8 * kWaves) * kThreads <= 0xffffffffll;
 }

@@ -24,7 +24,8 @@ int64_t nf4_kv_attention_masked_workspace_bytes(int32_t batch, int32_t max_rows,
  *
  * sinks: with window > 0, row i of the n_b rows of sequence b, whose place is P = kv_lens[b] -
  * n_b + i, sees the positions p <= P of which p > P - window or p < sinks. (Without a window
- * all p <= P, whatever sinks is.)
+ * all p <= P, whatever sinks is.) Where the window begins behind the table's last column the first
+ * positions are still in sight.
  *
  * tree: NULL, or the rows that each row sees of its sequence's in the call: row t of the row
  * tensors has tree_words words of 32 bits at tree + t tree_stride (device memory, 4-byte
